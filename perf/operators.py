@@ -176,7 +176,6 @@ def prepare(case, seed):
                 x = normal(t, heads, d)
                 s[name] = (x * gain if name == "q" else x).to(torch.bfloat16).view(torch.int16)
         s["lse"] = torch.empty((tq, H), dtype=torch.float32, device="cuda")
-        seqs = case["seqs"]
     else:
         page, fp8 = case["page"], case["fp8"]
         if case["op"] == "decode":
@@ -202,11 +201,10 @@ def prepare(case, seed):
             s[name] = ((x * 40.0).clamp_(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8) if fp8
                        else x.to(torch.bfloat16).view(torch.int16))
             del x
-        seqs = case["seqs"]
     if own:
         import quantized_grouped_gemm_router_gb300 as moe
         s["dims"] = moe.AttnDims(H, K, d)
-        s["ws"] = moe.attn_workspace(s["dims"], seqs)
+        s["ws"] = moe.attn_workspace(s["dims"])
         if case["op"] != "prefill":
             s["cache"] = moe.KvCache(s["dims"], s["k"], s["v"], s["k_scale"], s["v_scale"])
     return s
