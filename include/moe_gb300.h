@@ -78,10 +78,13 @@ enum moe_status {
   MOE_ERR_CUDA = 5,               /* a CUDA launch or copy failed                           */
   MOE_ERR_NONFINITE = 6,          /* device: a router logit was NaN or infinite             */
   MOE_ERR_DEVICE_TIMEOUT = 7,     /* device: a bounded wait inside a kernel gave up         */
-  MOE_ERR_OUT_OF_RANGE = 8        /* device: a value outside what the fp16 operands of the expert
+  MOE_ERR_OUT_OF_RANGE = 8,       /* device: a value outside what the fp16 operands of the expert
                                      GEMMs hold: an activation (x or a SwiGLU output) with
                                      |v| > 65504, or (prefill) a nonzero scale or bias below
                                      2^-14 in magnitude or with 15*|scale| + |bias| > 65504  */
+  MOE_ERR_BAD_INDEX = 9           /* device (attention calls): offsets that do not ascend from 0 to
+                                     the row count, a length or position outside the page table,
+                                     or a page number outside the cache                       */
 };
 
 /* Layer dimensions. `group` is the quantization group along the input dimension (64). */
@@ -388,6 +391,107 @@ MOE_API int moe_decode_diag(const moe_layer* layer, const uint16_t* x, uint16_t*
  * CUDA synchronously.
  */
 MOE_API int moe_selftest_wait_timeout(void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Attention beside the MoE layer: packed prompts, a paged key-value cache, and one new token
+ * per sequence over that cache. The pages describe these layers next to the MoE layer (page
+ * "Perplexity's Lily beats MLX-LM ...", sections "Why Qwen3.6-35B-A3B is a weird workload" and
+ * "Decode: minimize bytes per token": grouped heads, cache reads that coalesce, contexts to
+ * 128K tokens).
+ *
+ * For one query row q (head h) and the keys it sees (head h / (n_q_heads / n_kv_heads)):
+ *   s_j = scale * q . k_j,   o = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)
+ * A row that sees no key gives o = 0 and lse = -inf. What a row does not see never reaches its
+ * outputs, whatever its value (NaN and infinities included).
+ *
+ * The conventions at the top of this file hold, with these additions:
+ *   - Activations are bf16. Scores, softmax statistics and the accumulated output are fp32. The
+ *     softmax weights are rounded once, to the other operand's 16-bit type (bf16; fp16 when the
+ *     cache is e4m3), for the product with v; o is rounded once to bf16. lse is natural-log, fp32.
+ *   - Supported: head_dim 64, 128 or 256; n_kv_heads divides n_q_heads; at most 64 query heads per
+ *     key-value head and 1024 query heads; 1 <= n_seqs <= 4096; page_size 1..65536
+ *     (MOE_ERR_UNSUPPORTED_SHAPE otherwise).
+ *   - int32 and float arrays need 4-byte alignment; bf16 and cache pointers 16 bytes, `ws` 128.
+ *   - Lengths, offsets and page numbers are device data. A kernel never follows a bad one out of
+ *     the buffers it was given: it clamps it or skips it and raises MOE_ERR_BAD_INDEX in `ws`, and
+ *     the rows concerned are undefined.
+ *   - `ws`: moe_attn_workspace_bytes(dims) bytes, zero-filled once before the first call; the rules
+ *     of moe_workspace_bytes hold (one workspace per stream of calls that do not overlap). The
+ *     workspaces of the MoE calls and of the attention calls are separate buffers.
+ */
+typedef struct moe_attn_dims {
+  int32_t n_q_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+} moe_attn_dims;
+
+/* bf16 rows [tokens, heads, head_dim] inside any buffer (a fused q|k|v projection, say): element
+ * (t, h, i) at p[t * token_stride + h * head_stride + i]. Strides in elements, multiples of 8, at
+ * least head_dim and below 2^38 (MOE_ERR_INVALID_ARG otherwise). */
+typedef struct moe_heads_view {
+  const uint16_t* p;
+  int64_t token_stride;
+  int64_t head_stride;
+} moe_heads_view;
+
+MOE_API size_t moe_attn_workspace_bytes(const moe_attn_dims* dims);
+
+/*
+ * Attention over whole prompts, packed: sequence b has the query rows cu_q[b] .. cu_q[b+1] - 1 of q
+ * and the key and value rows cu_k[b] .. cu_k[b+1] - 1 of k and v (device int32[n_seqs + 1], from 0
+ * to total_q and total_k; empty sequences are fine). With Lq and Lk rows, query i sees key j when
+ * j <= i + Lk - Lq (causal != 0: the last query sees every key, as when a prompt continues on
+ * earlier context) or always (causal == 0).
+ * o: bf16 [total_q, n_q_heads, head_dim], contiguous, not overlapping the inputs. lse: fp32
+ * [total_q, n_q_heads] or NULL. scale > 0 and finite.
+ */
+MOE_API int moe_attn_prefill(const moe_attn_dims* dims, moe_heads_view q, moe_heads_view k, moe_heads_view v,
+                             const int32_t* cu_q, const int32_t* cu_k, int32_t n_seqs, int32_t total_q,
+                             int32_t total_k, float scale, int32_t causal, uint16_t* o, float* lse, void* ws,
+                             size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * A paged key-value cache. k and v: [n_pages, n_kv_heads, page_size, head_dim], contiguous (one
+ * page's rows of one head are one run of memory), bf16 (MOE_KV_BF16) or e4m3 (MOE_KV_E4M3: a code c
+ * stands for k_scale[head] * c; scales are device fp32 [n_kv_heads], positive, NULL for bf16).
+ * n_pages * n_kv_heads * page_size < 2^31. A sequence's position p lies in page
+ * page_table[b * table_width + p / page_size], row p % page_size; pages are shared freely between
+ * sequences for reading.
+ */
+#define MOE_KV_BF16 0
+#define MOE_KV_E4M3 1
+typedef struct moe_kv_cache {
+  moe_attn_dims dims;
+  int32_t format;
+  int32_t page_size;
+  int32_t n_pages;
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+} moe_kv_cache;
+
+/*
+ * Writes new keys and values into the cache: row i of sequence b (rows cu[b] .. cu[b+1] - 1 of k
+ * and v, `total` rows in all) goes to position start[b] + i. e4m3: value / scale, clamped to +-448
+ * and rounded to nearest even (NaN stays NaN). Rows whose position or page is outside the table or
+ * the cache are skipped (MOE_ERR_BAD_INDEX). Two rows must not name the same place.
+ */
+MOE_API int moe_kv_append(const moe_kv_cache* cache, moe_heads_view k, moe_heads_view v, const int32_t* cu,
+                          const int32_t* start, const int32_t* page_table, int32_t table_width, int32_t n_seqs,
+                          int32_t total, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over the cache: row b of q sees the positions
+ * 0 .. lens[b] - 1 (device int32[n_seqs]; the new token's own key and value are appended first, so
+ * lens counts it; 0 gives an empty row). The work of all sequences is cut into equal runs of cache
+ * rows, one per SM, so that a batch of uneven lengths and one long sequence alike fill the GPU;
+ * cut sequences are joined in a fixed order (the result of a call does not vary from run to run).
+ * o: bf16 [n_seqs, n_q_heads, head_dim]; lse: fp32 [n_seqs, n_q_heads] or NULL.
+ */
+MOE_API int moe_attn_decode(const moe_kv_cache* cache, moe_heads_view q, const int32_t* lens,
+                            const int32_t* page_table, int32_t table_width, int32_t n_seqs, float scale, uint16_t* o,
+                            float* lse, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Synchronises `stream`, returns the sticky device status of `ws` (MOE_OK or a device error
  * code) and clears it. */

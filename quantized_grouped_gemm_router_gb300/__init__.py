@@ -41,3 +41,14 @@ from .binding import (  # noqa: F401
     workspace,
     workspace_bytes,
 )
+from .attention import (  # noqa: F401
+    AttnDims,
+    KV_BF16,
+    KV_E4M3,
+    KvCache,
+    attn_decode,
+    attn_prefill,
+    attn_workspace,
+    attn_workspace_bytes,
+    kv_append,
+)

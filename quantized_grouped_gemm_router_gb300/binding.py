@@ -38,7 +38,7 @@ class RouteOut(ctypes.Structure):
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE", 3: "MOE_ERR_MISALIGNED",
           4: "MOE_ERR_WORKSPACE_TOO_SMALL", 5: "MOE_ERR_CUDA", 6: "MOE_ERR_NONFINITE",
-          7: "MOE_ERR_DEVICE_TIMEOUT", 8: "MOE_ERR_OUT_OF_RANGE"}
+          7: "MOE_ERR_DEVICE_TIMEOUT", 8: "MOE_ERR_OUT_OF_RANGE", 9: "MOE_ERR_BAD_INDEX"}
 
 
 class MoeError(RuntimeError):

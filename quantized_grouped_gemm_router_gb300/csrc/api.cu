@@ -8,6 +8,7 @@
 #include <mutex>
 #include <vector>
 
+#include "attn.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -56,14 +57,18 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-bool encode(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, const void* ptr, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz) {
+}  // namespace
+
+bool moe::encode_tiled(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, const void* ptr,
+                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return fn(m, type, rank, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // A row-major [rows, cols] 16-bit matrix seen as (64 columns, rows, cols / 64 column blocks), so
 // that one box (64 x box_rows x kb) lands in shared memory as kb consecutive [box_rows][64] tiles,
@@ -73,7 +78,7 @@ bool make_rows_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols
   const cuuint64_t dims[3] = {64, rows, cols / 64};
   const cuuint64_t strides[2] = {cols * 2, 128};
   const cuuint32_t box[3] = {64, box_rows, kb};
-  return encode(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, box,
+  return encode_tiled(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, box,
                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -93,7 +98,7 @@ bool make_gemm_planes(GemmMaps* g, const void* ptr, uint64_t rows, uint64_t cols
     const cuuint64_t dims[4] = {64, rows, 2, cols / 64};
     const cuuint64_t strides[3] = {cols * 2, rows * cols * 2, 128};
     const cuuint32_t box[4] = {64, 16u * (i + 1), 2, kb};
-    if (!encode(&g->rows[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_tiled(&g->rows[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return false;
   }
   g->a = g->rows[0];
@@ -114,8 +119,8 @@ bool make_down_weight_maps(GemmMaps* g, const uint8_t* packed, const PackedLayou
   const cuuint64_t sdims[4] = {kSBBytes / 8, DM, KBD, E1};
   const cuuint64_t sstr[3] = {kSBBytes, DM * kSBBytes, P.expert_stride};
   const cuuint32_t sbox[4] = {kSBBytes / 8, 1, kb, 1};
-  return encode(&g->a, CU_TENSOR_MAP_DATA_TYPE_UINT64, 4, codes, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_NONE) &&
-         encode(&g->a2, CU_TENSOR_MAP_DATA_TYPE_UINT64, 4, sb, sdims, sstr, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
+  return encode_tiled(&g->a, CU_TENSOR_MAP_DATA_TYPE_UINT64, 4, codes, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+         encode_tiled(&g->a2, CU_TENSOR_MAP_DATA_TYPE_UINT64, 4, sb, sdims, sstr, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 }  // namespace
@@ -132,8 +137,8 @@ bool moe::make_decode_down_maps(DecodeMaps* m, const uint8_t* packed, const moe_
   const cuuint64_t sdims[4] = {kSBBytes / 8, DM, KBD, E1};
   const cuuint64_t sstr[3] = {kSBBytes, DM * kSBBytes, P.expert_stride};
   const cuuint32_t sbox[4] = {16 * 4 / 8, 1, pieces / 2, 1};
-  return encode(&m->codes, CU_TENSOR_MAP_DATA_TYPE_UINT64, 4, codes, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_NONE) &&
-         encode(&m->sb, CU_TENSOR_MAP_DATA_TYPE_UINT64, 4, sb, sdims, sstr, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
+  return encode_tiled(&m->codes, CU_TENSOR_MAP_DATA_TYPE_UINT64, 4, codes, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+         encode_tiled(&m->sb, CU_TENSOR_MAP_DATA_TYPE_UINT64, 4, sb, sdims, sstr, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 namespace {
@@ -638,7 +643,7 @@ int moe_read_device_status(void* ws, moe_stream_t stream) {
   WsHeader* h = static_cast<WsHeader*>(ws);
   if (cudaMemcpy(&bits, &h->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaMemset(&h->status, 0, sizeof(int)) != cudaSuccess) return MOE_ERR_CUDA;
-  for (int code = MOE_ERR_NONFINITE; code <= MOE_ERR_OUT_OF_RANGE; ++code)
+  for (int code = MOE_ERR_NONFINITE; code <= MOE_ERR_BAD_INDEX; ++code)
     if (bits & status_bit(code)) return code;
   return MOE_OK;
 }
@@ -654,6 +659,7 @@ const char* moe_status_string(int status) {
     case MOE_ERR_NONFINITE: return "non-finite router logit";
     case MOE_ERR_DEVICE_TIMEOUT: return "bounded device wait gave up";
     case MOE_ERR_OUT_OF_RANGE: return "activation outside the fp16 operand range";
+    case MOE_ERR_BAD_INDEX: return "offset, length or page number outside its range";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,491 @@
+"""The attention calls on a GB300 against plain 64-bit arithmetic (tests/attn_check.py): packed
+prompts, the paged cache's append, one new token per sequence over the cache."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import attn_check as C  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(16, 2), (8, 8), (7, 1), (12, 4), (10, 2), (64, 1)]
+
+
+@pytest.fixture(scope="module")
+def m():
+    from quantized_grouped_gemm_router_gb300 import build as B
+    B.build()
+    import quantized_grouped_gemm_router_gb300 as mod
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return mod
+
+
+def rand(seed, *shape, gain=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * gain).to(torch.bfloat16)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def cu(lens):
+    return ints([0] + torch.tensor(lens).cumsum(0).tolist())
+
+
+def status(m, ws):
+    return m.read_device_status(ws)
+
+
+# ------------------------------------------------------------------------------------ prompts
+def run_prefill(m, dims, q, k, v, lens, causal, scale=None, ws=None):
+    """q, k, v: CUDA int16 views; returns o, lse with every element pre-filled with NaN."""
+    ws = m.attn_workspace(dims) if ws is None else ws
+    o = torch.full((q.shape[0], dims.n_q_heads, dims.head_dim), 0x7FC0, dtype=torch.int16, device="cuda")
+    lse = torch.full((q.shape[0], dims.n_q_heads), math.nan, device="cuda")
+    r = m.attn_prefill(dims, q, k, v, cu([x for x, _ in lens]), cu([x for _, x in lens]), ws, causal=causal,
+                       scale=scale, o=o, lse=lse)
+    assert r is o
+    assert status(m, ws) == 0
+    return o, lse
+
+
+def prompt_case(m, heads, d, lens, causal, seed=0, scale=None, gain=2.0):
+    hq, hkv = heads
+    tq, tk = sum(x for x, _ in lens), sum(x for _, x in lens)
+    q, k, v = rand(seed, tq, hq, d, gain=gain), rand(seed + 1, tk, hkv, d), rand(seed + 2, tk, hkv, d)
+    o, lse = run_prefill(m, m.AttnDims(hq, hkv, d), *(x.view(torch.int16).cuda() for x in (q, k, v)), lens, causal,
+                         scale)
+    ref = C.prefill(q.double(), k.double(), v.double(), lens, 1 / math.sqrt(d) if scale is None else scale, causal)
+    C.check(o, lse, ref, 8, f"{heads} {d} {lens} causal={causal}")
+
+
+LENS = {
+    "one": [(1, 1)],
+    "odd": [(131, 131)],
+    "ragged": [(0, 0), (1, 1), (70, 70), (0, 3), (129, 129), (2, 2)],
+    "continued": [(5, 133), (1, 260), (64, 64), (33, 161)],
+    "fewer_keys": [(40, 7), (3, 0), (130, 129), (1, 1)],   # rows that see nothing
+}
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "both"])
+@pytest.mark.parametrize("lens", LENS.values(), ids=LENS.keys())
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_lengths(m, d, lens, causal):
+    prompt_case(m, (16, 2), d, lens, causal)
+
+
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_heads(m, heads, d):
+    prompt_case(m, heads, d, [(37, 37), (19, 150)], True, seed=5)
+
+
+@pytest.mark.parametrize("d,n", [(64, 700), (128, 641), (256, 515)])
+def test_prompt_many_tiles(m, d, n):
+    prompt_case(m, (4, 2), d, [(n, n)], True, seed=9, gain=4.0)
+    prompt_case(m, (2, 2), d, [(n, n + 100)], False, seed=10, gain=4.0)
+
+
+def test_prompt_many_sequences(m):
+    prompt_case(m, (4, 2), 64, [(i % 4, (i * 7) % 9) for i in range(300)], True, seed=11)
+
+
+def test_prompt_growing_scores(m):
+    """Scores that grow along the keys: the running maximum moves in every tile."""
+    d, n = 128, 600
+    q, v = torch.full((n, 1, d), 0.5).to(torch.bfloat16), rand(1, n, 1, d)
+    k = (torch.arange(n).double()[:, None, None] / 40 * torch.ones(1, 1, d)).to(torch.bfloat16)
+    o, lse = run_prefill(m, m.AttnDims(1, 1, d), *(x.view(torch.int16).cuda() for x in (q, k, v)), [(n, n)], True,
+                         scale=1.0)
+    C.check(o, None, C.prefill(q.double(), k.double(), v.double(), [(n, n)], 1.0, True), 8)
+    # scores up to 960: an fp32 sum of 128 equal products below 2^11, in steps of 2^-13 at most
+    ref = C.prefill(q.double(), k.double(), v.double(), [(n, n)], 1.0, True)[1]
+    assert (lse.cpu().double() - ref).abs().max() < 2.0 ** -9
+
+
+def test_prompt_scale_and_negative_scores(m):
+    prompt_case(m, (4, 2), 64, [(90, 90)], True, seed=12, scale=0.01)
+    d, n = 64, 300                                   # every score strongly negative
+    q, v = torch.ones(n, 2, d).to(torch.bfloat16), rand(2, n, 1, d)
+    k = -torch.ones(n, 1, d).to(torch.bfloat16) * 4 + rand(3, n, 1, d, gain=0.1)
+    o, lse = run_prefill(m, m.AttnDims(2, 1, d), *(x.view(torch.int16).cuda() for x in (q, k, v)), [(n, n)], True,
+                         scale=1.0)
+    C.check(o, None, C.prefill(q.double(), k.double(), v.double(), [(n, n)], 1.0, True), 8)
+
+
+@pytest.mark.parametrize("layout", ["fused", "heads_first", "padded"])
+def test_prompt_strides(m, layout):
+    hq, hkv, d, n = 6, 2, 64, 150
+    q, k, v = rand(1, n, hq, d), rand(2, n, hkv, d), rand(3, n, hkv, d)
+    if layout == "fused":
+        rows = torch.cat([q, k, v], 1).contiguous().view(torch.int16).cuda()
+        dev = rows[:, :hq], rows[:, hq:hq + hkv], rows[:, hq + hkv:]
+    elif layout == "heads_first":
+        dev = [x.permute(1, 0, 2).contiguous().view(torch.int16).cuda().permute(1, 0, 2) for x in (q, k, v)]
+    else:
+        dev = [torch.cat([x, torch.full((n, x.shape[1], 8), math.nan, dtype=torch.bfloat16)], 2).view(torch.int16)
+               .cuda()[:, :, :d] for x in (q, k, v)]
+    o, lse = run_prefill(m, m.AttnDims(hq, hkv, d), *dev, [(n, n)], True)
+    C.check(o, lse, C.prefill(q.double(), k.double(), v.double(), [(n, n)], 1 / 8, True), 8, layout)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf], ids=str)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_nonfinite_unseen(m, d, bad):
+    """Keys and values that a row does not see (later tokens of its own sequence, other sequences)
+    never reach it; the rows that see them are not compared."""
+    lens, hq, hkv = [(50, 50), (140, 140), (20, 20)], 4, 2
+    n = sum(x for x, _ in lens)
+    q, k, v = rand(1, n, hq, d), rand(2, n, hkv, d), rand(3, n, hkv, d)
+    ref = C.prefill(q.double(), k.double(), v.double(), lens, 1 / math.sqrt(d), True)
+    kb, vb = k.clone(), v.clone()
+    kb[50 + 100:50 + 140], vb[50 + 90:50 + 140] = bad, bad      # seen from row 90 of the middle sequence on
+    kb[190, 0], vb[190, 1, 3] = bad, bad                        # first key of the last sequence
+    o, lse = run_prefill(m, m.AttnDims(hq, hkv, d), *(x.view(torch.int16).cuda() for x in (q, kb, vb)), lens, True)
+    C.check(o[:140], lse[:140], [x[:140] for x in ref], 8)
+    got = C.values(o)
+    assert not torch.isfinite(got[140:190]).all(dim=-1).any()   # and rows that do see them show it
+    # in the last sequence only the heads and columns that read the bad cells
+    assert torch.isfinite(got[190:, 2:, :3]).all() and torch.isfinite(got[190:, 2:, 4:]).all()
+    assert not torch.isfinite(got[190:, 2:, 3]).any()
+
+
+def test_prompt_nonfinite_both_ways(m):
+    """Without causality the tail of a tile still belongs to another sequence."""
+    lens, d = [(70, 70), (30, 30)], 128
+    q, k, v = rand(1, 100, 2, d), rand(2, 100, 1, d), rand(3, 100, 1, d)
+    ref = C.prefill(q.double(), k.double(), v.double(), lens, 1 / math.sqrt(d), False)
+    k[70:], v[70:] = math.inf, math.nan
+    o, lse = run_prefill(m, m.AttnDims(2, 1, d), *(x.view(torch.int16).cuda() for x in (q, k, v)), lens, False)
+    C.check(o[:70], lse[:70], [x[:70] for x in ref], 8)
+
+
+def test_prompt_bad_offsets(m):
+    """Offsets outside the rows raise the status and touch nothing outside the buffers."""
+    dims = m.AttnDims(4, 2, 64)
+    x = rand(1, 40, 4, 64).view(torch.int16).cuda()
+    for cq, ck in (([0, 30, 20, 40], [0, 30, 30, 40]), ([0, 10, 20, 400], [0, 10, 20, 40]),
+                   ([0, 10, 20, 40], [0, 10, 20, 1000000]), ([-5, 10, 20, 40], [0, 10, 20, 40]),
+                   ([0, 10, 20, 40], [0, -1000000, 20, 40])):
+        ws = m.attn_workspace(dims)
+        m.attn_prefill(dims, x, x[:, :2], x[:, 2:], ints(cq), ints(ck), ws)
+        assert status(m, ws) == 9, (cq, ck)
+        assert status(m, ws) == 0
+
+
+def test_prompt_streams_graphs_and_repeats(m):
+    dims, lens = m.AttnDims(8, 2, 128), [(200, 200), (77, 77)]
+    q, k, v = (rand(i, 277, h, 128).view(torch.int16).cuda() for i, h in ((1, 8), (2, 2), (3, 2)))
+    c, ws = cu([200, 77]), m.attn_workspace(dims)
+    a, _ = run_prefill(m, dims, q, k, v, lens, True, ws=ws)
+    b, _ = run_prefill(m, dims, q, k, v, lens, True, ws=ws)
+    assert torch.equal(a, b)
+    o = torch.zeros_like(a)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        m.attn_prefill(dims, q, k, v, c, c, ws, o=o)
+    side.synchronize()
+    assert torch.equal(a, o)
+    o.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.attn_prefill(dims, q, k, v, c, c, ws, o=o)
+    for _ in range(2):
+        o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, o)
+
+
+def test_prompt_far_offsets(m):
+    """Rows more than 2^32 bytes apart (2^31 elements and more from the base)."""
+    d, n, step = 64, 1100, 1 << 22
+    big = torch.empty((n * step,), dtype=torch.int16, device="cuda")
+    rows = big.as_strided((n, 4, d), (step, d, 1))
+    x = rand(1, n, 4, d)
+    rows.copy_(x.view(torch.int16).cuda())
+    lens = [(1000, 1000), (100, 100)]
+    o, lse = run_prefill(m, m.AttnDims(2, 1, d), rows[:, :2], rows[:, 2:3], rows[:, 3:], lens, True)
+    ref = C.prefill(x[1000:, :2].double(), x[1000:, 2:3].double(), x[1000:, 3:].double(), lens[1:], 1 / 8, True)
+    C.check(o[1000:], lse[1000:], ref, 8)
+
+
+def test_prompt_empty(m):
+    dims = m.AttnDims(4, 2, 64)
+    ws = m.attn_workspace(dims)
+    none = torch.empty((0, 4, 64), dtype=torch.int16, device="cuda")
+    assert m.attn_prefill(dims, none, none[:, :2], none[:, :2], ints([0, 0]), ints([0, 0]), ws).shape == (0, 4, 64)
+    q = rand(1, 5, 4, 64).view(torch.int16).cuda()
+    o, lse = run_prefill(m, dims, q, none[:, :2], none[:, :2], [(5, 0)], False)
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
+# ------------------------------------------------------------------------------------ the cache
+def table_for(lens, page, seed=0, spare=2):
+    """A random page table; entries past a sequence's pages name no page at all."""
+    g = torch.Generator().manual_seed(seed)
+    need = [(n + page - 1) // page for n in lens]
+    total = sum(need) + spare
+    order = torch.randperm(total, generator=g).tolist()
+    t = torch.full((len(lens), max(1, max(need))), -7, dtype=torch.int32)
+    for b, n in enumerate(need):
+        for i in range(n):
+            t[b, i] = order.pop()
+    return t, total
+
+
+def e4m3(x, scale):
+    return (x.float() / scale).clamp(-448, 448).to(torch.float8_e4m3fn)
+
+
+def make_cache(m, dims, lens, page, fp8, seed=0, table=None):
+    """Random keys and values of every position, in the cache's own cells (all others hold NaN), and
+    the values they stand for, [hkv, len, d] in 64 bits per sequence."""
+    hkv, d = dims.n_kv_heads, dims.head_dim
+    t, total = table_for(lens, page, seed) if table is None else table
+    scales = [torch.rand(hkv, generator=torch.Generator().manual_seed(seed + i)) * 0.02 + 0.01 for i in range(2)]
+    cells = [torch.full((total, hkv, page, d), 0x7F if fp8 else 0x7FC0, dtype=torch.uint8 if fp8 else torch.int16)
+             for _ in range(2)]
+    vals = []
+    for b, n in enumerate(lens):
+        both = []
+        pos = torch.arange(n)
+        at = t[b, pos // page].long()
+        for i in range(2):
+            x = rand(seed + 10 * b + i, n, hkv, d)
+            if fp8:
+                code = e4m3(x, scales[i][None, :, None])
+                cells[i][at, :, pos % page] = code.view(torch.uint8)
+                both.append((code.float().double() * scales[i].double()[None, :, None]).transpose(0, 1))
+            else:
+                cells[i][at, :, pos % page] = x.view(torch.int16)
+                both.append(x.double().transpose(0, 1))
+        vals.append(both)
+    cache = m.KvCache(dims, cells[0].cuda(), cells[1].cuda(), *((s.cuda() for s in scales) if fp8 else ()))
+    return cache, t.cuda(), vals
+
+
+def run_decode(m, cache, q, lens, table, ws=None, scale=None):
+    dims = cache.dims
+    ws = m.attn_workspace(dims) if ws is None else ws
+    o = torch.full((q.shape[0], dims.n_q_heads, dims.head_dim), 0x7FC0, dtype=torch.int16, device="cuda")
+    lse = torch.full((q.shape[0], dims.n_q_heads), math.nan, device="cuda")
+    m.attn_decode(cache, q, ints(lens), table, ws, o=o, lse=lse, scale=scale)
+    assert status(m, ws) == 0
+    return o, lse
+
+
+def decode_ref(q, vals, scale):
+    b, hq, d = q.shape
+    g = hq // vals[0][0].shape[0]
+    out = [torch.zeros(b, hq, d).double(), torch.zeros(b, hq).double(), torch.zeros(b, hq, d).double()]
+    for i in range(b):
+        for h in range(hq):
+            k, v = vals[i][0][h // g], vals[i][1][h // g]
+            r = C.attend(q[i, h:h + 1].double(), k, v, scale, torch.ones(1, len(k), dtype=torch.bool))
+            for to, x in zip(out, r):
+                to[i, h] = x[0]
+    return out
+
+
+def decode_case(m, heads, d, lens, page, fp8, seed=0, gain=2.0):
+    dims = m.AttnDims(*heads, d)
+    cache, table, vals = make_cache(m, dims, lens, page, fp8, seed)
+    q = rand(seed + 7, len(lens), heads[0], d, gain=gain)
+    o, lse = run_decode(m, cache, q.view(torch.int16).cuda(), lens, table)
+    C.check(o, lse, decode_ref(q, vals, 1 / math.sqrt(d)), 11 if fp8 else 8, f"{heads} {d} {lens} {page} {fp8}")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,page", [([1], 16), ([0, 5, 0], 16), ([15, 16, 17, 33], 16), ([700], 64), ([129, 1, 64], 128),
+                                       ([7, 300], 1), ([100, 55, 3], 48), ([513], 7)], ids=str)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_token_lengths_and_pages(m, d, lens, page, fp8):
+    decode_case(m, (16, 2), d, lens, page, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("heads", HEADS + [(17, 1), (32, 2)], ids=str)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_token_heads(m, heads, d, fp8):
+    decode_case(m, heads, d, [90, 33, 1], 16, fp8, seed=3)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_token_long_and_batched(m, fp8):
+    decode_case(m, (4, 2), 128, [9001], 64, fp8, seed=4, gain=4.0)
+    decode_case(m, (4, 4), 64, [(37 * i) % 211 for i in range(190)], 32, fp8, seed=5)
+    decode_case(m, (8, 1), 256, [3000, 1, 0, 2999], 16, fp8, seed=6)
+
+
+def test_token_batch_with_long_one(m):
+    """More sequences than SMs and one that is far longer than the rest."""
+    decode_case(m, (2, 1), 64, [3] * 100 + [20000] + [40] * 99, 16, False, seed=8)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_token_large_and_small_queries(m, fp8):
+    """Queries far from 1 (fp16 holds neither end of bf16's range)."""
+    dims, lens = m.AttnDims(4, 1, 64), [50, 20]
+    cache, table, vals = make_cache(m, dims, lens, 16, fp8)
+    for size in (1e-30, 1e6, 1e35):
+        q = rand(3, 2, 4, 64) * size
+        scale = float(1.0 / (8.0 * size))
+        o, lse = run_decode(m, cache, q.view(torch.int16).cuda(), lens, table, scale=scale)
+        C.check(o, lse, decode_ref(q, vals, scale), 11 if fp8 else 8, f"{size}")
+
+
+def test_token_workspace_reused(m):
+    """One workspace over calls of different batches; same call, same bits; another stream; a graph."""
+    dims = m.AttnDims(16, 2, 128)
+    ws = m.attn_workspace(dims)
+    first = None
+    for lens in ([5000, 3], [17] * 30, [1], [0], [2222, 1111, 4444], [5000, 3]):
+        cache, table, vals = make_cache(m, dims, lens, 32, False, seed=len(lens))
+        q = rand(1, len(lens), 16, 128)
+        o, lse = run_decode(m, cache, q.view(torch.int16).cuda(), lens, table, ws)
+        if lens == [5000, 3]:
+            if first is None:
+                first = o
+                C.check(o, lse, decode_ref(q, vals, 1 / math.sqrt(128)), 8)
+            else:
+                assert torch.equal(first, o)
+    qd, n, out = q.view(torch.int16).cuda(), ints(lens), torch.zeros_like(first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        m.attn_decode(cache, qd, n, table, ws, o=out)
+    side.synchronize()
+    assert torch.equal(first, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.attn_decode(cache, qd, n, table, ws, o=out)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, out)
+
+
+def test_token_bad_pages_and_lengths(m):
+    dims = m.AttnDims(4, 2, 64)
+    cache, table, _ = make_cache(m, dims, [100, 100], 16, False)
+    q = rand(1, 2, 4, 64).view(torch.int16).cuda()
+    for bad in (-1, 1 << 30, cache.k.shape[0]):
+        t, ws = table.clone(), m.attn_workspace(dims)
+        t[1, 3] = bad
+        m.attn_decode(cache, q, ints([100, 100]), t, ws)
+        assert status(m, ws) == 9 and status(m, ws) == 0
+    for lens in ([100, -1], [100, 7 * 16 + 1], [1 << 30, 100]):
+        ws = m.attn_workspace(dims)
+        m.attn_decode(cache, q, ints(lens), table, ws)
+        assert status(m, ws) == 9, lens
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_cache_far_offsets(m, fp8):
+    """Pages more than 2^32 bytes into the cache, appended to and read back."""
+    dims, page, lens = m.AttnDims(4, 2, 128), 64, [200]
+    size = 1 if fp8 else 2
+    n_pages = (5 << 30) // (2 * page * 128 * size)
+    s = torch.tensor([0.02, 0.03], device="cuda") if fp8 else None
+    cache = m.KvCache.empty(dims, n_pages, page, s, s)
+    table = ints([[n_pages - 1, n_pages - 3, 0, n_pages - 2]])
+    k, v, ws = rand(1, 200, 2, 128), rand(2, 200, 2, 128), m.attn_workspace(dims)
+    m.kv_append(cache, k.view(torch.int16).cuda(), v.view(torch.int16).cuda(), cu([200]), ints([0]), table, ws)
+    q = rand(3, 1, 4, 128)
+    o, lse = run_decode(m, cache, q.view(torch.int16).cuda(), lens, table, ws)
+    if fp8:
+        sc = s.cpu()[None, :, None]
+        k, v = (e4m3(x, sc).float().double() * sc.double() for x in (k, v))
+    ref = decode_ref(q, [[k.double().transpose(0, 1), v.double().transpose(0, 1)]], 1 / math.sqrt(128))
+    C.check(o, lse, ref, 11 if fp8 else 8)
+
+
+# ------------------------------------------------------------------------------------ the append
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("new,start,page", [([1], [0], 16), ([3, 0, 40, 1], [5, 9, 14, 0], 16), ([1] * 70, list(range(70)), 32),
+                                            ([200, 7], [1000, 3], 7)], ids=["one", "ragged", "tokens", "long"])
+@pytest.mark.parametrize("hkv,d", [(2, 128), (1, 64), (3, 256), (5, 64)])
+def test_append(m, hkv, d, new, start, page, fp8):
+    dims = m.AttnDims(hkv, hkv, d)
+    lens = [a + b for a, b in zip(new, start)]
+    t, total = table_for(lens, page)
+    n = sum(new)
+    scales = torch.rand(2, hkv, generator=torch.Generator().manual_seed(1)) * 0.02 + 0.01
+    cells = torch.randint(0, 100, (2, total, hkv, page, d), dtype=torch.uint8 if fp8 else torch.int16)
+    x = rand(4, n, 2 * hkv, d)
+    x[0, 0, :6] = torch.tensor([math.nan, math.inf, -math.inf, 1e30, -0.0, 1e-30])
+    cache = m.KvCache(dims, cells[0].cuda(), cells[1].cuda(), *((scales[0].cuda(), scales[1].cuda()) if fp8 else ()))
+    rows, ws = x.view(torch.int16).cuda(), m.attn_workspace(dims)
+    m.kv_append(cache, rows[:, :hkv], rows[:, hkv:], cu(new), ints(start), t.cuda(), ws)
+    assert status(m, ws) == 0
+    want, r = cells.clone(), 0
+    for b, c in enumerate(new):
+        for i in range(c):
+            pos = start[b] + i
+            for s in range(2):
+                y = x[r, s * hkv:(s + 1) * hkv]
+                want[s, t[b, pos // page], :, pos % page] = (e4m3(y, scales[s][:, None]).view(torch.uint8) if fp8
+                                                             else y.view(torch.int16))
+            r += 1
+    got = torch.stack([cache.k.cpu(), cache.v.cpu()])
+    if fp8:  # a NaN may carry either sign
+        got, want = (torch.where((y & 0x7F) == 0x7F, torch.full_like(y, 0x7F), y) for y in (got, want))
+    assert torch.equal(got, want)
+
+
+def test_append_bad_places(m):
+    """Rows without a place are skipped, the others written."""
+    dims = m.AttnDims(2, 2, 64)
+    k = rand(1, 4, 2, 64).view(torch.int16).cuda()
+    for start, table, cuq in (([60, 0], [[0, 1], [2, 3]], [0, 2, 4]), ([-3, 0], [[0, 1], [2, 3]], [0, 2, 4]),
+                              ([0, 0], [[9, 1], [2, 3]], [0, 2, 4]), ([0, 0], [[-1, 1], [2, 3]], [0, 2, 4]),
+                              ([0, 0], [[0, 1], [2, 3]], [0, 5, 3]), ([0, 0], [[0, 1], [2, 3]], [1, 2, 4])):
+        cache, ws = m.KvCache.empty(dims, 4, 16), m.attn_workspace(dims)
+        cache.k.fill_(7), cache.v.fill_(7)
+        m.kv_append(cache, k, k, ints(cuq), ints(start), ints(table), ws)
+        assert status(m, ws) == 9, (start, table, cuq)
+        if cuq == [0, 2, 4]:
+            assert torch.equal(cache.k[2, :, 0], k[2]) and torch.equal(cache.v[2, :, 1], k[3])
+            assert (cache.k[:2] == 7).all()
+
+
+# ------------------------------------------------------------------------------------ together
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_prompt_then_tokens(m, fp8):
+    """A prompt's keys and values appended to the cache, then new tokens one by one: each token's
+    output is the last row of attention over the whole text so far."""
+    dims, page, d = m.AttnDims(4, 2, 128), 16, 128
+    lens, steps = [45, 3], 3
+    scale = torch.tensor([0.02, 0.015])
+    q, k, v = (rand(i, len(lens), 60, h, d) for i, h in ((1, 4), (2, 2), (3, 2)))
+    ws = m.attn_workspace(dims)
+    s = scale.cuda() if fp8 else None
+    cache = m.KvCache.empty(dims, 10, page, s, s)
+    table = ints([[3, 9, 1, 0], [5, 2, 8, 7]])
+    pack = lambda x: torch.cat([x[b, :n] for b, n in enumerate(lens)]).view(torch.int16).cuda()  # noqa: E731
+    c = cu(lens)
+    m.attn_prefill(dims, pack(q), pack(k), pack(v), c, c, ws)
+    m.kv_append(cache, pack(k), pack(v), c, ints([0, 0]), table, ws)
+    if fp8:
+        k, v = ((e4m3(x, scale[:, None]).float() * scale[:, None]).double() for x in (k, v))
+    at = list(lens)
+    one = ints([0, 1, 2])
+    for _ in range(steps):
+        row = lambda x: torch.stack([x[b, n] for b, n in enumerate(at)])  # noqa: E731
+        if fp8:  # the new rows before rounding
+            kn, vn = (torch.stack([rand(i, len(lens), 60, 2, d)[b, n] for b, n in enumerate(at)]) for i in (2, 3))
+        else:
+            kn, vn = row(k), row(v)
+        m.kv_append(cache, kn.view(torch.int16).cuda(), vn.view(torch.int16).cuda(), one, ints(at), table, ws)
+        at = [n + 1 for n in at]
+        qn = torch.stack([q[b, n - 1] for b, n in enumerate(at)])
+        o, lse = run_decode(m, cache, qn.view(torch.int16).cuda(), at, table, ws)
+        vals = [[x[b, :n].double().transpose(0, 1) for x in (k, v)] for b, n in enumerate(at)]
+        C.check(o, lse, decode_ref(qn, vals, 1 / math.sqrt(d)), 11 if fp8 else 8)
