@@ -1,90 +1,487 @@
-// moe_attn_prefill: attention over packed prompts.
+// moe_attn_prefill: attention over packed prompts on the tensor cores.
 //
-// One warp per (query row, head): the row's key-value head's keys one after the other, each lane
-// holding d / 32 of the products, with the running maximum and sum of a softmax.
+// For a tile of query rows, over tiles of BN keys: S = Q K^T (tcgen05, fp32 in tensor memory), the
+// running maximum m and sum l of a softmax in registers, P = 2^(c S - c m) (c = scale log2 e) rounded
+// to bf16 back into tensor memory over S, O += P V (tcgen05, O in tensor memory, P its A operand). K and
+// V are read once per tile of rows; nothing of size rows x keys leaves the SM.
+//
+//  * Rows. The G query heads of one key-value head read the same keys, so a 128-row tile is 128 / G
+//    positions x G heads: a K or V tile serves all of them, and the diagonal of a causal mask spans
+//    few positions. One CTA holds NT tiles of rows (each with its own softmax warps).
+//  * Steps. Step n is (key tile n / NT, row tile n % NT); its scores go to S buffer n % 2. The MMA
+//    warp issues S(0), S(1), then for every n: P(n) V, S(n + 2). The tensor cores thus work on one
+//    tile while the softmax of the other runs, with two row tiles (NT = 2) as with one.
+//  * Rescaling. O is scaled down only when a row's maximum has grown by more than 2^8 since the last
+//    time (weights up to 2^8 are as exact in bf16, and l and O have fp32's range): softmax warps read O
+//    back on few tiles.
+//  * Masks. A tile that every row sees takes no compare. Scores a row does not see become -inf, so
+//    their weight is 0; but 0 times a NaN or infinity in V is not 0, so a warp checks the V tiles that
+//    some row does not see whole, and a tile with such a value is multiplied by the softmax warps,
+//    seen keys only (rare, and bounded by one tile's work).
+//  * K and V tiles are one ring, filled by TMA in the order in which the MMA warp frees them.
 #include "attn_device.cuh"
+#include "attn_ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 4;
+// With two row tiles the warpgroups share the block's registers out: 168 x 384 at launch, then 80 for
+// the four issuing warps and 208 for each softmax thread (2 x 128 x 208 + 128 x 80 <= 168 x 384).
+constexpr int kLaunchRegs = 168;
+__device__ __forceinline__ void regs_for_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+__device__ __forceinline__ void regs_for_issue() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRescaleLog2 = 8.f;
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) attn_prefill_kernel(AttnPrefillParams p) {
-  constexpr int W = D / 64;  // words of two values per lane
-  const int lane = threadIdx.x & 31, t = blockIdx.x, h = blockIdx.y * kWarps + threadIdx.x / 32;
-  if (h >= p.hq) return;
-  if (t == 0 && h == 0) {
-    check_offsets(p.cu_q, p.n_seqs, p.total_q, p.hdr, lane, 32);
-    check_offsets(p.cu_k, p.n_seqs, p.total_k, p.hdr, lane, 32);
-  }
-  int lo = 0, hi = p.n_seqs;
-  while (hi - lo > 1) {  // the last sequence that begins at or before t
-    const int mid = (lo + hi) / 2;
-    if (p.cu_q[mid] <= t) lo = mid; else hi = mid;
-  }
-  const int q0 = p.cu_q[lo], q1 = min(p.cu_q[lo + 1], p.total_q);
-  const int k0 = max(p.cu_k[lo], 0), k1 = min(p.cu_k[lo + 1], p.total_k);
-  if (q0 > t || q1 <= t || q0 < 0 || k1 < k0) {
-    if (lane == 0) raise_bad_index(p.hdr);
-    return;
-  }
-  int n = k1 - k0;
-  if (p.causal) n = min(n, max(0, t - q0 + 1 + (k1 - k0) - (q1 - q0)));
-  const int kvh = h / p.group;
-  float q[2 * W], acc[2 * W], m = -INFINITY, l = 0.f;
-  const uint32_t* qp = reinterpret_cast<const uint32_t*>(p.q.p + t * p.q.token_stride + h * p.q.head_stride);
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    q[2 * i] = bf16_lo(qp[lane + 32 * i]) * p.scale;
-    q[2 * i + 1] = bf16_hi(qp[lane + 32 * i]) * p.scale;
-    acc[2 * i] = acc[2 * i + 1] = 0.f;
-  }
-  for (int j = 0; j < n; ++j) {
-    const int64_t r = k0 + j;
-    const uint32_t* kp = reinterpret_cast<const uint32_t*>(p.k.p + r * p.k.token_stride + kvh * p.k.head_stride);
-    const uint32_t* vp = reinterpret_cast<const uint32_t*>(p.v.p + r * p.v.token_stride + kvh * p.v.head_stride);
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      s = fmaf(q[2 * i], bf16_lo(kp[lane + 32 * i]), s);
-      s = fmaf(q[2 * i + 1], bf16_hi(kp[lane + 32 * i]), s);
+template <int D, int NT>
+struct Cfg {
+  static constexpr int BN = D == 256 ? 64 : 128;       // keys per tile (D = 256: two more tiles in flight)
+  static constexpr int kChunks = D / 64;               // 128-byte columns of a row
+  static constexpr int kQTile = kChunks * 16384;       // one row tile
+  static constexpr int kSlot = BN * D * 2;             // one K or V tile
+  static constexpr int kSlots = (224 * 1024 - NT * kQTile) / kSlot < 8 ? (224 * 1024 - NT * kQTile) / kSlot : 8;
+  static constexpr int kSmem = NT * kQTile + kSlots * kSlot + 1024 + 512;  // + alignment + barriers
+  static constexpr int kSoftWarps = 4 * NT;
+  static constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 1, kWarpCheck = kSoftWarps + 2;
+  static constexpr int kThreads = 32 * (kSoftWarps + 4);  // one more warp idles: whole warpgroups
+  static constexpr uint32_t kOCol = 2 * BN;            // S buffers at 0 and BN, O tiles behind them
+  static_assert(kOCol + NT * D <= 512 && kSlots >= 4 && kSmem <= 232448, "on-chip memory");
+};
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+// What a CTA works on.
+struct Item {
+  int q_row, n_pos;  // first query row (absolute) and positions of this CTA
+  int pos0;          // the first position within the sequence
+  int k_row, lk;     // first key row and keys of the sequence
+  int off;           // keys that query 0 sees before its own: lk - lq
+};
+
+// Tile `slot` of all sequences' tiles of P positions, each sequence's last tile first (under a causal
+// mask it has the most keys). One warp; false if there is no such tile.
+__device__ __forceinline__ bool find_item(const AttnPrefillParams& p, int slot, int P, Item& it) {
+  const int lane = threadIdx.x & 31;
+  for (int base = 0; base < p.n_seqs; base += 32) {
+    const int i = base + lane;
+    int q0 = 0, n = 0;
+    if (i < p.n_seqs) {
+      q0 = min(max(__ldg(p.cu_q + i), 0), p.total_q);
+      n = min(max(__ldg(p.cu_q + i + 1), q0), p.total_q) - q0;
     }
+    const int tiles = (n + P - 1) / P;
+    int sum = tiles;
 #pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-    const float m2 = fmaxf(m, s), base = m2 == -INFINITY ? 0.f : m2;
-    const float a = expf(m - base), e = expf(s - base);
-    m = m2;
-    l = l * a + e;
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(~0u, sum, x);
+      if (lane >= x) sum += y;
+    }
+    const unsigned m = __ballot_sync(~0u, sum > slot);
+    if (m) {
+      const int src = __ffs(m) - 1;
+      const int mine = tiles - 1 - (slot - (sum - tiles));  // meaningful in lane src only
+      const int tile = __shfl_sync(~0u, mine, src), lq = __shfl_sync(~0u, n, src);
+      const int s = base + src;
+      it.pos0 = tile * P;
+      it.q_row = __shfl_sync(~0u, q0, src) + it.pos0;
+      it.n_pos = min(P, lq - it.pos0);
+      it.k_row = min(max(__ldg(p.cu_k + s), 0), p.total_k);
+      it.lk = min(max(__ldg(p.cu_k + s + 1), it.k_row), p.total_k) - it.k_row;
+      it.off = it.lk - lq;
+      return true;
+    }
+    slot -= __shfl_sync(~0u, sum, 31);
+  }
+  return false;
+}
+
+// Adds seen weights x V to this thread's row of O, key by key: for V tiles that hold a NaN or an
+// infinity some row does not see. P: this row's bf16 weights in tensor memory.
+template <int D, int BN>
+__device__ __forceinline__ void add_seen(uint32_t o_tmem, uint32_t p_tmem, const uint8_t* v, int seen, bool fresh) {
+  for (int d0 = 0; d0 < D; d0 += 32) {
+    float acc[32];
+    tmem_ld32(o_tmem + d0, acc);
+    tmem_wait_ld();
+    if (fresh)
+      for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+    for (int j0 = 0; j0 < BN; j0 += 32) {
+      uint32_t w[16];
+      __syncwarp();
+      tmem_ld16(p_tmem + j0 / 2, w);
+      tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      acc[2 * i] = fmaf(acc[2 * i], a, e * bf16_lo(vp[lane + 32 * i]));
-      acc[2 * i + 1] = fmaf(acc[2 * i + 1], a, e * bf16_hi(vp[lane + 32 * i]));
+      for (int j = 0; j < 32; ++j) {
+        const int row = j0 + j;
+        if (row >= seen) continue;
+        const float x = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+        const uint8_t* at = v + (d0 / 64) * (BN * 128) + row * 128;
+        for (int i = 0; i < 32; i += 2) {
+          const uint32_t y = *reinterpret_cast<const uint32_t*>(at + (((d0 % 64 + i) * 2) ^ ((row & 7) << 4)));
+          acc[i] = fmaf(x, __uint_as_float(y << 16), acc[i]);
+          acc[i + 1] = fmaf(x, __uint_as_float(y & 0xFFFF0000u), acc[i + 1]);
+        }
+      }
+    }
+    __syncwarp();
+    tmem_st32(o_tmem + d0, reinterpret_cast<uint32_t*>(acc));
+    tmem_wait_st();
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+    attn_prefill_kernel(const __grid_constant__ AttnPrefillParams p, const __grid_constant__ Maps maps) {
+  using C = Cfg<D, NT>;
+  constexpr int BN = C::BN;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = smem + NT * C::kQTile;
+  uint8_t* misc = ring + C::kSlots * C::kSlot;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(misc);
+  volatile int* s_bad = reinterpret_cast<volatile int*>(misc + 4);  // [2] V tile (counted from j_masked, % 2) holds a non-finite value
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + 12);
+  Item* s_item = reinterpret_cast<Item*>(misc + 16);
+  int* s_found = reinterpret_cast<int*>(misc + 48);
+  const uint32_t bars = smem_u32(misc + 64);
+  const uint32_t q_full = bars;
+  const auto s_full = [&](int b) { return bars + 8 + 8 * b; };
+  const auto p_ready = [&](int b) { return bars + 24 + 8 * b; };
+  const auto pv_done = [&](int a) { return bars + 40 + 8 * a; };
+  const auto checked = [&](int b) { return bars + 56 + 8 * b; };
+  const auto check = [&](int b) { return bars + 72 + 8 * b; };
+  const auto kv_full = [&](int s) { return bars + 88 + 8 * s; };
+  const auto kv_free = [&](int s) { return bars + 88 + 8 * C::kSlots + 8 * s; };
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int G = p.group, Ppt = 128 / G;  // positions per row tile
+  const int kvh = blockIdx.x % p.hkv, slot = blockIdx.x / p.hkv;
+
+  if (warp == 0) {
+    Item it;
+    const bool found = find_item(p, slot, NT * Ppt, it);
+    if (lane == 0) {
+      *s_found = found;
+      if (found) *s_item = it;
+    }
+    if (blockIdx.x == 0) {
+      check_offsets(p.cu_q, p.n_seqs, p.total_q, p.hdr, lane, 32);
+      check_offsets(p.cu_k, p.n_seqs, p.total_k, p.hdr, lane, 32);
+    }
+  } else if (warp == C::kWarpMma) {
+    tmem_alloc(smem_u32(s_tmem), 512);
+    tmem_relinquish();
+  } else if (warp == C::kWarpTma && lane == 0) {
+    *s_abort = 0;
+    mbar_init(q_full, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(s_full(b), 1);
+      mbar_init(p_ready(b), 4);
+      mbar_init(pv_done(b), 1);
+      mbar_init(checked(b), 1);
+      mbar_init(check(b), 1);
+    }
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_free(s), 1);
+    }
+    fence_barrier_init();
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const bool found = *s_found;
+
+  if (found) {
+    const Item it = *s_item;
+    // keys that the first and the last position of this CTA see
+    const int first_seen = p.causal ? min(max(it.pos0 + 1 + it.off, 0), it.lk) : it.lk;
+    const int last_seen = p.causal ? min(max(it.pos0 + it.n_pos + it.off, 0), it.lk) : it.lk;
+    const int nj = (last_seen + BN - 1) / BN, steps = NT * nj;
+    const int j_masked = first_seen / BN;  // tiles from here on are not seen whole by every row
+    // the place of K tile j and V tile j in the ring's order
+    const auto k_idx = [&](int j) { return NT == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
+    const auto v_idx = [&](int j) { return NT == 2 ? 2 * j + 1 : (j == nj - 1 ? 2 * j + 1 : 2 * j + 2); };
+
+    if (warp >= C::kSoftWarps) {
+    if (NT == 2) regs_for_issue();
+    if (warp == C::kWarpTma) {
+      // ------------------------------------------------------------------ TMA producer
+      if (lane == 0 && steps) {
+        mbar_arrive_expect_tx(q_full, (uint32_t)(NT * C::kChunks * Ppt * G * 128));
+        for (int a = 0; a < NT; ++a)
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(smem_u32(smem) + a * C::kQTile + c * 16384, &maps.q, c * 64, kvh * G, it.q_row + a * Ppt, q_full);
+        int issued = 0;
+        for (; issued < 2 * nj; ++issued) {
+          const int i = issued, s = i % C::kSlots;
+          if (i >= C::kSlots && !mbar_wait(kv_free(s), ((i / C::kSlots) & 1) ^ 1, s_abort)) break;
+          // entry i of the order K0 V0 K1 V1 ... (NT = 2) or K0 K1 V0 K2 V1 ... (NT = 1)
+          bool is_v;
+          int j;
+          if (NT == 2) {
+            is_v = i & 1;
+            j = i / 2;
+          } else if (i == 2 * nj - 1) {
+            is_v = true;
+            j = nj - 1;
+          } else {
+            is_v = i >= 2 && !(i & 1);
+            j = is_v ? i / 2 - 1 : (i + 1) / 2;
+          }
+          mbar_arrive_expect_tx(kv_full(s), (uint32_t)C::kSlot);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(smem_u32(ring) + s * C::kSlot + c * (BN * 128), is_v ? &maps.v : &maps.k, c * 64, kvh,
+                        it.k_row + j * BN, kv_full(s));
+        }
+        if (*s_abort) {  // copies in flight must land before the CTA's memory is given up
+          int none = 0;
+          mbar_wait(q_full, 0, &none);
+          for (int i = max(0, issued - C::kSlots); i < issued; ++i)
+            mbar_wait(kv_full(i % C::kSlots), (i / C::kSlots) & 1, &none);
+        }
+      }
+    } else if (warp == C::kWarpMma) {
+      // ------------------------------------------------------------------ MMA issuer
+      const uint32_t idesc_s = idesc_f16(128, BN, false), idesc_o = idesc_f16(128, D, false) | kIdescBMn;
+      const auto wait = [&](uint32_t bar, int parity) { return __all_sync(~0u, mbar_wait(bar, parity & 1, s_abort)); };
+      const auto scores = [&](int n) {
+        const int j = n / NT, a = n % NT, i = k_idx(j), s = i % C::kSlots;
+        if (!wait(kv_full(s), i / C::kSlots)) return false;
+        tc_fence_after();
+        const uint64_t qd = sw128_desc(smem_u32(smem) + a * C::kQTile), kd = sw128_desc(smem_u32(ring) + s * C::kSlot);
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16_ss_elect(tmem + (n & 1) * BN, qd + c * (16384 / 16) + ks * 2, kd + c * (BN * 128 / 16) + ks * 2,
+                              idesc_s, c + ks != 0);
+        umma_commit_elect(s_full(n & 1));
+        if (a == NT - 1) umma_commit_elect(kv_free(s));
+        // V tile j's slot has seen its last copy but one arrive (an earlier K or V tile than K tile j), and
+        // s_bad of tile j - 2 has been read: the check of V tile j may begin
+        if (a == 0 && j >= j_masked && lane == 0) mbar_arrive(check((j - j_masked) & 1));
+        __syncwarp();
+        return true;
+      };
+      bool ok = steps > 0 && wait(q_full, 0) && scores(0) && (steps == 1 || scores(1));
+      for (int n = 0; ok && n < steps; ++n) {
+        const int j = n / NT, a = n % NT, i = v_idx(j), s = i % C::kSlots;
+        if (!(ok = wait(p_ready(n & 1), n >> 1) && wait(kv_full(s), i / C::kSlots))) break;
+        tc_fence_after();
+        if (!(j >= j_masked && s_bad[(j - j_masked) & 1])) {
+          const uint64_t vd = sw128_mn_desc(smem_u32(ring) + s * C::kSlot, BN * 128);
+#pragma unroll
+          for (int ks = 0; ks < BN / 16; ++ks)
+            umma_f16_ts_elect(tmem + C::kOCol + a * D, tmem + (n & 1) * BN + ks * 8, vd + ks * (16 * 128 / 16), idesc_o,
+                              j + ks != 0);
+        }
+        umma_commit_elect(pv_done(a));
+        if (a == NT - 1) umma_commit_elect(kv_free(s));
+        if (n + 2 < steps) ok = scores(n + 2);
+      }
+    } else if (warp == C::kWarpCheck) {
+      // ------------------------------------------------------------------ V tiles not seen whole
+      for (int j = j_masked; j < nj; ++j) {
+        const int i = v_idx(j), s = i % C::kSlots, x = j - j_masked, b = x & 1;
+        if (!__all_sync(~0u, mbar_wait(check(b), (x >> 1) & 1, s_abort) && mbar_wait(kv_full(s), (i / C::kSlots) & 1, s_abort))) break;
+        const uint4* v = reinterpret_cast<const uint4*>(ring + s * C::kSlot);
+        uint32_t hit = 0;
+#pragma unroll 8
+        for (int y = lane; y < C::kSlot / 16; y += 32) {
+          const uint4 w = v[y];
+          const uint32_t e = 0x7F807F80u, one = 0x00800080u;  // exponent 255: + 1 carries into the sign's place
+          hit |= ((w.x & e) + one) | ((w.y & e) + one) | ((w.z & e) + one) | ((w.w & e) + one);
+        }
+        const bool bad = __any_sync(~0u, hit & 0x80008000u);
+        if (lane == 0) {
+          s_bad[b] = bad;
+          mbar_arrive(checked(b));
+        }
+      }
+    }
+    } else {
+      // ------------------------------------------------------------------ softmax of row tile a
+      if (NT == 2) regs_for_softmax();
+      const int a = warp / 4, row = threadIdx.x & 127;
+      const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
+      const int pos = a * Ppt + row / G, head = kvh * G + row % G;
+      const bool valid = row < Ppt * G && pos < it.n_pos;
+      // keys this row sees (rows of no position: all, so that they add no compares)
+      const int seen = !valid ? nj * BN : p.causal ? min(max(it.pos0 + pos + 1 + it.off, 0), it.lk) : it.lk;
+      const float c = p.scale * kLog2e, grown = kRescaleLog2 / c;
+      float m = -INFINITY, mc = 0.f, l = 0.f;  // mc = c m, 0 while m = -inf
+      bool ok = true;
+      for (int j = 0; j < nj; ++j) {
+        const int n = j * NT + a;
+        const uint32_t st = lanes + (n & 1) * BN, ot = lanes + C::kOCol + a * D;
+        if (!(ok = __all_sync(~0u, mbar_wait(s_full(n & 1), (n >> 1) & 1, s_abort)))) break;
+        tc_fence_after();
+        float s[BN];
+#pragma unroll
+        for (int i = 0; i < BN; i += 32) tmem_ld32(st + i, s + i);
+        tmem_wait_ld();
+        const int lim = seen - j * BN;
+        if (!__all_sync(~0u, lim >= BN)) {
+#pragma unroll
+          for (int i = 0; i < BN; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+        }
+        float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < BN; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i]);
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        if (j == 0) {
+          m = mx;
+          mc = m == -INFINITY ? 0.f : m * c;
+        } else if (__any_sync(~0u, mx > m + grown)) {
+          const float m2 = fmaxf(m, mx), mc2 = m2 == -INFINITY ? 0.f : m2 * c;
+          const float f = m == -INFINITY ? 0.f : ex2(mc - mc2);
+          m = m2;
+          mc = mc2;
+          l *= f;
+          if (!(ok = __all_sync(~0u, mbar_wait(pv_done(a), (j - 1) & 1, s_abort)))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < D; i += 32) {
+            float o[32];
+            tmem_ld32(ot + i, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] *= f;
+            tmem_st32(ot + i, reinterpret_cast<uint32_t*>(o));
+          }
+        }
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < BN; i += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const float p0 = ex2(fmaf(s[i + x], c, -mc)), p1 = ex2(fmaf(s[i + x + 1], c, -mc));
+            l4[x & 2] += p0;
+            l4[(x & 2) + 1] += p1;
+            w[x / 2] = bf16x2_rn(p0, p1);
+          }
+          tmem_st16(st + i / 2, w);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        tmem_wait_st();
+        if (j >= j_masked) {
+          const int x = j - j_masked;
+          if (!(ok = __all_sync(~0u, mbar_wait(checked(x & 1), (x >> 1) & 1, s_abort)))) break;
+          if (s_bad[x & 1]) {
+            const int i = v_idx(j);
+            ok = mbar_wait(kv_full(i % C::kSlots), (i / C::kSlots) & 1, s_abort) &&
+                 (j == 0 || mbar_wait(pv_done(a), (j - 1) & 1, s_abort));
+            if (!(ok = __all_sync(~0u, ok))) break;
+            tc_fence_after();
+            add_seen<D, BN>(ot, st, ring + (i % C::kSlots) * C::kSlot, lim, j == 0);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready(n & 1));
+      }
+      if (nj && ok) ok = __all_sync(~0u, mbar_wait(pv_done(a), (nj - 1) & 1, s_abort));
+      if (ok) {
+        tc_fence_after();
+        const bool none = nj == 0 || l == 0.f;
+        const float inv = none ? 0.f : 1.f / l;
+        const int64_t t = it.q_row + pos;
+        uint16_t* out = p.o + (t * p.hq + head) * D;
+#pragma unroll
+        for (int i = 0; i < D; i += 32) {
+          float o[32];
+          if (nj) {
+            tmem_ld32(lanes + C::kOCol + a * D + i, o);
+            tmem_wait_ld();
+          }
+          if (valid) {
+#pragma unroll
+            for (int x = 0; x < 32; x += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[y] = none ? 0u : bf16x2_rn(o[x + 2 * y] * inv, o[x + 2 * y + 1] * inv);
+              *reinterpret_cast<uint4*>(out + i + x) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (valid && p.lse) p.lse[t * p.hq + head] = none ? -INFINITY : mc * kLn2 + logf(l);
+      }
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* op = reinterpret_cast<uint32_t*>(p.o + ((int64_t)t * p.hq + h) * D);
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    uint32_t w;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(l == 0.f ? 0.f : acc[2 * i + 1] * inv),
-        "f"(l == 0.f ? 0.f : acc[2 * i] * inv));
-    op[lane + 32 * i] = w;
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
-  if (p.lse && lane == 0) p.lse[(int64_t)t * p.hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+  if (threadIdx.x == 0 && *s_abort) set_device_status(p.hdr, MOE_ERR_DEVICE_TIMEOUT);
+}
+
+// [tokens, heads, d] rows as (d, heads, tokens); one box is 64 values x box_heads x box_tokens.
+bool make_map(CUtensorMap* m, const moe_heads_view& v, int d, int heads, int tokens, int box_heads, int box_tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)v.head_stride * 2, (cuuint64_t)v.token_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v.p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D, int NT>
+cudaError_t launch(const AttnPrefillParams& p, cudaStream_t s) {
+  using C = Cfg<D, NT>;
+  static cudaError_t attr = cudaFuncSetAttribute(attn_prefill_kernel<D, NT>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (attr != cudaSuccess) return attr;
+  if (NT == 2) {  // the register split waits for ever unless the launch brings what it hands out
+    static int regs = [] {
+      cudaFuncAttributes a;
+      return cudaFuncGetAttributes(&a, attn_prefill_kernel<D, NT>) == cudaSuccess ? a.numRegs : 0;
+    }();
+    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
+  const int ppt = 128 / p.group;
+  Maps maps;
+  // without keys no tile of K or V is read: any valid map will do
+  const bool keys = p.total_k > 0;
+  if (!make_map(&maps.q, p.q, D, p.hq, p.total_q, p.group, ppt) ||
+      !make_map(&maps.k, keys ? p.k : p.q, D, keys ? p.hkv : p.hq, keys ? p.total_k : p.total_q, 1, C::BN) ||
+      !make_map(&maps.v, keys ? p.v : p.q, D, keys ? p.hkv : p.hq, keys ? p.total_k : p.total_q, 1, C::BN))
+    return cudaErrorInvalidValue;
+  // every sequence has at most one ragged tile
+  const int64_t tiles = (int64_t)p.total_q / (NT * ppt) + (p.n_seqs < p.total_q ? p.n_seqs : p.total_q);
+  if (tiles * p.hkv > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  attn_prefill_kernel<D, NT><<<(unsigned)(tiles * p.hkv), C::kThreads, C::kSmem, s>>>(p, maps);
+  return cudaGetLastError();
+}
+
+int num_sms() {
+  static int n = [] {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      v = 1;
+    return v > 0 ? v : 1;
+  }();
+  return n;
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int d, cudaStream_t s) {
-  const dim3 grid(p.total_q, (p.hq + kWarps - 1) / kWarps);
-  if (d == 64) attn_prefill_kernel<64><<<grid, 32 * kWarps, 0, s>>>(p);
-  if (d == 128) attn_prefill_kernel<128><<<grid, 32 * kWarps, 0, s>>>(p);
-  if (d == 256) attn_prefill_kernel<256><<<grid, 32 * kWarps, 0, s>>>(p);
-  return cudaGetLastError();
+  // two row tiles per CTA halve the K and V traffic; one fills the GPU with half the rows
+  const bool two = (int64_t)p.total_q / (2 * (128 / p.group)) * p.hkv >= num_sms();
+  if (d == 64) return two ? launch<64, 2>(p, s) : launch<64, 1>(p, s);
+  if (d == 128) return two ? launch<128, 2>(p, s) : launch<128, 1>(p, s);
+  return launch<256, 1>(p, s);
 }
 
 }  // namespace moe
