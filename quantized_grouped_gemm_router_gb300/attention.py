@@ -11,7 +11,7 @@ import math
 
 import torch
 
-from .binding import MoeError, _check, _check_dev, _stream, c_int32, c_size_t, c_void_p, lib
+from .binding import MoeError, _check, _check_dev, c_int32, c_size_t, c_void_p, lib
 
 KV_BF16, KV_E4M3 = 0, 1
 
@@ -52,6 +52,12 @@ def _fn(name: str):
     return f
 
 
+def _stream(t: torch.Tensor) -> int:
+    """The current stream of t's device, as a handle (without building a torch.cuda.Stream, which
+    costs as much as a kernel launch)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def attn_workspace_bytes(dims: AttnDims) -> int:
     return int(_fn("moe_attn_workspace_bytes")(ctypes.byref(dims)))
 
@@ -89,9 +95,10 @@ def _lse(lse: torch.Tensor | None, rows: int, heads: int) -> int | None:
     return lse.data_ptr()
 
 
-def _out(o: torch.Tensor | None, rows: int, heads: int, d: int, device) -> torch.Tensor:
+def _out(o: torch.Tensor | None, q: torch.Tensor) -> torch.Tensor:
     if o is None:
-        return torch.empty((rows, heads, d), dtype=torch.int16, device=device)
+        return torch.empty_like(q, memory_format=torch.contiguous_format)
+    rows, heads, d = q.shape
     if o.dtype is not torch.int16 or not o.is_cuda or not o.is_contiguous() or o.shape != (rows, heads, d):
         raise ValueError(f"o must be a contiguous CUDA int16 tensor [{rows}, {heads}, {d}]")
     return o
@@ -109,11 +116,11 @@ def attn_prefill(dims: AttnDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     tq, tk, n = q.shape[0], k.shape[0], cu_q.numel() - 1
     if v.shape[0] != tk:
         raise ValueError("k and v must have the same number of rows")
-    o = _out(o, tq, hq, d, q.device)
+    o = _out(o, q)
     _check(_fn("moe_attn_prefill")(ctypes.byref(dims), qv, kv, vv, _ints(cu_q, None, "cu_q"),
                                    _ints(cu_k, n + 1, "cu_k"), n, tq, tk,
                                    1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, o.data_ptr(),
-                                   _lse(lse, tq, hq), ws.data_ptr(), ws.numel(), _stream()), "moe_attn_prefill")
+                                   _lse(lse, tq, hq), ws.data_ptr(), ws.numel(), _stream(q)), "moe_attn_prefill")
     return o
 
 
@@ -176,7 +183,7 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor
         raise ValueError("k and v must have the same number of rows")
     _check(_fn("moe_kv_append")(ctypes.byref(cache._c), kv, vv, _ints(cu, n + 1, "cu"), _ints(start, n, "start"),
                                 _table(page_table, n), page_table.shape[1], n, total, ws.data_ptr(), ws.numel(),
-                                _stream()), "moe_kv_append")
+                                _stream(k)), "moe_kv_append")
 
 
 def attn_decode(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, page_table: torch.Tensor, ws: torch.Tensor, *,
@@ -187,9 +194,9 @@ def attn_decode(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, page_table:
     dims = cache.dims
     hq, d, n = dims.n_q_heads, dims.head_dim, q.shape[0]
     qv = _view(q, hq, d, "q")
-    o = _out(o, n, hq, d, q.device)
+    o = _out(o, q)
     _check(_fn("moe_attn_decode")(ctypes.byref(cache._c), qv, _ints(lens, n, "lens"), _table(page_table, n),
                                   page_table.shape[1], n, 1.0 / math.sqrt(d) if scale is None else scale,
-                                  o.data_ptr(), _lse(lse, n, hq), ws.data_ptr(), ws.numel(), _stream()),
+                                  o.data_ptr(), _lse(lse, n, hq), ws.data_ptr(), ws.numel(), _stream(q)),
            "moe_attn_decode")
     return o

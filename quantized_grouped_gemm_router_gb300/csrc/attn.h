@@ -52,9 +52,27 @@ struct AttnDecodeParams {
   uint16_t* o;
   float* lse;
   WsHeader* hdr;
+  int* counters;   // [kAttnMaxCtas] arrivals at the head that begins in a CTA; zero between calls
+  float* parts;    // [kAttnMaxCtas][2] partial results of a CTA: 16 rows of d + 8 values, 16 m, 16 l
+  float* scratch;  // [kAttnMaxCtas * kAttnMaxWarps] partial rows of a warp
 };
 
-inline size_t attn_ws_bytes(const moe_attn_dims&) { return sizeof(WsHeader); }
+// Workspace of the attention calls: status word, join counters, partial results of the decode. The
+// counters lie at one place for every head layout, and each call leaves them at zero.
+constexpr int kAttnMaxCtas = 256;
+constexpr int kAttnMaxWarps = 8;
+struct AttnWs {
+  size_t counters, parts, scratch, total;
+};
+inline AttnWs attn_ws(const moe_attn_dims& d) {
+  AttnWs w;
+  const size_t rows = (size_t)16 * (d.head_dim + 8) * 4;
+  w.counters = sizeof(WsHeader);
+  w.parts = w.counters + kAttnMaxCtas * 4;
+  w.scratch = w.parts + (size_t)kAttnMaxCtas * 2 * (rows + 128);
+  w.total = w.scratch + (size_t)kAttnMaxCtas * kAttnMaxWarps * rows;
+  return w;
+}
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int d, cudaStream_t s);
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t s);

@@ -29,7 +29,7 @@ int check_view(const moe_heads_view& v, int d) {
 int check_attn_ws(void* ws, size_t ws_bytes, const moe_attn_dims& d) {
   if (!ws) return MOE_ERR_INVALID_ARG;
   if (!aligned(ws, 128)) return MOE_ERR_MISALIGNED;
-  return ws_bytes < attn_ws_bytes(d) ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+  return ws_bytes < attn_ws(d).total ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
 int check_seqs(int n_seqs) {
@@ -59,7 +59,7 @@ using namespace moe;
 extern "C" {
 
 size_t moe_attn_workspace_bytes(const moe_attn_dims* dims) {
-  return check_attn_dims(dims) == MOE_OK ? attn_ws_bytes(*dims) : 0;
+  return check_attn_dims(dims) == MOE_OK ? attn_ws(*dims).total : 0;
 }
 
 int moe_attn_prefill(const moe_attn_dims* dims, moe_heads_view q, moe_heads_view k, moe_heads_view v,
@@ -156,7 +156,12 @@ int moe_attn_decode(const moe_kv_cache* cache, moe_heads_view q, const int32_t* 
   p.scale = scale;
   p.o = o;
   p.lse = lse;
-  p.hdr = static_cast<WsHeader*>(ws);
+  const AttnWs w = attn_ws(cache->dims);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  p.hdr = reinterpret_cast<WsHeader*>(base);
+  p.counters = reinterpret_cast<int*>(base + w.counters);
+  p.parts = reinterpret_cast<float*>(base + w.parts);
+  p.scratch = reinterpret_cast<float*>(base + w.scratch);
   return launch_attn_decode(p, cache->dims.head_dim, cache->format == MOE_KV_E4M3, stream) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
