@@ -37,6 +37,26 @@ struct KvAppendParams {
   WsHeader* hdr;
 };
 
+// Division by an invariant: n / d = (t + ((n - t) >> s1)) >> s2 with t = the high half of m n, for every
+// 32-bit n (Granlund and Montgomery, Division by Invariant Integers using Multiplication).
+struct FastDiv {
+  uint32_t m;
+  int s1, s2;
+  explicit FastDiv(uint32_t d = 1) {
+    int l = 0;
+    while (((uint64_t)1 << l) < d) ++l;
+    m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1);
+    s1 = l < 1 ? l : 1;
+    s2 = l > 1 ? l - 1 : 0;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    const uint32_t t = __umulhi(m, n);
+    return (t + ((n - t) >> s1)) >> s2;
+  }
+#endif
+};
+
 struct AttnDecodeParams {
   moe_heads_view q;
   const void* kc;
@@ -48,27 +68,27 @@ struct AttnDecodeParams {
   int table_width, n_seqs;
   int hq, hkv, group;
   int page_size, n_pages;
+  FastDiv page_div;
   float scale;
   uint16_t* o;
   float* lse;
   WsHeader* hdr;
-  int* counters;   // [kAttnMaxCtas] arrivals at the head that begins in a CTA; zero between calls
-  float* parts;    // [kAttnMaxCtas][2] partial results of a CTA: 16 rows of d + 8 values, 16 m, 16 l
+  int4* splits;    // [kAttnMaxCtas] the head that begins in a CTA and ends in a later one: sequence, unit, CTAs (0: none)
+  float* parts;    // [kAttnMaxCtas][2] partial results of a CTA: 16 rows of d + 4 values, 16 m, 16 l
   float* scratch;  // [kAttnMaxCtas * kAttnMaxWarps] partial rows of a warp
 };
 
-// Workspace of the attention calls: status word, join counters, partial results of the decode. The
-// counters lie at one place for every head layout, and each call leaves them at zero.
+// Workspace of the attention calls: status word, then what the decode's two kernels hand over.
 constexpr int kAttnMaxCtas = 256;
 constexpr int kAttnMaxWarps = 8;
 struct AttnWs {
-  size_t counters, parts, scratch, total;
+  size_t splits, parts, scratch, total;
 };
 inline AttnWs attn_ws(const moe_attn_dims& d) {
   AttnWs w;
-  const size_t rows = (size_t)16 * (d.head_dim + 8) * 4;
-  w.counters = sizeof(WsHeader);
-  w.parts = w.counters + kAttnMaxCtas * 4;
+  const size_t rows = (size_t)16 * (d.head_dim + 4) * 4;
+  w.splits = sizeof(WsHeader);
+  w.parts = w.splits + kAttnMaxCtas * sizeof(int4);
   w.scratch = w.parts + (size_t)kAttnMaxCtas * 2 * (rows + 128);
   w.total = w.scratch + (size_t)kAttnMaxCtas * kAttnMaxWarps * rows;
   return w;

@@ -138,6 +138,10 @@ int moe_attn_decode(const moe_kv_cache* cache, moe_heads_view q, const int32_t* 
     return MOE_ERR_INVALID_ARG;
   if (!aligned(lens, 4) || !aligned(page_table, 4) || !aligned(lse, 4) || !aligned(o, 16)) return MOE_ERR_MISALIGNED;
   if ((st = check_attn_ws(ws, ws_bytes, cache->dims)) || (st = check_view(q, cache->dims.head_dim))) return st;
+  // the kernel numbers the 16-row tiles of all sequences and heads in 31 bits
+  const int64_t units = cache->dims.n_kv_heads * ((cache->dims.n_q_heads / cache->dims.n_kv_heads + 15) / 16);
+  if (((int64_t)table_width * cache->page_size + 15) / 16 >= ((int64_t)1 << 31) / (units * n_seqs))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
   AttnDecodeParams p;
   p.q = q;
   p.kc = cache->k;
@@ -153,13 +157,14 @@ int moe_attn_decode(const moe_kv_cache* cache, moe_heads_view q, const int32_t* 
   p.group = p.hq / p.hkv;
   p.page_size = cache->page_size;
   p.n_pages = cache->n_pages;
+  p.page_div = FastDiv(cache->page_size);
   p.scale = scale;
   p.o = o;
   p.lse = lse;
   const AttnWs w = attn_ws(cache->dims);
   uint8_t* base = static_cast<uint8_t*>(ws);
   p.hdr = reinterpret_cast<WsHeader*>(base);
-  p.counters = reinterpret_cast<int*>(base + w.counters);
+  p.splits = reinterpret_cast<int4*>(base + w.splits);
   p.parts = reinterpret_cast<float*>(base + w.parts);
   p.scratch = reinterpret_cast<float*>(base + w.scratch);
   return launch_attn_decode(p, cache->dims.head_dim, cache->format == MOE_KV_E4M3, stream) == cudaSuccess

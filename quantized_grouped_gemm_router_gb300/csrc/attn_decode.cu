@@ -8,15 +8,18 @@
 //    per SM, whatever the lengths. A warp carries a running softmax (m, l, O in registers) through a
 //    sequence's tiles; a sequence that it holds from its first to its last tile it finishes itself.
 //    The other partial results are joined by weight 2^(m - max m), in tile order: those of one CTA
-//    through shared memory, those of several CTAs through the workspace, by the CTA that finishes last.
+//    through shared memory, those of several CTAs by a second kernel, one CTA per head, which is
+//    launched early (programmatic dependent launch) and waits for the first.
 //  * Loads in flight. Each warp has a ring of its own, filled by 16-byte asynchronous copies two tiles
 //    ahead (8 warps x 2 x 8 KB per SM), with no barrier between warps. The page numbers of a tile are
 //    read one tile earlier still. Rows past a sequence's end are filled with zeros, so what lies there
 //    is never used.
 //
-// The products run on mma.sync (16 heads x 8 keys x 16): a group's heads fill at most 16 rows, and the
-// matrix work is a small share of the copy's time. In e4m3 the codes become fp16 (exactly), the query
-// row fp16 times a power of two, and the softmax weights fp16; in bf16 all operands are bf16.
+// The products run on mma.sync with the cache as the 16-row operand and the heads as the 8 columns: S^T =
+// K Q^T (16 keys x 8 heads), O^T = V^T P^T (16 values x 8 heads), P^T turned by movmatrix. A group of up
+// to 8 heads thus wastes no rows; up to 16 heads take two column blocks over the same fragments of K
+// and V. In e4m3 the codes become fp16 (exactly), the query row fp16 times a power of two, and the
+// softmax weights fp16; in bf16 all operands are bf16.
 #include <cuda_fp8.h>
 
 #include "attn_device.cuh"
@@ -29,17 +32,18 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;  // O is scaled down when a maximum has grown by more than 2^8
 constexpr int kMaxGroups = kAttnMaxSeqs / 32;
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NH>
 struct Cfg {
   static constexpr int RB = D * (E4M3 ? 1 : 2);     // bytes of a cache row
   static constexpr int TR = RB <= 128 ? 32 : 16;    // rows of a tile
   static constexpr int NW = RB == 512 ? 4 : 8;      // warps
   static constexpr int kTile = 2 * TR * RB;         // K rows, then V rows
-  static constexpr int kStages = kTile == 4096 ? 4 : 3;
+  static constexpr int kStages = 192 * 1024 / (NW * kTile);
   static constexpr int kRing = kStages * kTile;     // per warp
-  static constexpr int kStride = D + 8;             // floats between the heads of a partial O (bank spread)
+  static constexpr int kStride = D + 4;             // floats between the heads of a partial O (bank spread)
+  static constexpr int kPart = 16 * kStride + 32;   // floats of a CTA's partial result: O, then 16 m and 16 l
   static constexpr int kSmem = NW * kRing;
-  static_assert(16 * kStride * 4 <= kRing, "a partial O fits its warp's ring");
+  static_assert(8 * NH * kStride * 4 <= kRing, "a partial O fits its warp's ring");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
@@ -70,21 +74,23 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
 }
-// c += a b; bf16 or fp16 operands. HALF: rows 8..15 of a are zero and their sums are not kept.
-template <bool FP16, bool HALF>
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  float x = 0.f, y = 0.f;
-  float& c2 = HALF ? x : c[2];
-  float& c3 = HALF ? y : c[3];
-  const uint32_t a1 = HALF ? 0u : a[1], a2 = HALF ? a[1] : a[2], a3 = HALF ? 0u : a[3];
+// c += a b; bf16 or fp16 operands.
+template <bool FP16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t (&b)[2]) {
   if (FP16)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c2), "+f"(c3)
-                 : "r"(a[0]), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
   else
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c2), "+f"(c3)
-                 : "r"(a[0]), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+}
+// Transposes an 8 x 8 matrix of 16-bit values, one row's pair (lane / 4; 2 (lane % 4), + 1) per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
   uint32_t w;
@@ -125,21 +131,21 @@ struct Walk {
     nt = (len + TR - 1) / TR;
   }
   // the tile `at` (counted from the group's first)
-  __device__ __forceinline__ void start(const AttnDecodeParams& p, int g, int64_t at, int units) {
+  __device__ __forceinline__ void start(const AttnDecodeParams& p, int g, int at, int units) {
     group(p, g);
     const int lane = threadIdx.x & 31;
     const int tiles = (len32 + TR - 1) / TR;
-    int64_t sum = (int64_t)tiles * units;
+    int sum = tiles * units;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-      const int64_t y = __shfl_up_sync(~0u, sum, x);
+      const int y = __shfl_up_sync(~0u, sum, x);
       if (lane >= x) sum += y;
     }
     const int src = __ffs(__ballot_sync(~0u, sum > at)) - 1;
-    const int64_t before = __shfl_sync(~0u, sum - (int64_t)tiles * units, src);
+    at -= __shfl_sync(~0u, sum - tiles * units, src);
     seq(src);
-    u = (int)((at - before) / nt);
-    t = (int)((at - before) % nt);
+    u = at / nt;
+    t = at % nt;
   }
   __device__ __forceinline__ void next(const AttnDecodeParams& p, int units) {
     if (++t < nt) return;
@@ -156,75 +162,78 @@ struct Walk {
   }
 };
 
-// One partial result: rows of O (unnormalised), their maxima (log2, scaled) and sums.
-struct Part {
-  const float* o;
-  const float* ml;  // [16] m, [16] l
-};
-
+// A partial result of a warp: of the tiles of unit u of sequence b, which are nt tiles from number
+// `begin` of all on; whether the first and the last of them are in it.
 struct PartInfo {
-  int64_t seg;  // b * units + u, -1: none
-  int first, last, len;
+  int b, u, begin, nt, first, last;  // b = -1: none
   const float* o;
 };
 
-// Joins n partial results into the final rows of (b, u), or into another partial result (to != nullptr,
-// to_ml). All threads of the CTA; `get(i)` gives partial i, in tile order.
-template <int D, int TH, class Get>
-__device__ __forceinline__ void join(const AttnDecodeParams& p, int64_t seg, int units, int nhb, int n, Get get, float* to,
-                                     float* to_ml, int stride, float* s_w, float vscale_or) {
-  const int b = (int)(seg / units), u = (int)(seg % units), kvh = u / nhb, h0 = (u % nhb) * 16;
-  const int rows = min(16, p.group - h0);
-  // thread x: row x / (TH / 16)... every thread of a row's share computes that row's statistics itself
-  constexpr int kV = D / 4;  // float4 per row
-  for (int e = threadIdx.x; e < rows * kV; e += TH) {
-    const int r = e / kV, c = e % kV;
-    float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, get(i).ml[r]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const Part q = get(i);
-      const float w = ex2(q.ml[r] - base);
-      const float4 x = *reinterpret_cast<const float4*>(q.o + r * stride + c * 4);
-      l = fmaf(w, q.ml[16 + r], l);
-      acc.x = fmaf(w, x.x, acc.x);
-      acc.y = fmaf(w, x.y, acc.y);
-      acc.z = fmaf(w, x.z, acc.z);
-      acc.w = fmaf(w, x.w, acc.w);
-    }
-    if (to) {
-      *reinterpret_cast<float4*>(to + r * stride + c * 4) = acc;
-      if (c == 0) {
-        to_ml[r] = m;
-        to_ml[16 + r] = l;
+// Four values of one head over several partial results, with a running maximum.
+struct Sum4 {
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  // Adds the partial results first, first + step, ... below n; kBatch of them in flight. get(i): partial i.
+  template <class Get>
+  __device__ __forceinline__ void add(int first, int step, int n, Get get) {
+    constexpr int kBatch = 8;
+    for (int i0 = first; i0 < n; i0 += step * kBatch) {
+      float4 x[kBatch];
+      float xm[kBatch], xl[kBatch], top = m;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = i0 + i * step;
+        get(min(j, n - 1), x[i], xm[i], xl[i]);
+        if (j >= n) xm[i] = -INFINITY;
       }
-    } else {
-      const int64_t row = (int64_t)b * p.hq + kvh * p.group + h0 + r;
-      const float inv = l == 0.f ? 0.f : vscale_or / l;
-      const bool none = l == 0.f;
-      *reinterpret_cast<uint2*>(p.o + row * D + c * 4) =
-          none ? make_uint2(0u, 0u) : make_uint2(bf16x2_rn(acc.x * inv, acc.y * inv), bf16x2_rn(acc.z * inv, acc.w * inv));
-      if (c == 0 && p.lse) p.lse[row] = none ? -INFINITY : m * kLn2 + logf(l);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, xm[i]);
+      const float base = top == -INFINITY ? 0.f : top;
+      scale(ex2(m - base));
+      m = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) take(ex2(xm[i] - base), x[i], xl[i]);  // weight 0 past the last
     }
   }
-}
+  __device__ __forceinline__ void scale(float f) {
+    l *= f;
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+  }
+  __device__ __forceinline__ void take(float w, const float4& x, float xl) {
+    l = fmaf(w, xl, l);
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
+  }
+  // The final four values, at c * 4 of output row `row`.
+  template <int D>
+  __device__ __forceinline__ void finish(const AttnDecodeParams& p, int64_t row, int c, float v_scale) const {
+    const bool none = l == 0.f;
+    const float inv = v_scale / l;
+    *reinterpret_cast<uint2*>(p.o + row * D + c * 4) =
+        none ? make_uint2(0u, 0u) : make_uint2(bf16x2_rn(acc.x * inv, acc.y * inv), bf16x2_rn(acc.z * inv, acc.w * inv));
+    if (c == 0 && p.lse) p.lse[row] = none ? -INFINITY : m * kLn2 + logf(l);
+  }
+};
 
-template <int D, bool E4M3, bool HALF>
-__global__ void __launch_bounds__(32 * Cfg<D, E4M3>::NW, 1) attn_decode_kernel(const __grid_constant__ AttnDecodeParams p) {
-  using C = Cfg<D, E4M3>;
-  constexpr int RB = C::RB, TR = C::TR, NW = C::NW, TH = 32 * NW, NB = TR / 8, ND = D / 8;
-  constexpr int AR = HALF ? 2 : 4, CR = HALF ? 2 : 4;  // registers of an A and a C fragment
+template <int D, bool E4M3, int NH>
+__global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kernel(const __grid_constant__ AttnDecodeParams p) {
+  using C = Cfg<D, E4M3, NH>;
+  constexpr int RB = C::RB, TR = C::TR, NW = C::NW, TH = 32 * NW;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_before[kMaxGroups + 1];  // tiles before each group of 32 sequences
-  __shared__ PartInfo s_part[NW][2];
-  __shared__ float s_ml[NW][2][32];
-  __shared__ int s_last;
+  __shared__ int s_before[kMaxGroups + 1];  // tiles before each group of 32 sequences
+  __shared__ PartInfo s_part[2 * NW];
+  __shared__ float s_ml[2 * NW][32];
+  __shared__ int s_order[2 * NW];  // the partial results there are, in tile order
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int nhb = (p.group + 15) / 16, units = p.hkv * nhb;
+  pdl_launch_dependents();
 
   // ---- the tiles of all sequences
   const int groups = (p.n_seqs + 31) / 32;
@@ -232,49 +241,52 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3>::NW, 1) attn_decode_kernel(c
     const int b = g * 32 + lane;
     const int n = Walk<TR>::length(p, b);
     if (blockIdx.x == 0 && b < p.n_seqs && n != __ldg(p.lens + b)) raise_bad_index(p.hdr);
-    int64_t tiles = (n + TR - 1) / TR;
+    // rows of empty sequences, the CTAs in turn
+    unsigned none = __ballot_sync(~0u, b < p.n_seqs && n == 0 && b % gridDim.x == blockIdx.x);
+    for (; none; none &= none - 1) {
+      const int64_t e = g * 32 + __ffs(none) - 1;
+      for (int x = lane; x < p.hq * (D / 8); x += 32)
+        *reinterpret_cast<uint4*>(p.o + e * p.hq * D + x * 8) = make_uint4(0, 0, 0, 0);
+      if (p.lse)
+        for (int h = lane; h < p.hq; h += 32) p.lse[e * p.hq + h] = -INFINITY;
+    }
+    int tiles = (n + TR - 1) / TR;
 #pragma unroll
     for (int x = 16; x; x >>= 1) tiles += __shfl_xor_sync(~0u, tiles, x);
     if (lane == 0) s_before[g + 1] = tiles * units;
   }
-  // rows of empty sequences
-  for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x) {
-    if (Walk<TR>::length(p, b) > 0) continue;
-    for (int e = threadIdx.x; e < p.hq * (D / 8); e += TH)
-      *reinterpret_cast<uint4*>(p.o + (int64_t)b * p.hq * D + e * 8) = make_uint4(0, 0, 0, 0);
-    if (p.lse)
-      for (int h = threadIdx.x; h < p.hq; h += TH) p.lse[(int64_t)b * p.hq + h] = -INFINITY;
-  }
-  if (threadIdx.x < NW * 2) s_part[threadIdx.x / 2][threadIdx.x & 1].seg = -1;
+  if (threadIdx.x < 2 * NW) s_part[threadIdx.x].b = -1;
+  if (threadIdx.x == 0) s_before[0] = 0;
   __syncthreads();
-  if (warp == 0) {  // inclusive sums, four groups per lane
-    int64_t v[kMaxGroups / 32], sum = 0;
+  if (groups > 1) {
+    if (warp == 0) {  // inclusive sums, kMaxGroups / 32 groups per lane
+      int v[kMaxGroups / 32], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kMaxGroups / 32; ++i) {
-      const int g = lane * (kMaxGroups / 32) + i;
-      sum += g < groups ? s_before[g + 1] : 0;
-      v[i] = sum;
-    }
-    int64_t inc = sum;
+      for (int i = 0; i < kMaxGroups / 32; ++i) {
+        const int g = lane * (kMaxGroups / 32) + i;
+        sum += g < groups ? s_before[g + 1] : 0;
+        v[i] = sum;
+      }
+      int inc = sum;
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const int64_t y = __shfl_up_sync(~0u, inc, x);
-      if (lane >= x) inc += y;
-    }
+      for (int x = 1; x < 32; x <<= 1) {
+        const int y = __shfl_up_sync(~0u, inc, x);
+        if (lane >= x) inc += y;
+      }
 #pragma unroll
-    for (int i = 0; i < kMaxGroups / 32; ++i) {
-      const int g = lane * (kMaxGroups / 32) + i;
-      if (g < groups) s_before[g + 1] = inc - sum + v[i];
+      for (int i = 0; i < kMaxGroups / 32; ++i) {
+        const int g = lane * (kMaxGroups / 32) + i;
+        if (g < groups) s_before[g + 1] = inc - sum + v[i];
+      }
     }
-    if (lane == 0) s_before[0] = 0;
+    __syncthreads();
   }
-  __syncthreads();
-  const int64_t total = s_before[groups];
-  const int64_t ctas = min((int64_t)gridDim.x, (total + NW - 1) / NW);  // a tile per warp at least
-  if (blockIdx.x >= ctas) return;
-  const int64_t cta_lo = total * blockIdx.x / ctas, cta_hi = total * (blockIdx.x + 1) / ctas;
-  const int64_t lo = cta_lo + (cta_hi - cta_lo) * warp / NW, hi = cta_lo + (cta_hi - cta_lo) * (warp + 1) / NW;
+  const unsigned total = s_before[groups];
+  const unsigned per = max((total + gridDim.x * NW - 1) / (gridDim.x * NW), 1u);  // tiles per warp
+  const unsigned lo = min((blockIdx.x * NW + warp) * per, total), hi = min(lo + per, total);
   const int n = (int)(hi - lo);
+  if (threadIdx.x == 0) p.splits[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (blockIdx.x * NW * per >= total) return;
 
   uint8_t* ring = smem + warp * C::kRing;
   const uint32_t ring_s = smem_u32(ring);
@@ -282,41 +294,45 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3>::NW, 1) attn_decode_kernel(c
 
   if (n > 0) {
     int g = 0;
-    for (int x = lane; x < groups; x += 32) g += s_before[x + 1] <= lo;
+    for (int x = lane; x < groups; x += 32) g += s_before[x + 1] <= (int)lo;
 #pragma unroll
     for (int x = 16; x; x >>= 1) g += __shfl_xor_sync(~0u, g, x);
     Walk<TR> w, ld;
-    w.start(p, g, lo - s_before[g], units);
+    w.start(p, g, (int)lo - s_before[g], units);
     ld = w;
 
     // ---- copies: the pages of the next tile to copy are already in `page`
+    const int row = lane & (TR - 1);  // the tile row whose place this lane looks up
     const auto page_of = [&]() {
-      const int pos = ld.t * TR + (lane & (TR - 1));
-      return pos < ld.len ? __ldg(p.table + (int64_t)ld.b * p.table_width + (unsigned)pos / (unsigned)p.page_size) : -1;
+      const int pos = ld.t * TR + row;
+      return pos < ld.len ? __ldg(p.table + (int64_t)ld.b * p.table_width + p.page_div(pos)) : -1;
     };
+    constexpr int CPR = RB / 16, RPI = 32 / CPR;  // copies per row, rows per instruction
+    const auto swz = [](int r) { return RB == 64 ? (r >> 1) & 3 : r & 7; };
+    const uint32_t at0 = ring_s + (lane / CPR) * RB, at_x = ((lane % CPR) ^ swz(lane / CPR)) << 4;
+    const uint8_t* kc = static_cast<const uint8_t*>(p.kc) + (lane % CPR) * 16;
+    const uint8_t* vc = static_cast<const uint8_t*>(p.vc) + (lane % CPR) * 16;
     int page = page_of();
     int left = n;  // tiles not yet copied
     const auto issue = [&](int stage) {
       if (left > 0) {
-        const int pos = ld.t * TR + (lane & (TR - 1));
+        const int pos = ld.t * TR + row;
         int cell = -1;  // this lane's cache row
         if (pos < ld.len) {
           if (page >= 0 && page < p.n_pages)
-            cell = (page * p.hkv + ld.u / nhb) * p.page_size + (int)((unsigned)pos % (unsigned)p.page_size);
+            cell = (page * p.hkv + ld.u / nhb) * p.page_size + (pos - (int)p.page_div(pos) * p.page_size);
           else
             raise_bad_index(p.hdr);
         }
-        const uint32_t dst = ring_s + stage * C::kTile;
-        constexpr int CPR = RB / 16, RPI = 32 / CPR;  // copies per row, rows per instruction
-        const int chunk = lane % CPR;
+        const uint32_t dst = at0 + stage * C::kTile;
+        const bool all = __all_sync(~0u, cell >= 0);
 #pragma unroll
         for (int i = 0; i < TR / RPI; ++i) {
-          const int r = i * RPI + lane / CPR;
-          const int c = __shfl_sync(~0u, cell, r);
-          const int64_t off = (int64_t)max(c, 0) * RB + chunk * 16;
-          const uint32_t at = dst + r * RB + ((chunk ^ (RB == 64 ? (r >> 1) & 3 : r & 7)) << 4);
-          cp16(at, static_cast<const uint8_t*>(p.kc) + off, c >= 0);
-          cp16(at + TR * RB, static_cast<const uint8_t*>(p.vc) + off, c >= 0);
+          const int c = __shfl_sync(~0u, cell, i * RPI + lane / CPR);
+          const int64_t off = (int64_t)max(c, 0) * RB;
+          const uint32_t at = dst + i * RPI * RB + (at_x ^ (swz(i * RPI) << 4));
+          cp16(at, kc + off, all || c >= 0);
+          cp16(at + TR * RB, vc + off, all || c >= 0);
         }
         if (--left > 0) {
           ld.next(p, units);
@@ -325,42 +341,46 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3>::NW, 1) attn_decode_kernel(c
       }
       cp_commit();
     };
-#pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) issue(s);
 
-    uint32_t q[D / 16][AR];
-    float o[ND][CR];
-    float m[CR / 2], mc[CR / 2], l[CR / 2], cr[CR / 2];  // per row (lane / 4, and + 8): maximum, scaled, sum, scale
+    const int g8 = lane >> 2, t4 = lane & 3;                // fragment coordinates
+    const int slot = E4M3 ? (g8 >> 1) + 4 * (g8 & 1) : g8;  // e4m3: the key of A row g8 (spreads the row reads over the banks)
+    uint32_t q[NH][D / 16][2];
+    float o[NH][D / 16][4];
+    float m[NH][2], mc[NH][2], l[NH][2], cr[NH][2];  // of heads 2 t4, + 1: maximum, scaled, this lane's sum, scale
     bool fresh = true, from_start = false;
     int out = 0, stage = 0, fill = C::kStages - 1;
     for (int i = 0; i < n; ++i) {
       issue(fill);
       if (++fill == C::kStages) fill = 0;
-      const int kvh = w.u / nhb, h0 = (w.u % nhb) * 16, rows = min(16, p.group - h0);
+      const int kvh = w.u / nhb, h0 = (w.u % nhb) * 16, heads = min(16, p.group - h0);
       if (fresh) {
-        // ---- a new sequence or head: its query rows as A fragments
+        // ---- a new sequence or head: its query rows as B fragments
         fresh = false;
         from_start = w.t == 0;
 #pragma unroll
-        for (int x = 0; x < ND; ++x)
+        for (int nh = 0; nh < NH; ++nh) {
 #pragma unroll
-          for (int y = 0; y < CR; ++y) o[x][y] = 0.f;
+          for (int x = 0; x < D / 16; ++x)
 #pragma unroll
-        for (int y = 0; y < CR / 2; ++y) {
-          m[y] = -INFINITY;
-          mc[y] = 0.f;
-          l[y] = 0.f;
-          cr[y] = p.scale * kLog2e * (E4M3 ? __ldg(p.k_scale + kvh) : 1.f);
-          const int r = lane / 4 + 8 * y;
-          const uint16_t* src = p.q.p + (int64_t)w.b * p.q.token_stride + (int64_t)(kvh * p.group + h0 + r) * p.q.head_stride;
-          uint32_t v[D / 16][2];
+            for (int y = 0; y < 4; ++y) o[nh][x][y] = 0.f;
+          const float scale = p.scale * kLog2e * (E4M3 ? __ldg(p.k_scale + kvh) : 1.f);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            m[nh][y] = -INFINITY;
+            mc[nh][y] = 0.f;
+            l[nh][y] = 0.f;
+            cr[nh][y] = scale;
+          }
+          const int h = nh * 8 + g8;
+          const uint16_t* src = p.q.p + (int64_t)w.b * p.q.token_stride + (int64_t)(kvh * p.group + h0 + h) * p.q.head_stride;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               // bf16: k step ks holds values 16 ks + (0..15); e4m3: see the K fragments below
-              const int d = E4M3 ? (ks / 4) * 64 + (lane & 3) * 16 + (ks & 3) * 4 + half * 2 : ks * 16 + (lane & 3) * 2 + half * 8;
-              v[ks][half] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + d)) : 0u;
+              const int d = E4M3 ? (ks / 4) * 64 + t4 * 16 + (ks & 3) * 4 + half * 2 : ks * 16 + t4 * 2 + half * 8;
+              q[nh][ks][half] = h < heads ? __ldg(reinterpret_cast<const uint32_t*>(src + d)) : 0u;
             }
           if (E4M3) {
             // fp16 has bf16's precision but not its range: the row times a power of two that brings its
@@ -369,167 +389,176 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3>::NW, 1) attn_decode_kernel(c
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                big = max(big, v[ks][half] & 0x7FFFu);
-                big = max(big, (v[ks][half] >> 16) & 0x7FFFu);
-              }
+              for (int half = 0; half < 2; ++half)
+                big = max(big, max(q[nh][ks][half] & 0x7FFFu, (q[nh][ks][half] >> 16) & 0x7FFFu));
             big = max(big, __shfl_xor_sync(~0u, big, 1));
             big = max(big, __shfl_xor_sync(~0u, big, 2));
-            const int e = (int)(big >> 7) - 127;  // exponent of the largest
-            const int up = big == 0 || big >= 0x7F80u ? 0 : min(14 - e, 126);
+            const int up = big == 0 || big >= 0x7F80u ? 0 : min(14 - ((int)(big >> 7) - 127), 126);
             const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-            cr[y] *= __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-              for (int half = 0; half < 2; ++half)
-                v[ks][half] = f16x2_rn(__uint_as_float(v[ks][half] << 16) * f, __uint_as_float(v[ks][half] & 0xFFFF0000u) * f);
-          }
+              for (int half = 0; half < 2; ++half) {
+                const uint32_t v = q[nh][ks][half];
+                q[nh][ks][half] = f16x2_rn(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
+              }
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            q[ks][y] = v[ks][0];
-            q[ks][y + AR / 2] = v[ks][1];
+            for (int y = 0; y < 2; ++y)
+              cr[nh][y] *= __uint_as_float((uint32_t)(127 - __shfl_sync(~0u, up, (2 * t4 + y) * 4)) << 23);
           }
         }
       }
 
       cp_wait<C::kStages - 1>();
       __syncwarp();
-      const uint32_t ks_ = ring_s + stage * C::kTile, vs_ = ks_ + TR * RB;
+      const uint32_t kt = ring_s + stage * C::kTile, vt = kt + TR * RB;
 
-      // ---- scores. C fragment nb: rows lane / 4 (+ 8), columns 2 (lane % 4), + 1, that is keys
-      //   bf16: 8 nb + column; e4m3: 8 nb + lane % 4 and 8 nb + lane % 4 + 4 (bank spread of the row reads)
-      float s[NB][CR];
+      // ---- scores. C fragment kb: keys 16 kb + slot (values 0, 1) and + 8 (2, 3) of heads 2 t4, + 1
+      float s[TR / 16][NH][4];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float s2[CR];
+      for (int kb = 0; kb < TR / 16; ++kb) {
+        float s2[NH][4];
 #pragma unroll
-        for (int y = 0; y < CR; ++y) s[nb][y] = s2[y] = 0.f;
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s[kb][nh][y] = s2[nh][y] = 0.f;
         if (!E4M3) {
-          const int x = (lane >> 3) ^ (lane & 7);
-          const uint32_t row = ks_ + (nb * 8 + (lane & 7)) * RB;
+          const uint32_t at = kt + (kb * 16 + (lane & 15)) * RB;
+          const uint32_t x = ((lane >> 4) ^ (lane & 7)) << 4;
 #pragma unroll
-          for (int kp = 0; kp < D / 32; ++kp) {
-            uint32_t b[4];
-            ldsm4(row + ((kp * 64) ^ (x << 4)), b);
-            mma<false, HALF>(s[nb], q[2 * kp], b[0], b[1]);
-            mma<false, HALF>(s2, q[2 * kp + 1], b[2], b[3]);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t a[4];
+            ldsm4(at + ((ks * 32) ^ x), a);
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) mma<false>(ks & 1 ? s2[nh] : s[kb][nh], a[0], a[1], a[2], a[3], q[nh][ks]);
           }
         } else {
-          // a lane reads 16 codes of one key: values 64 i + 16 (lane % 4) + 0..15 serve four k steps
-          const int r = nb * 8 + (lane >> 3) + 4 * ((lane >> 2) & 1);
+          // a lane reads 16 codes of two keys: values 64 i + 16 t4 + 0..15 serve four k steps
+          const uint32_t at = kt + (kb * 16 + slot) * RB;
 #pragma unroll
           for (int i4 = 0; i4 < D / 64; ++i4) {
-            const int chunk = i4 * 4 + (lane & 3);
-            const uint4 b = lds128(ks_ + r * RB + ((chunk ^ (RB == 64 ? (r >> 1) & 3 : r & 7)) << 4));
-            mma<true, HALF>(s[nb], q[4 * i4], e4m3x2_f16<0>(b.x), e4m3x2_f16<1>(b.x));
-            mma<true, HALF>(s2, q[4 * i4 + 1], e4m3x2_f16<0>(b.y), e4m3x2_f16<1>(b.y));
-            mma<true, HALF>(s[nb], q[4 * i4 + 2], e4m3x2_f16<0>(b.z), e4m3x2_f16<1>(b.z));
-            mma<true, HALF>(s2, q[4 * i4 + 3], e4m3x2_f16<0>(b.w), e4m3x2_f16<1>(b.w));
+            const int c = i4 * 4 + t4;
+            const uint4 u = lds128(at + ((c ^ swz(slot)) << 4)), v = lds128(at + 8 * RB + ((c ^ swz(slot + 8)) << 4));
+            const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a0 = e4m3x2_f16<0>(uw[k]), a1 = e4m3x2_f16<0>(vw[k]), a2 = e4m3x2_f16<1>(uw[k]), a3 = e4m3x2_f16<1>(vw[k]);
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh) mma<true>(k & 1 ? s2[nh] : s[kb][nh], a0, a1, a2, a3, q[nh][4 * i4 + k]);
+            }
           }
         }
 #pragma unroll
-        for (int y = 0; y < CR; ++y) s[nb][y] += s2[y];
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s[kb][nh][y] += s2[nh][y];
       }
       const int lim = w.len - w.t * TR;
       if (lim < TR) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int kb = 0; kb < TR / 16; ++kb)
 #pragma unroll
-          for (int y = 0; y < CR; ++y) {
-            const int key = nb * 8 + (E4M3 ? (lane & 3) + 4 * (y & 1) : (lane & 3) * 2 + (y & 1));
-            if (key >= lim) s[nb][y] = -INFINITY;
-          }
+          for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (kb * 16 + slot + (y >> 1) * 8 >= lim) s[kb][nh][y] = -INFINITY;
       }
 
       // ---- running softmax
       bool grown = false;
-      float mx[CR / 2];
+      float mx[NH][2];
 #pragma unroll
-      for (int y = 0; y < CR / 2; ++y) {
-        mx[y] = -INFINITY;
+      for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mx[y] = fmaxf(mx[y], fmaxf(s[nb][2 * y], s[nb][2 * y + 1]));
-        mx[y] = fmaxf(mx[y], __shfl_xor_sync(~0u, mx[y], 1));
-        mx[y] = fmaxf(mx[y], __shfl_xor_sync(~0u, mx[y], 2));
-        grown |= mx[y] * cr[y] > mc[y] + kRescaleLog2 || (m[y] == -INFINITY && mx[y] > m[y]);
-      }
+        for (int y = 0; y < 2; ++y) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int kb = 0; kb < TR / 16; ++kb) x = fmaxf(x, fmaxf(s[kb][nh][y], s[kb][nh][y + 2]));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+          mx[nh][y] = x;
+          grown |= x * cr[nh][y] > mc[nh][y] + kRescaleLog2 || (m[nh][y] == -INFINITY && x > m[nh][y]);
+        }
       if (__any_sync(~0u, grown)) {
 #pragma unroll
-        for (int y = 0; y < CR / 2; ++y) {
-          const float m2 = fmaxf(m[y], mx[y]), mc2 = m2 == -INFINITY ? 0.f : m2 * cr[y];
-          const float f = m[y] == -INFINITY ? 0.f : ex2(mc[y] - mc2);
-          m[y] = m2;
-          mc[y] = mc2;
-          l[y] *= f;
+        for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-          for (int x = 0; x < ND; ++x) {
-            o[x][2 * y] *= f;
-            o[x][2 * y + 1] *= f;
+          for (int y = 0; y < 2; ++y) {
+            const float m2 = fmaxf(m[nh][y], mx[nh][y]), mc2 = m2 == -INFINITY ? 0.f : m2 * cr[nh][y];
+            const float f = m[nh][y] == -INFINITY ? 0.f : ex2(mc[nh][y] - mc2);
+            m[nh][y] = m2;
+            mc[nh][y] = mc2;
+            l[nh][y] *= f;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              o[nh][x][y] *= f;
+              o[nh][x][y + 2] *= f;
+            }
           }
-        }
       }
-      uint32_t a[TR / 16][AR];
+      uint32_t b[TR / 16][NH][2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int kb = 0; kb < TR / 16; ++kb)
 #pragma unroll
-        for (int y = 0; y < CR / 2; ++y) {
-          const float p0 = ex2(fmaf(s[nb][2 * y], cr[y], -mc[y])), p1 = ex2(fmaf(s[nb][2 * y + 1], cr[y], -mc[y]));
-          l[y] += p0 + p1;
-          a[nb / 2][(nb & 1) * (AR / 2) + y] = E4M3 ? f16x2_rn(p0, p1) : bf16x2_rn(p0, p1);
+        for (int nh = 0; nh < NH; ++nh) {
+          float e[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) e[y] = ex2(fmaf(s[kb][nh][y], cr[nh][y & 1], -mc[nh][y & 1]));
+          l[nh][0] += e[0] + e[2];
+          l[nh][1] += e[1] + e[3];
+          b[kb][nh][0] = transpose8x8(E4M3 ? f16x2_rn(e[0], e[1]) : bf16x2_rn(e[0], e[1]));
+          b[kb][nh][1] = transpose8x8(E4M3 ? f16x2_rn(e[2], e[3]) : bf16x2_rn(e[2], e[3]));
         }
 
-      // ---- O += P V. C fragment x holds columns
-      //   bf16: 8 x + 2 (lane % 4), + 1;  e4m3, D = 64: 16 (lane % 4) + x and + 8;
-      //   e4m3, D >= 128: 128 (x / 16) + 16 (lane % 4) + x % 16 and + 64
+      // ---- O^T += V^T P^T. C fragment x holds, of heads 2 t4, + 1, the values
+      //   bf16: 16 x + g8 (values 0, 1) and + 8 (2, 3);  e4m3, D = 64: 8 g8 + 2 x and + 1;
+      //   e4m3, D >= 128: 128 (x / 8) + 16 slot + 2 (x % 8) and + 1
 #pragma unroll
       for (int kb = 0; kb < TR / 16; ++kb) {
         if (!E4M3) {
-          const int x = (lane >> 4) ^ (lane & 7);
-          const uint32_t row = vs_ + (kb * 16 + (lane & 15)) * RB;
+          const uint32_t at = vt + (kb * 16 + (lane & 7) + ((lane >> 4) & 1) * 8) * RB;
+          const uint32_t x8 = (((lane >> 3) & 1) ^ (lane & 7)) << 4;
 #pragma unroll
-          for (int dp = 0; dp < ND / 2; ++dp) {
-            uint32_t b[4];
-            ldsm4t(row + ((dp * 32) ^ (x << 4)), b);
-            mma<false, HALF>(o[2 * dp], a[kb], b[0], b[1]);
-            mma<false, HALF>(o[2 * dp + 1], a[kb], b[2], b[3]);
-          }
-        } else if (D == 64) {
-          uint2 v[4];
+          for (int x = 0; x < D / 16; ++x) {
+            uint32_t a[4];
+            ldsm4t(at + ((x * 32) ^ x8), a);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int r = kb * 16 + (lane & 3) + 4 * y, chunk = lane >> 3;
-            v[y] = lds64(vs_ + r * RB + ((chunk ^ ((r >> 1) & 3)) << 4) + ((lane >> 2) & 1) * 8);
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t r0 = x ? v[0].y : v[0].x, r1 = x ? v[1].y : v[1].x, r2 = x ? v[2].y : v[2].x, r3 = x ? v[3].y : v[3].x;
-            const uint32_t e01 = __byte_perm(r0, r1, 0x5140), e23 = __byte_perm(r0, r1, 0x7362);
-            const uint32_t f01 = __byte_perm(r2, r3, 0x5140), f23 = __byte_perm(r2, r3, 0x7362);
-            mma<true, HALF>(o[4 * x], a[kb], e4m3x2_f16<0>(e01), e4m3x2_f16<0>(f01));
-            mma<true, HALF>(o[4 * x + 1], a[kb], e4m3x2_f16<1>(e01), e4m3x2_f16<1>(f01));
-            mma<true, HALF>(o[4 * x + 2], a[kb], e4m3x2_f16<0>(e23), e4m3x2_f16<0>(f23));
-            mma<true, HALF>(o[4 * x + 3], a[kb], e4m3x2_f16<1>(e23), e4m3x2_f16<1>(f23));
+            for (int nh = 0; nh < NH; ++nh) mma<false>(o[nh][x], a[0], a[1], a[2], a[3], b[kb][nh]);
           }
         } else {
+          // keys t4, t4 + 4, t4 + 8, t4 + 12 of the 16 (the places of k 2 t4, + 1, + 8, + 9)
+          const auto products = [&](int x, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {  // 4 codes of each key
 #pragma unroll
-          for (int dq = 0; dq < D / 128; ++dq) {
-            uint4 v[4];
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t u = __byte_perm(r0, r1, k ? 0x7362 : 0x5140), v = __byte_perm(r2, r3, k ? 0x7362 : 0x5140);
+              const uint32_t a0 = e4m3x2_f16<0>(u), a1 = e4m3x2_f16<1>(u), a2 = e4m3x2_f16<0>(v), a3 = e4m3x2_f16<1>(v);
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh) mma<true>(o[nh][x + k], a0, a1, a2, a3, b[kb][nh]);
+            }
+          };
+          if (D == 64) {
+            uint2 v[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const int r = kb * 16 + (lane & 3) + 4 * y, chunk = dq * 8 + (lane >> 3) + 4 * ((lane >> 2) & 1);
-              v[y] = lds128(vs_ + r * RB + ((chunk ^ (r & 7)) << 4));
+              const int r = kb * 16 + t4 + 4 * y;
+              v[y] = lds64(vt + r * RB + (((g8 >> 1) ^ swz(r)) << 4) + (g8 & 1) * 8);
             }
+            products(0, v[0].x, v[1].x, v[2].x, v[3].x);
+            products(2, v[0].y, v[1].y, v[2].y, v[3].y);
+          } else {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const auto word = [&](const uint4& y) { return x == 0 ? y.x : x == 1 ? y.y : x == 2 ? y.z : y.w; };
-              const uint32_t r0 = word(v[0]), r1 = word(v[1]), r2 = word(v[2]), r3 = word(v[3]);
-              const uint32_t e01 = __byte_perm(r0, r1, 0x5140), e23 = __byte_perm(r0, r1, 0x7362);
-              const uint32_t f01 = __byte_perm(r2, r3, 0x5140), f23 = __byte_perm(r2, r3, 0x7362);
-              mma<true, HALF>(o[dq * 16 + 4 * x], a[kb], e4m3x2_f16<0>(e01), e4m3x2_f16<0>(f01));
-              mma<true, HALF>(o[dq * 16 + 4 * x + 1], a[kb], e4m3x2_f16<1>(e01), e4m3x2_f16<1>(f01));
-              mma<true, HALF>(o[dq * 16 + 4 * x + 2], a[kb], e4m3x2_f16<0>(e23), e4m3x2_f16<0>(f23));
-              mma<true, HALF>(o[dq * 16 + 4 * x + 3], a[kb], e4m3x2_f16<1>(e23), e4m3x2_f16<1>(f23));
+            for (int dq = 0; dq < D / 128; ++dq) {
+              uint4 v[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int r = kb * 16 + t4 + 4 * y;
+                v[y] = lds128(vt + r * RB + (((dq * 8 + slot) ^ swz(r)) << 4));
+              }
+              products(dq * 8, v[0].x, v[1].x, v[2].x, v[3].x);
+              products(dq * 8 + 2, v[0].y, v[1].y, v[2].y, v[3].y);
+              products(dq * 8 + 4, v[0].z, v[1].z, v[2].z, v[3].z);
+              products(dq * 8 + 6, v[0].w, v[1].w, v[2].w, v[3].w);
             }
           }
         }
@@ -542,59 +571,67 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3>::NW, 1) attn_decode_kernel(c
       if (to_end || i == n - 1) {
         const bool whole = to_end && from_start, mid = i < n - 1;
         float* to = mid ? scratch : reinterpret_cast<float*>(ring);
-        const float vs = E4M3 && whole ? __ldg(p.v_scale + kvh) : 1.f;
         if (!whole && !mid) {
           cp_wait<0>();  // the ring is idle: every copy has landed and been used
           __syncwarp();
         }
 #pragma unroll
-        for (int y = 0; y < CR / 2; ++y) {
-          const int r = lane / 4 + 8 * y;
-          float sum = l[y];
-          sum += __shfl_xor_sync(~0u, sum, 1);
-          sum += __shfl_xor_sync(~0u, sum, 2);
-          const bool none = sum == 0.f;
-          const float inv = whole ? (none ? 0.f : vs / sum) : 1.f;
-          const int64_t row = (int64_t)w.b * p.hq + kvh * p.group + h0 + r;
-          if (r < rows) {
-            // pieces of values that lie together: 2 (bf16), 8 (e4m3)
-            if (!E4M3) {
+        for (int nh = 0; nh < NH; ++nh) {
+          float inv[2];
 #pragma unroll
-              for (int x = 0; x < ND; ++x) {
-                const float u0 = whole && none ? 0.f : o[x][2 * y] * inv, u1 = whole && none ? 0.f : o[x][2 * y + 1] * inv;
-                const int d = 8 * x + 2 * (lane & 3);
-                if (whole)
-                  *reinterpret_cast<uint32_t*>(p.o + row * D + d) = bf16x2_rn(u0, u1);
-                else
-                  *reinterpret_cast<float2*>(to + r * C::kStride + d) = make_float2(u0, u1);
-              }
-            } else {
-#pragma unroll
-              for (int z = 0; z < 2; ++z)
-#pragma unroll
-                for (int x = 0; x < ND; x += 4) {
-                  const int d = D == 64 ? 16 * (lane & 3) + 8 * z + x : 128 * (x / 16) + 16 * (lane & 3) + 64 * z + x % 16;
-                  float v[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) v[k] = whole && none ? 0.f : o[x + k][2 * y + z] * inv;
-                  if (whole)
-                    *reinterpret_cast<uint2*>(p.o + row * D + d) = make_uint2(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]));
-                  else
-                    *reinterpret_cast<float4*>(to + r * C::kStride + d) = make_float4(v[0], v[1], v[2], v[3]);
-                }
-            }
-            if ((lane & 3) == 0) {
+          for (int y = 0; y < 2; ++y) {
+            const int h = nh * 8 + 2 * t4 + y;
+            float sum = l[nh][y];
+            sum += __shfl_xor_sync(~0u, sum, 4);
+            sum += __shfl_xor_sync(~0u, sum, 8);
+            sum += __shfl_xor_sync(~0u, sum, 16);
+            inv[y] = sum == 0.f ? 0.f : (E4M3 ? __ldg(p.v_scale + kvh) : 1.f) / sum;
+            if (lane < 4 && h < heads) {
               if (!whole) {
-                s_ml[warp][out][r] = m[y] == -INFINITY ? -INFINITY : mc[y];
-                s_ml[warp][out][16 + r] = sum;
+                s_ml[warp * 2 + out][h] = m[nh][y] == -INFINITY ? -INFINITY : mc[nh][y];
+                s_ml[warp * 2 + out][16 + h] = sum;
               } else if (p.lse) {
-                p.lse[row] = none ? -INFINITY : mc[y] * kLn2 + logf(sum);
+                p.lse[(int64_t)w.b * p.hq + kvh * p.group + h0 + h] = sum == 0.f ? -INFINITY : mc[nh][y] * kLn2 + logf(sum);
               }
             }
           }
+          uint16_t* dst = p.o + ((int64_t)w.b * p.hq + kvh * p.group + h0 + nh * 8) * D;  // head 0 of this block
+          const auto scaled = [&](float x, int y) { return inv[y] == 0.f ? 0.f : x * inv[y]; };
+          if (!whole) {
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int h = nh * 8 + 2 * t4 + (y & 1);
+                const int d = !E4M3     ? 16 * x + g8 + 8 * (y >> 1)
+                              : D == 64 ? 8 * g8 + 2 * x + (y >> 1)
+                                        : 128 * (x / 8) + 16 * slot + 2 * (x % 8) + (y >> 1);
+                if (h < heads) to[h * C::kStride + d] = o[nh][x][y];
+              }
+          } else if (!E4M3) {
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                // turned: head g8, values 2 t4, + 1
+                const uint32_t v = transpose8x8(bf16x2_rn(scaled(o[nh][x][2 * z], 0), scaled(o[nh][x][2 * z + 1], 1)));
+                if (nh * 8 + g8 < heads) *reinterpret_cast<uint32_t*>(dst + g8 * D + 16 * x + 8 * z + 2 * t4) = v;
+              }
+          } else {
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int x = 0; x < D / 16; x += 4) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = bf16x2_rn(scaled(o[nh][x + k][y], y), scaled(o[nh][x + k][y + 2], y));
+                const int d = D == 64 ? 8 * g8 : 128 * (x / 8) + 16 * slot + 2 * (x % 8);
+                if (nh * 8 + 2 * t4 + y < heads) *reinterpret_cast<uint4*>(dst + (2 * t4 + y) * D + d) = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+          }
         }
         if (!whole) {
-          if (lane == 0) s_part[warp][out] = PartInfo{(int64_t)w.b * units + w.u, from_start, to_end, w.nt, to};
+          if (lane == 0) s_part[warp * 2 + out] = PartInfo{w.b, w.u, (int)lo + i - w.t, w.nt, from_start, to_end, to};
           ++out;
         }
         fresh = true;
@@ -605,71 +642,84 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3>::NW, 1) attn_decode_kernel(c
   }
   __syncthreads();
 
-  // ---- partial results of this CTA's warps, in tile order; runs of one sequence's head are joined
-  int pend = 0;
-  int64_t pend_seg[2];
-  int pend_first[2], pend_count[2];
-  for (int x = 0; x < 2 * NW;) {
-    const PartInfo a = s_part[x / 2][x & 1];
-    if (a.seg < 0) {
-      ++x;
-      continue;
+  // ---- partial results of this CTA's warps, in tile order: those of one sequence's head are joined
+  const PartInfo mine = lane < 2 * NW ? s_part[lane] : PartInfo{-1, 0, 0, 0, 0, 0, nullptr};
+  unsigned rest = __ballot_sync(~0u, mine.b >= 0);
+  if (!rest) return;
+  if (warp == 0 && mine.b >= 0) s_order[__popc(rest & ((1u << lane) - 1))] = lane;
+  __syncthreads();
+  int at = 0;
+  while (rest) {
+    const int head = __ffs(rest) - 1, b = __shfl_sync(~0u, mine.b, head), u = __shfl_sync(~0u, mine.u, head);
+    const unsigned same = __ballot_sync(~0u, mine.b == b && mine.u == u);
+    const int cnt = __popc(same), tail = 31 - __clz(same);
+    const int first = __shfl_sync(~0u, mine.first, head), last = __shfl_sync(~0u, mine.last, tail);
+    const unsigned begin = __shfl_sync(~0u, mine.begin, head), end = begin + __shfl_sync(~0u, mine.nt, head) - 1;
+    rest &= ~same;
+    const int kvh = u / nhb, h0 = (u % nhb) * 16, heads = min(16, p.group - h0);
+    float* to = p.parts + (int64_t)(blockIdx.x * 2 + (first ? 1 : 0)) * C::kPart;
+    for (int e = threadIdx.x; e < heads * (D / 4); e += TH) {
+      const int h = e / (D / 4), c = e % (D / 4);
+      Sum4 sum;
+      sum.add(0, 1, cnt, [&](int i, float4& x, float& xm, float& xl) {
+        const int y = s_order[at + i];
+        x = *reinterpret_cast<const float4*>(s_part[y].o + h * C::kStride + c * 4);
+        xm = s_ml[y][h];
+        xl = s_ml[y][16 + h];
+      });
+      if (first && last) {
+        sum.finish<D>(p, (int64_t)b * p.hq + kvh * p.group + h0 + h, c, E4M3 ? __ldg(p.v_scale + kvh) : 1.f);
+      } else {
+        *reinterpret_cast<float4*>(to + h * C::kStride + c * 4) = sum.acc;
+        if (c == 0) {
+          to[16 * C::kStride + h] = sum.m;
+          to[16 * C::kStride + 16 + h] = sum.l;
+        }
+      }
     }
-    int list[2 * NW], cnt = 0, y = x;
-    bool last = false;
-    for (; y < 2 * NW; ++y) {
-      const PartInfo b = s_part[y / 2][y & 1];
-      if (b.seg < 0) continue;
-      if (b.seg != a.seg) break;
-      list[cnt++] = y;
-      last = b.last;
-    }
-    x = y;
-    const int kvh = (int)(a.seg % units) / nhb;
-    const bool done = a.first && last;
-    float* to = p.parts + (int64_t)(blockIdx.x * 2 + (a.first ? 1 : 0)) * (16 * C::kStride + 32);
-    join<D, TH>(p, a.seg, units, nhb, cnt,
-                [&](int i) {
-                  const int z = list[i];
-                  return Part{s_part[z / 2][z & 1].o, s_ml[z / 2][z & 1]};
-                },
-                done ? nullptr : to, to + 16 * C::kStride, C::kStride, nullptr,
-                E4M3 ? __ldg(p.v_scale + kvh) : 1.f);
-    if (!done) {
-      // the CTAs that hold tiles of this head: its first tile is number `begin` of all
-      const int b = (int)(a.seg / units), u = (int)(a.seg % units);
-      int64_t begin = s_before[b / 32];
-      for (int z = b & ~31; z < b; ++z) begin += (int64_t)((Walk<TR>::length(p, z) + TR - 1) / TR) * units;
-      begin += (int64_t)u * a.len;
-      const int64_t end = begin + a.len - 1;
-      const int c0 = (int)(((begin + 1) * ctas - 1) / total), c1 = (int)(((end + 1) * ctas - 1) / total);
-      pend_seg[pend] = a.seg;
-      pend_first[pend] = c0;
-      pend_count[pend] = c1 - c0 + 1;
-      ++pend;
-    }
+    at += cnt;
+    // a head that begins here and goes on in the next CTAs, up to the one that holds its last tile
+    if (threadIdx.x == 0 && first && !last) p.splits[blockIdx.x] = make_int4(b, u, (int)(end / (per * NW)) - blockIdx.x + 1, 0);
   }
-  if (pend == 0) return;
-  __threadfence();
-  for (int x = 0; x < pend; ++x) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      __threadfence();
-      const int ticket = atomicAdd(p.counters + pend_first[x], 1);
-      s_last = ticket == pend_count[x] - 1;
-      if (s_last) p.counters[pend_first[x]] = 0;  // every CTA of this head has been here
-      __threadfence();
-    }
-    __syncthreads();
-    if (!s_last) continue;
-    const int kvh = (int)(pend_seg[x] % units) / nhb, c0 = pend_first[x];
-    join<D, TH>(p, pend_seg[x], units, nhb, pend_count[x],
-                [&](int i) {
-                  const float* at = p.parts + (int64_t)((c0 + i) * 2 + (i == 0 ? 1 : 0)) * (16 * C::kStride + 32);
-                  return Part{at, at + 16 * C::kStride};
-                },
-                nullptr, nullptr, C::kStride, nullptr, E4M3 ? __ldg(p.v_scale + kvh) : 1.f);
+}
+
+// Joins the partial results of the head that begins in CTA blockIdx.x of the kernel above, for query head
+// blockIdx.y of its unit: 256 threads walk the partials D / 4 threads to one.
+template <int D, bool E4M3, int NH>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnDecodeParams p) {
+  using C = Cfg<D, E4M3, NH>;
+  constexpr int V = D / 4, R = 256 / V;
+  __shared__ float4 s_acc[R][V];
+  __shared__ float s_ml[R][2];
+  pdl_wait();
+  const int4 split = p.splits[blockIdx.x];
+  const int n = split.z;
+  if (n == 0) return;
+  const int nhb = (p.group + 15) / 16, kvh = split.y / nhb, h0 = (split.y % nhb) * 16, h = blockIdx.y;
+  if (h >= min(16, p.group - h0)) return;
+  const int r = threadIdx.x / V, c = threadIdx.x % V;
+  Sum4 sum;
+  sum.add(r, R, n, [&](int i, float4& x, float& xm, float& xl) {
+    // CTA blockIdx.x + i: its partial of a head that begins there (1) or before (0)
+    const float* o = p.parts + (int64_t)((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * C::kPart;
+    x = *reinterpret_cast<const float4*>(o + h * C::kStride + c * 4);
+    xm = o[16 * C::kStride + h];
+    xl = o[16 * C::kStride + 16 + h];
+  });
+  s_acc[r][c] = sum.acc;
+  if (c == 0) {
+    s_ml[r][0] = sum.m;
+    s_ml[r][1] = sum.l;
   }
+  __syncthreads();
+  if (r) return;
+  Sum4 all;
+  all.add(0, 1, min(R, n), [&](int i, float4& x, float& xm, float& xl) {
+    x = s_acc[i][c];
+    xm = s_ml[i][0];
+    xl = s_ml[i][1];
+  });
+  all.finish<D>(p, (int64_t)split.x * p.hq + kvh * p.group + h0 + h, c, E4M3 ? __ldg(p.v_scale + kvh) : 1.f);
 }
 
 int num_sms() {
@@ -682,20 +732,21 @@ int num_sms() {
   return n;
 }
 
-template <int D, bool E4M3, bool HALF>
+template <int D, bool E4M3, int NH>
 cudaError_t launch(const AttnDecodeParams& p, cudaStream_t s) {
-  using C = Cfg<D, E4M3>;
-  static cudaError_t attr = cudaFuncSetAttribute(attn_decode_kernel<D, E4M3, HALF>,
+  using C = Cfg<D, E4M3, NH>;
+  static cudaError_t attr = cudaFuncSetAttribute(attn_decode_kernel<D, E4M3, NH>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (attr != cudaSuccess) return attr;
-  attn_decode_kernel<D, E4M3, HALF><<<num_sms(), 32 * C::NW, C::kSmem, s>>>(p);
-  return cudaGetLastError();
+  attn_decode_kernel<D, E4M3, NH><<<num_sms(), 32 * C::NW, C::kSmem, s>>>(p);
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  return launch_pdl(attn_join_kernel<D, E4M3, NH>, dim3(num_sms(), p.group < 16 ? p.group : 16), 256, 0, 1, s, p);
 }
 
 template <int D, bool E4M3>
 cudaError_t launch(const AttnDecodeParams& p, cudaStream_t s) {
-  // up to 8 query heads per key-value head: half the rows of the matrix products are not kept
-  return p.group <= 8 ? launch<D, E4M3, true>(p, s) : launch<D, E4M3, false>(p, s);
+  return p.group <= 8 ? launch<D, E4M3, 1>(p, s) : launch<D, E4M3, 2>(p, s);  // blocks of 8 heads
 }
 
 }  // namespace
