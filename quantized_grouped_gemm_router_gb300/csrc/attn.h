@@ -80,7 +80,7 @@ struct AttnDecodeParams {
 
 // Workspace of the attention calls: status word, then what the decode's two kernels hand over.
 constexpr int kAttnMaxCtas = 256;
-constexpr int kAttnMaxWarps = 8;
+constexpr int kAttnMaxWarps = 16;
 struct AttnWs {
   size_t splits, parts, scratch, total;
 };

@@ -36,7 +36,8 @@ template <int D, bool E4M3, int NH>
 struct Cfg {
   static constexpr int RB = D * (E4M3 ? 1 : 2);     // bytes of a cache row
   static constexpr int TR = RB <= 128 ? 32 : 16;    // rows of a tile
-  static constexpr int NW = RB == 512 ? 4 : 8;      // warps
+  // warps: as many as the registers allow where a tile takes most instructions for its bytes
+  static constexpr int NW = RB == 512 ? (NH == 1 ? 6 : 4) : RB == 64 && NH == 1 ? 16 : 8;
   static constexpr int kTile = 2 * TR * RB;         // K rows, then V rows
   static constexpr int kStages = 192 * 1024 / (NW * kTile);
   static constexpr int kRing = kStages * kTile;     // per warp
@@ -348,6 +349,24 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
     uint32_t q[NH][D / 16][2];
     float o[NH][D / 16][4];
     float m[NH][2], mc[NH][2], l[NH][2], cr[NH][2];  // of heads 2 t4, + 1: maximum, scaled, this lane's sum, scale
+    // the query rows of a sequence's head, as B fragments
+    const auto load_q = [&](const Walk<TR>& at) {
+      const int kvh = at.u / nhb, h0 = (at.u % nhb) * 16;
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh) {
+        const int h = h0 + nh * 8 + g8;
+        const uint16_t* src = p.q.p + (int64_t)at.b * p.q.token_stride + (int64_t)(kvh * p.group + h) * p.q.head_stride;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            // bf16: k step ks holds values 16 ks + (0..15); e4m3: see the K fragments below
+            const int d = E4M3 ? (ks / 4) * 64 + t4 * 16 + (ks & 3) * 4 + half * 2 : ks * 16 + t4 * 2 + half * 8;
+            q[nh][ks][half] = h < p.group ? __ldg(reinterpret_cast<const uint32_t*>(src + d)) : 0u;
+          }
+      }
+    };
+    load_q(w);
     bool fresh = true, from_start = false;
     int out = 0, stage = 0, fill = C::kStages - 1;
     for (int i = 0; i < n; ++i) {
@@ -355,7 +374,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
       if (++fill == C::kStages) fill = 0;
       const int kvh = w.u / nhb, h0 = (w.u % nhb) * 16, heads = min(16, p.group - h0);
       if (fresh) {
-        // ---- a new sequence or head: its query rows as B fragments
+        // ---- a new sequence or head; its query rows have been loaded
         fresh = false;
         from_start = w.t == 0;
 #pragma unroll
@@ -372,16 +391,6 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
             l[nh][y] = 0.f;
             cr[nh][y] = scale;
           }
-          const int h = nh * 8 + g8;
-          const uint16_t* src = p.q.p + (int64_t)w.b * p.q.token_stride + (int64_t)(kvh * p.group + h0 + h) * p.q.head_stride;
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              // bf16: k step ks holds values 16 ks + (0..15); e4m3: see the K fragments below
-              const int d = E4M3 ? (ks / 4) * 64 + t4 * 16 + (ks & 3) * 4 + half * 2 : ks * 16 + t4 * 2 + half * 8;
-              q[nh][ks][half] = h < heads ? __ldg(reinterpret_cast<const uint32_t*>(src + d)) : 0u;
-            }
           if (E4M3) {
             // fp16 has bf16's precision but not its range: the row times a power of two that brings its
             // largest magnitude to 2^14
@@ -453,7 +462,13 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
 #pragma unroll
           for (int y = 0; y < 4; ++y) s[kb][nh][y] += s2[nh][y];
       }
+      const bool to_end = w.t == w.nt - 1;
       const int lim = w.len - w.t * TR;
+      Walk<TR> nx = w;
+      if (i < n - 1) {
+        nx.next(p, units);
+        if (to_end) load_q(nx);  // while the rest of this tile is worked on
+      }
       if (lim < TR) {
 #pragma unroll
         for (int kb = 0; kb < TR / 16; ++kb)
@@ -567,7 +582,6 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
       __syncwarp();
 
       // ---- the end of a sequence's head, or of this warp's run
-      const bool to_end = w.t == w.nt - 1;
       if (to_end || i == n - 1) {
         const bool whole = to_end && from_start, mid = i < n - 1;
         float* to = mid ? scratch : reinterpret_cast<float*>(ring);
@@ -636,7 +650,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
         }
         fresh = true;
       }
-      if (i < n - 1) w.next(p, units);
+      w = nx;
     }
     cp_wait<0>();
   }
