@@ -8,9 +8,12 @@
 //  * Rows. The G query heads of one key-value head read the same keys, so a 128-row tile is 128 / G
 //    positions x G heads: a K or V tile serves all of them, and the diagonal of a causal mask spans
 //    few positions. One CTA holds NT tiles of rows (each with its own softmax warps).
-//  * Steps. Step n is (key tile n / NT, row tile n % NT); its scores go to S buffer n % 2. The MMA
-//    warp issues S(0), S(1), then for every n: P(n) V, S(n + 2). The tensor cores thus work on one
-//    tile while the softmax of the other runs, with two row tiles (NT = 2) as with one.
+//  * Steps. Step n is (key tile n / NT, row tile n % NT); its scores go to S buffer n % 2. An MMA warp
+//    issues S of its first steps, then for every step n of its row tile: P(n) V, S(n + 2). The tensor
+//    cores thus work on one tile while the softmax of the other runs, with two row tiles (NT = 2) as
+//    with one. Each row tile has an MMA warp of its own: the issue of an MMA waits for the ones before
+//    it, and a warp's waits for its operands (about 400 cycles a step, against 1024 of MMAs at D = 128)
+//    pass while the other warp's MMAs run.
 //  * Rescaling. O is scaled down only when a row's maximum has grown by more than 2^8 since the last
 //    time (weights up to 2^8 are as exact in bf16, and l and O have fp32's range): softmax warps read O
 //    back on few tiles.
@@ -25,11 +28,11 @@
 namespace moe {
 namespace {
 
-// With two row tiles the warpgroups share the block's registers out: 168 x 384 at launch, then 80 for
-// the four issuing warps and 208 for each softmax thread (2 x 128 x 208 + 128 x 80 <= 168 x 384).
+// With two row tiles the warpgroups share the block's registers out: 168 x 384 at launch, then 72 for
+// the four issuing warps and 216 for each softmax thread (2 x 128 x 216 + 128 x 72 = 168 x 384).
 constexpr int kLaunchRegs = 168;
-__device__ __forceinline__ void regs_for_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
-__device__ __forceinline__ void regs_for_issue() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+__device__ __forceinline__ void regs_for_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
+__device__ __forceinline__ void regs_for_issue() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;
@@ -43,8 +46,8 @@ struct Cfg {
   static constexpr int kSlots = (224 * 1024 - NT * kQTile) / kSlot < 8 ? (224 * 1024 - NT * kQTile) / kSlot : 8;
   static constexpr int kSmem = NT * kQTile + kSlots * kSlot + 1024 + 512;  // + alignment + barriers
   static constexpr int kSoftWarps = 4 * NT;
-  static constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 1, kWarpCheck = kSoftWarps + 2;
-  static constexpr int kThreads = 32 * (kSoftWarps + 4);  // one more warp idles: whole warpgroups
+  static constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 2, kWarpCheck = kSoftWarps + 3;  // NT MMA warps
+  static constexpr int kThreads = 32 * (kSoftWarps + 4);
   static constexpr uint32_t kOCol = 2 * BN;            // S buffers at 0 and BN, O tiles behind them
   static_assert(kOCol + NT * D <= 512 && kSlots >= 4 && kSmem <= 232448, "on-chip memory");
 };
@@ -153,8 +156,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   const auto pv_done = [&](int a) { return bars + 40 + 8 * a; };
   const auto checked = [&](int b) { return bars + 56 + 8 * b; };
   const auto check = [&](int b) { return bars + 72 + 8 * b; };
-  const auto kv_full = [&](int s) { return bars + 88 + 8 * s; };
-  const auto kv_free = [&](int s) { return bars + 88 + 8 * C::kSlots + 8 * s; };
+  const auto p_half = [&](int b) { return bars + 88 + 8 * b; };
+  const auto kv_full = [&](int s) { return bars + 104 + 8 * s; };
+  const auto kv_free = [&](int s) { return bars + 104 + 8 * C::kSlots + 8 * s; };
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int G = p.group, Ppt = 128 / G;  // positions per row tile
@@ -179,14 +183,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     mbar_init(q_full, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
+      mbar_init(p_half(b), 4);
       mbar_init(p_ready(b), 4);
       mbar_init(pv_done(b), 1);
       mbar_init(checked(b), 1);
-      mbar_init(check(b), 1);
+      mbar_init(check(b), NT);
     }
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(kv_full(s), 1);
-      mbar_init(kv_free(s), 1);
+      mbar_init(kv_free(s), NT);
     }
     fence_barrier_init();
     prefetch_tmap(&maps.q);
@@ -248,43 +253,49 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             mbar_wait(kv_full(i % C::kSlots), (i / C::kSlots) & 1, &none);
         }
       }
-    } else if (warp == C::kWarpMma) {
-      // ------------------------------------------------------------------ MMA issuer
+    } else if (warp < C::kWarpMma + NT) {
+      // ------------------------------------------------------------------ MMA issuer of row tile a (NT = 2) or of all
+      constexpr uint32_t kSChunk = BN * 128 / 16, kQChunk = 16384 / 16;
+      const int a = warp - C::kWarpMma;
       const uint32_t idesc_s = idesc_f16(128, BN, false), idesc_o = idesc_f16(128, D, false) | kIdescBMn;
+      const uint64_t qd = sw128_desc(smem_u32(smem) + a * C::kQTile);
       const auto wait = [&](uint32_t bar, int parity) { return __all_sync(~0u, mbar_wait(bar, parity & 1, s_abort)); };
       const auto scores = [&](int n) {
-        const int j = n / NT, a = n % NT, i = k_idx(j), s = i % C::kSlots;
+        const int j = n / NT, i = k_idx(j), s = i % C::kSlots;
         if (!wait(kv_full(s), i / C::kSlots)) return false;
         tc_fence_after();
-        const uint64_t qd = sw128_desc(smem_u32(smem) + a * C::kQTile), kd = sw128_desc(smem_u32(ring) + s * C::kSlot);
+        const uint64_t kd = sw128_desc(smem_u32(ring) + s * C::kSlot);
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_f16_ss_elect(tmem + (n & 1) * BN, qd + c * (16384 / 16) + ks * 2, kd + c * (BN * 128 / 16) + ks * 2,
-                              idesc_s, c + ks != 0);
+          umma_f16_ss_k64_elect(tmem + (n & 1) * BN, qd + c * kQChunk, kd + c * kSChunk, idesc_s, c != 0);
         umma_commit_elect(s_full(n & 1));
-        if (a == NT - 1) umma_commit_elect(kv_free(s));
-        // V tile j's slot has seen its last copy but one arrive (an earlier K or V tile than K tile j), and
-        // s_bad of tile j - 2 has been read: the check of V tile j may begin
-        if (a == 0 && j >= j_masked && lane == 0) mbar_arrive(check((j - j_masked) & 1));
+        umma_commit_elect(kv_free(s));
+        // every copy before V tile j's into its slot has arrived (it is an earlier one than K tile j's), and
+        // this warp has read s_bad of tile j - 2: the check of V tile j may begin
+        if (j >= j_masked && lane == 0) mbar_arrive(check((j - j_masked) & 1));
         __syncwarp();
         return true;
       };
-      bool ok = steps > 0 && wait(q_full, 0) && scores(0) && (steps == 1 || scores(1));
-      for (int n = 0; ok && n < steps; ++n) {
-        const int j = n / NT, a = n % NT, i = v_idx(j), s = i % C::kSlots;
-        if (!(ok = wait(p_ready(n & 1), n >> 1) && wait(kv_full(s), i / C::kSlots))) break;
+      bool ok = nj > 0 && wait(q_full, 0) && scores(a) && (NT == 2 || nj == 1 || scores(1));
+      for (int n = a; ok && n < steps; n += NT) {
+        const int j = n / NT, i = v_idx(j), s = i % C::kSlots;
+        if (!(ok = wait(kv_full(s), i / C::kSlots) && wait(p_half(n & 1), n >> 1))) break;
         tc_fence_after();
-        if (!(j >= j_masked && s_bad[(j - j_masked) & 1])) {
-          const uint64_t vd = sw128_mn_desc(smem_u32(ring) + s * C::kSlot, BN * 128);
+        const bool skip = j >= j_masked && s_bad[(j - j_masked) & 1];  // the softmax warps add this product
+        const uint64_t vd = sw128_mn_desc(smem_u32(ring) + s * C::kSlot, BN * 128);
 #pragma unroll
-          for (int ks = 0; ks < BN / 16; ++ks)
-            umma_f16_ts_elect(tmem + C::kOCol + a * D, tmem + (n & 1) * BN + ks * 8, vd + ks * (16 * 128 / 16), idesc_o,
-                              j + ks != 0);
+        for (int kb = 0; kb < BN / 64; ++kb) {
+          if (kb == BN / 128) {
+            if (!(ok = wait(p_ready(n & 1), n >> 1))) break;
+            tc_fence_after();
+          }
+          if (!skip)
+            umma_f16_ts_mn_k64_elect(tmem + C::kOCol + a * D, tmem + (n & 1) * BN + kb * 32, vd + kb * (64 * 128 / 16),
+                                     idesc_o, j + kb != 0);
         }
+        if (!ok) break;
         umma_commit_elect(pv_done(a));
-        if (a == NT - 1) umma_commit_elect(kv_free(s));
+        umma_commit_elect(kv_free(s));
         if (n + 2 < steps) ok = scores(n + 2);
       }
     } else if (warp == C::kWarpCheck) {
@@ -327,15 +338,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         float s[BN];
 #pragma unroll
         for (int i = 0; i < BN; i += 32) tmem_ld32(st + i, s + i);
-        tmem_wait_ld();
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         const int lim = seen - j * BN;
-        if (!__all_sync(~0u, lim >= BN)) {
+        const bool all = __all_sync(~0u, lim >= BN);
 #pragma unroll
-          for (int i = 0; i < BN; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+        for (int i = 0; i < BN; i += 32) {
+          tmem_wait_ld32(s + i);
+          if (!all) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) s[i + x] = i + x < lim ? s[i + x] : -INFINITY;
+          }
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) m4[(x / 2) & 3] = max3(m4[(x / 2) & 3], s[i + x], s[i + x + 1]);
         }
-        float m4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int i = 4; i < BN; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i]);
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         if (j == 0) {
           m = mx;
@@ -349,28 +364,40 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           if (!(ok = __all_sync(~0u, mbar_wait(pv_done(a), (j - 1) & 1, s_abort)))) break;
           tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < D; i += 32) {
-            float o[32];
-            tmem_ld32(ot + i, o);
+          for (int i = 0; i < D; i += 16) {  // few values at a time: s is live
+            uint32_t o[16];
+            tmem_ld16(ot + i, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] *= f;
-            tmem_st32(ot + i, reinterpret_cast<uint32_t*>(o));
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            tmem_st16(ot + i, o);
           }
         }
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+        uint64_t l2[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < BN; i += 32) {
           uint32_t w[16];
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
-            const float p0 = ex2(fmaf(s[i + x], c, -mc)), p1 = ex2(fmaf(s[i + x + 1], c, -mc));
-            l4[x & 2] += p0;
-            l4[(x & 2) + 1] += p1;
+            float p0, p1;
+            unpack2(fma2(pack2(s[i + x], s[i + x + 1]), c2, mc2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            l2[(x / 2) & 1] = add2(l2[(x / 2) & 1], pack2(p0, p1));
             w[x / 2] = bf16x2_rn(p0, p1);
           }
           tmem_st16(st + i / 2, w);
+          if (BN == 128 && i + 32 == BN / 2 && j < j_masked) {  // the first half's product may begin
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_half(n & 1));
+          }
         }
+        float l4[4];
+        unpack2(l2[0], l4[0], l4[1]);
+        unpack2(l2[1], l4[2], l4[3]);
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         tmem_wait_st();
         if (j >= j_masked) {
@@ -387,7 +414,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready(n & 1));
+        if (lane == 0) {
+          if (BN == 64 || j >= j_masked) mbar_arrive(p_half(n & 1));
+          mbar_arrive(p_ready(n & 1));
+        }
       }
       if (nj && ok) ok = __all_sync(~0u, mbar_wait(pv_done(a), (nj - 1) & 1, s_abort));
       if (ok) {
