@@ -9,11 +9,12 @@
 //    positions x G heads: a K or V tile serves all of them, and the diagonal of a causal mask spans
 //    few positions. One CTA holds NT tiles of rows (each with its own softmax warps).
 //  * Steps. Step n is (key tile n / NT, row tile n % NT); its scores go to S buffer n % 2. An MMA warp
-//    issues S of its first steps, then for every step n of its row tile: P(n) V, S(n + 2). The tensor
-//    cores thus work on one tile while the softmax of the other runs, with two row tiles (NT = 2) as
-//    with one. Each row tile has an MMA warp of its own: the issue of an MMA waits for the ones before
-//    it, and a warp's waits for its operands (about 400 cycles a step, against 1024 of MMAs at D = 128)
-//    pass while the other warp's MMAs run.
+//    issues S of its first step, then for every second step n: P(n) V, S(n + 2). The tensor cores thus
+//    work on one step while the softmax of the other runs, with two row tiles (NT = 2) as with one.
+//    There are two MMA warps: the issue of an MMA waits for the ones before it, and a warp's waits for
+//    its operands (about 400 cycles a step, against 1024 of MMAs at D = 128) pass while the other
+//    warp's MMAs run. They take turns, a step each: mixed, both steps' scores would be done at the same
+//    time, and both softmaxes would run while the tensor cores idle.
 //  * Rescaling. O is scaled down only when a row's maximum has grown by more than 2^8 since the last
 //    time (weights up to 2^8 are as exact in bf16, and l and O have fp32's range): softmax warps read O
 //    back on few tiles.
@@ -39,17 +40,21 @@ constexpr float kRescaleLog2 = 8.f;
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int BN = D == 256 ? 64 : 128;       // keys per tile (D = 256: two more tiles in flight)
+  static constexpr int BN = NT == 2 ? 128 : 64;        // keys per tile
+  static constexpr int kPerSm = NT == 1 && D <= 128 ? 2 : 1;  // CTAs per SM
   static constexpr int kChunks = D / 64;               // 128-byte columns of a row
   static constexpr int kQTile = kChunks * 16384;       // one row tile
   static constexpr int kSlot = BN * D * 2;             // one K or V tile
-  static constexpr int kSlots = (224 * 1024 - NT * kQTile) / kSlot < 8 ? (224 * 1024 - NT * kQTile) / kSlot : 8;
+  static constexpr int kRoom = (kPerSm == 2 ? 110 : 224) * 1024 - NT * kQTile;
+  static constexpr int kSlots = kRoom / kSlot < 8 ? kRoom / kSlot : 8;
   static constexpr int kSmem = NT * kQTile + kSlots * kSlot + 1024 + 512;  // + alignment + barriers
   static constexpr int kSoftWarps = 4 * NT;
-  static constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 2, kWarpCheck = kSoftWarps + 3;  // NT MMA warps
+  static constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 2, kWarpCheck = kSoftWarps + 3;  // two MMA warps
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
   static constexpr uint32_t kOCol = 2 * BN;            // S buffers at 0 and BN, O tiles behind them
-  static_assert(kOCol + NT * D <= 512 && kSlots >= 4 && kSmem <= 232448, "on-chip memory");
+  static constexpr uint32_t kTmemCols = kOCol + NT * D <= 256 ? 256 : 512;
+  static_assert(kOCol + NT * D <= 512 && kTmemCols * kPerSm <= 512 && kSlots >= 4 && kPerSm * (kSmem + 1024) <= 233472,
+                "on-chip memory");
 };
 
 struct Maps {
@@ -135,8 +140,74 @@ __device__ __forceinline__ void add_seen(uint32_t o_tmem, uint32_t p_tmem, const
   }
 }
 
+template <int N>
+__device__ __forceinline__ float max_of(const float* s) {
+  float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int i = 4; i < N; i += 2) m[(i / 2) & 3] = max3(m[(i / 2) & 3], s[i], s[i + 1]);
+  return max3(m[0], m[1], fmaxf(m[2], m[3]));
+}
+
+// One row's running softmax. Weights are relative to m, which follows the maximum only when that has
+// grown by more than 2^8.
+template <int D>
+struct Softmax {
+  float c, grown;            // scale log2 e; the growth of a score that m follows
+  float m = -INFINITY, mc = 0.f;  // mc = c m, 0 while m = -inf
+  uint64_t l[2] = {0, 0};    // the sum of the weights, four parts of it
+  __device__ __forceinline__ explicit Softmax(float c_) : c(c_), grown(kRescaleLog2 / c_) {}
+
+  // Takes mx into m; the factor by which what was summed so far shrinks.
+  __device__ __forceinline__ float raise(float mx) {
+    const float m2 = fmaxf(m, mx), mc2 = m2 == -INFINITY ? 0.f : m2 * c;
+    const float f = m == -INFINITY ? 0.f : ex2(mc - mc2);
+    m = m2;
+    mc = mc2;
+    const uint64_t f2 = pack2(f, f);
+    l[0] = mul2(l[0], f2);
+    l[1] = mul2(l[1], f2);
+    return f;
+  }
+  __device__ __forceinline__ void scale_o(uint32_t ot, float f) const {
+#pragma unroll
+    for (int i = 0; i < D; i += 16) {  // few values at a time: the scores are live
+      uint32_t o[16];
+      tmem_ld16(ot + i, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+      tmem_st16(ot + i, o);
+    }
+  }
+  // The weights of N scores, as bf16 to tensor memory.
+  template <int N>
+  __device__ __forceinline__ void weights(const float* s, uint32_t to) {
+    const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+#pragma unroll
+    for (int i = 0; i < N; i += 32) {
+      uint32_t w[16];
+#pragma unroll
+      for (int x = 0; x < 32; x += 2) {
+        float p0, p1;
+        unpack2(fma2(pack2(s[i + x], s[i + x + 1]), c2, mc2), p0, p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        l[(x / 2) & 1] = add2(l[(x / 2) & 1], pack2(p0, p1));
+        w[x / 2] = bf16x2_rn(p0, p1);
+      }
+      tmem_st16(to + i / 2, w);
+    }
+  }
+  __device__ __forceinline__ float sum() const {
+    float x[4];
+    unpack2(l[0], x[0], x[1]);
+    unpack2(l[1], x[2], x[3]);
+    return (x[0] + x[1]) + (x[2] + x[3]);
+  }
+};
+
 template <int D, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
     attn_prefill_kernel(const __grid_constant__ AttnPrefillParams p, const __grid_constant__ Maps maps) {
   using C = Cfg<D, NT>;
   constexpr int BN = C::BN;
@@ -157,8 +228,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   const auto checked = [&](int b) { return bars + 56 + 8 * b; };
   const auto check = [&](int b) { return bars + 72 + 8 * b; };
   const auto p_half = [&](int b) { return bars + 88 + 8 * b; };
-  const auto kv_full = [&](int s) { return bars + 104 + 8 * s; };
-  const auto kv_free = [&](int s) { return bars + 104 + 8 * C::kSlots + 8 * s; };
+  const auto turn = [&](int a) { return bars + 104 + 8 * a; };
+  const auto pv_half = [&](int a) { return bars + 120 + 8 * a; };
+  const auto kv_full = [&](int s) { return bars + 136 + 8 * s; };
+  const auto kv_free = [&](int s) { return bars + 136 + 8 * C::kSlots + 8 * s; };
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int G = p.group, Ppt = 128 / G;  // positions per row tile
@@ -176,7 +249,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       check_offsets(p.cu_k, p.n_seqs, p.total_k, p.hdr, lane, 32);
     }
   } else if (warp == C::kWarpMma) {
-    tmem_alloc(smem_u32(s_tmem), 512);
+    tmem_alloc(smem_u32(s_tmem), C::kTmemCols);
     tmem_relinquish();
   } else if (warp == C::kWarpTma && lane == 0) {
     *s_abort = 0;
@@ -187,6 +260,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       mbar_init(p_ready(b), 4);
       mbar_init(pv_done(b), 1);
       mbar_init(checked(b), 1);
+      mbar_init(turn(b), 1);
+      mbar_init(pv_half(b), 1);
       mbar_init(check(b), NT);
     }
     for (int s = 0; s < C::kSlots; ++s) {
@@ -253,16 +328,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             mbar_wait(kv_full(i % C::kSlots), (i / C::kSlots) & 1, &none);
         }
       }
-    } else if (warp < C::kWarpMma + NT) {
-      // ------------------------------------------------------------------ MMA issuer of row tile a (NT = 2) or of all
+    } else if (warp < C::kWarpMma + 2) {
+      // ------------------------------------------------------------------ MMA issuer of the steps n0, n0 + 2, ...
       constexpr uint32_t kSChunk = BN * 128 / 16, kQChunk = 16384 / 16;
-      const int a = warp - C::kWarpMma;
+      const int n0 = warp - C::kWarpMma, a = n0 % NT;
       const uint32_t idesc_s = idesc_f16(128, BN, false), idesc_o = idesc_f16(128, D, false) | kIdescBMn;
       const uint64_t qd = sw128_desc(smem_u32(smem) + a * C::kQTile);
       const auto wait = [&](uint32_t bar, int parity) { return __all_sync(~0u, mbar_wait(bar, parity & 1, s_abort)); };
+      const auto have_k = [&](int n) {
+        const int i = k_idx(n / NT);
+        return wait(kv_full(i % C::kSlots), i / C::kSlots);
+      };
       const auto scores = [&](int n) {
-        const int j = n / NT, i = k_idx(j), s = i % C::kSlots;
-        if (!wait(kv_full(s), i / C::kSlots)) return false;
+        const int j = n / NT, s = k_idx(j) % C::kSlots;
         tc_fence_after();
         const uint64_t kd = sw128_desc(smem_u32(ring) + s * C::kSlot);
 #pragma unroll
@@ -274,18 +352,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         // this warp has read s_bad of tile j - 2: the check of V tile j may begin
         if (j >= j_masked && lane == 0) mbar_arrive(check((j - j_masked) & 1));
         __syncwarp();
-        return true;
       };
-      bool ok = nj > 0 && wait(q_full, 0) && scores(a) && (NT == 2 || nj == 1 || scores(1));
-      for (int n = a; ok && n < steps; n += NT) {
+      bool ok = n0 < steps && wait(q_full, 0) && have_k(n0);
+      if (ok) scores(n0);
+      for (int n = n0; ok && n < steps; n += 2) {
         const int j = n / NT, i = v_idx(j), s = i % C::kSlots;
-        if (!(ok = wait(kv_full(s), i / C::kSlots) && wait(p_half(n & 1), n >> 1))) break;
+        const bool more = n + 2 < steps;
+        if (!(ok = wait(kv_full(s), i / C::kSlots) && (!more || have_k(n + 2)) && wait(p_half(n & 1), n >> 1))) break;
+        if (n > 0 && !(ok = wait(turn(n0), n0 ? n >> 1 : (n >> 1) - 1))) break;
         tc_fence_after();
         const bool skip = j >= j_masked && s_bad[(j - j_masked) & 1];  // the softmax warps add this product
         const uint64_t vd = sw128_mn_desc(smem_u32(ring) + s * C::kSlot, BN * 128);
 #pragma unroll
         for (int kb = 0; kb < BN / 64; ++kb) {
           if (kb == BN / 128) {
+            if (BN == 128) umma_commit_elect(pv_half(a));
             if (!(ok = wait(p_ready(n & 1), n >> 1))) break;
             tc_fence_after();
           }
@@ -296,7 +377,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (!ok) break;
         umma_commit_elect(pv_done(a));
         umma_commit_elect(kv_free(s));
-        if (n + 2 < steps) ok = scores(n + 2);
+        if (more) scores(n + 2);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(turn(1 - n0));
       }
     } else if (warp == C::kWarpCheck) {
       // ------------------------------------------------------------------ V tiles not seen whole
@@ -327,78 +411,63 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const bool valid = row < Ppt * G && pos < it.n_pos;
       // keys this row sees (rows of no position: all, so that they add no compares)
       const int seen = !valid ? nj * BN : p.causal ? min(max(it.pos0 + pos + 1 + it.off, 0), it.lk) : it.lk;
-      const float c = p.scale * kLog2e, grown = kRescaleLog2 / c;
-      float m = -INFINITY, mc = 0.f, l = 0.f;  // mc = c m, 0 while m = -inf
+      Softmax<D> soft(p.scale * kLog2e);
+      const auto grow = [&](float mx, bool first, uint32_t ot, uint32_t bar, int parity) {
+        if (!__any_sync(~0u, mx > soft.m + soft.grown)) return true;
+        const float f = soft.raise(mx);
+        if (first) return true;
+        if (!__all_sync(~0u, mbar_wait(bar, parity & 1, s_abort))) return false;  // O is at rest
+        tc_fence_after();
+        soft.scale_o(ot, f);
+        return true;
+      };
       bool ok = true;
       for (int j = 0; j < nj; ++j) {
         const int n = j * NT + a;
         const uint32_t st = lanes + (n & 1) * BN, ot = lanes + C::kOCol + a * D;
         if (!(ok = __all_sync(~0u, mbar_wait(s_full(n & 1), (n >> 1) & 1, s_abort)))) break;
         tc_fence_after();
-        float s[BN];
-#pragma unroll
-        for (int i = 0; i < BN; i += 32) tmem_ld32(st + i, s + i);
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (BN == 128 && j < j_masked) {
+          // seen whole by every row: two halves, the second one's scores on their way while the first one's
+          // weights are made, the first one's product under way while the second one's are
+          float s0[64], s1[64];
+          tmem_ld32(st, s0);
+          tmem_ld32(st + 32, s0 + 32);
+          tmem_wait_ld32(s0);
+          tmem_wait_ld32(s0 + 32);
+          tmem_ld32(st + 64, s1);
+          tmem_ld32(st + 96, s1 + 32);
+          if (!(ok = grow(max_of<64>(s0), j == 0, ot, pv_done(a), j - 1))) break;
+          soft.template weights<64>(s0, st);
+          tmem_wait_ld32(s1);
+          tmem_wait_ld32(s1 + 32);
+          const float mx = max_of<64>(s1);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_half(n & 1));
+          if (!(ok = grow(mx, false, ot, pv_half(a), j))) break;
+          soft.template weights<64>(s1, st + 32);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_ready(n & 1));
+          continue;
+        }
         const int lim = seen - j * BN;
-        const bool all = __all_sync(~0u, lim >= BN);
+        {
+          float s[BN];
 #pragma unroll
-        for (int i = 0; i < BN; i += 32) {
-          tmem_wait_ld32(s + i);
-          if (!all) {
+          for (int i = 0; i < BN; i += 32) tmem_ld32(st + i, s + i);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[i + x] = i + x < lim ? s[i + x] : -INFINITY;
+          for (int i = 0; i < BN; i += 32) tmem_wait_ld32(s + i);
+          if (j >= j_masked) {
+#pragma unroll
+            for (int i = 0; i < BN; ++i) s[i] = i < lim ? s[i] : -INFINITY;
           }
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) m4[(x / 2) & 3] = max3(m4[(x / 2) & 3], s[i + x], s[i + x + 1]);
+          if (!(ok = grow(max_of<BN>(s), j == 0, ot, pv_done(a), j - 1))) break;
+          soft.template weights<BN>(s, st);
         }
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        if (j == 0) {
-          m = mx;
-          mc = m == -INFINITY ? 0.f : m * c;
-        } else if (__any_sync(~0u, mx > m + grown)) {
-          const float m2 = fmaxf(m, mx), mc2 = m2 == -INFINITY ? 0.f : m2 * c;
-          const float f = m == -INFINITY ? 0.f : ex2(mc - mc2);
-          m = m2;
-          mc = mc2;
-          l *= f;
-          if (!(ok = __all_sync(~0u, mbar_wait(pv_done(a), (j - 1) & 1, s_abort)))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < D; i += 16) {  // few values at a time: s is live
-            uint32_t o[16];
-            tmem_ld16(ot + i, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            tmem_st16(ot + i, o);
-          }
-        }
-        const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
-        uint64_t l2[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < BN; i += 32) {
-          uint32_t w[16];
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            float p0, p1;
-            unpack2(fma2(pack2(s[i + x], s[i + x + 1]), c2, mc2), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            l2[(x / 2) & 1] = add2(l2[(x / 2) & 1], pack2(p0, p1));
-            w[x / 2] = bf16x2_rn(p0, p1);
-          }
-          tmem_st16(st + i / 2, w);
-          if (BN == 128 && i + 32 == BN / 2 && j < j_masked) {  // the first half's product may begin
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_half(n & 1));
-          }
-        }
-        float l4[4];
-        unpack2(l2[0], l4[0], l4[1]);
-        unpack2(l2[1], l4[2], l4[3]);
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         tmem_wait_st();
         if (j >= j_masked) {
           const int x = j - j_masked;
@@ -415,13 +484,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (BN == 64 || j >= j_masked) mbar_arrive(p_half(n & 1));
+          mbar_arrive(p_half(n & 1));
           mbar_arrive(p_ready(n & 1));
         }
       }
       if (nj && ok) ok = __all_sync(~0u, mbar_wait(pv_done(a), (nj - 1) & 1, s_abort));
       if (ok) {
         tc_fence_after();
+        const float l = soft.sum();
         const bool none = nj == 0 || l == 0.f;
         const float inv = none ? 0.f : 1.f / l;
         const int64_t t = it.q_row + pos;
@@ -444,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
           }
         }
-        if (valid && p.lse) p.lse[t * p.hq + head] = none ? -INFINITY : mc * kLn2 + logf(l);
+        if (valid && p.lse) p.lse[t * p.hq + head] = none ? -INFINITY : soft.mc * kLn2 + logf(l);
       }
     }
   }
@@ -453,7 +523,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   __syncthreads();
   if (warp == C::kWarpMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kTmemCols);
   }
   if (threadIdx.x == 0 && *s_abort) set_device_status(p.hdr, MOE_ERR_DEVICE_TIMEOUT);
 }
