@@ -38,23 +38,26 @@ __device__ __forceinline__ void regs_for_issue() { asm volatile("setmaxnreg.dec.
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;
 
-template <int D, int NT>
+// What a CTA's streams of steps are: two row tiles over the same keys, two halves of one row tile's keys
+// (even and odd tiles), or one row tile alone (D = 256: tensor memory holds one O).
+enum Mode { kRows, kKeys, kOne };
+
+template <int D, Mode M>
 struct Cfg {
-  static constexpr int BN = NT == 2 ? 128 : 64;        // keys per tile
-  static constexpr int kPerSm = NT == 1 && D <= 128 ? 2 : 1;  // CTAs per SM
+  static constexpr int NT = M == kOne ? 1 : 2;         // streams: softmax warpgroups, O tiles
+  static constexpr int NQ = M == kRows ? 2 : 1;        // row tiles
+  static constexpr int BN = D == 256 ? 64 : 128;       // keys per tile
   static constexpr int kChunks = D / 64;               // 128-byte columns of a row
   static constexpr int kQTile = kChunks * 16384;       // one row tile
   static constexpr int kSlot = BN * D * 2;             // one K or V tile
-  static constexpr int kRoom = (kPerSm == 2 ? 110 : 224) * 1024 - NT * kQTile;
+  static constexpr int kRoom = (M == kKeys ? 222 : 224) * 1024 - NQ * kQTile;  // kKeys: the streams' statistics
   static constexpr int kSlots = kRoom / kSlot < 8 ? kRoom / kSlot : 8;
-  static constexpr int kSmem = NT * kQTile + kSlots * kSlot + 1024 + 512;  // + alignment + barriers
+  static constexpr int kSmem = NQ * kQTile + kSlots * kSlot + 1024 + 512;  // + alignment + barriers
   static constexpr int kSoftWarps = 4 * NT;
   static constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 2, kWarpCheck = kSoftWarps + 3;  // two MMA warps
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
   static constexpr uint32_t kOCol = 2 * BN;            // S buffers at 0 and BN, O tiles behind them
-  static constexpr uint32_t kTmemCols = kOCol + NT * D <= 256 ? 256 : 512;
-  static_assert(kOCol + NT * D <= 512 && kTmemCols * kPerSm <= 512 && kSlots >= 4 && kPerSm * (kSmem + 1024) <= 233472,
-                "on-chip memory");
+  static_assert(kOCol + NT * D <= 512 && kSlots >= 4 && kSmem <= 232448, "on-chip memory");
 };
 
 struct Maps {
@@ -110,28 +113,24 @@ __device__ __forceinline__ bool find_item(const AttnPrefillParams& p, int slot, 
 // infinity some row does not see. P: this row's bf16 weights in tensor memory.
 template <int D, int BN>
 __device__ __forceinline__ void add_seen(uint32_t o_tmem, uint32_t p_tmem, const uint8_t* v, int seen, bool fresh) {
+#pragma unroll 1
   for (int d0 = 0; d0 < D; d0 += 32) {
     float acc[32];
     tmem_ld32(o_tmem + d0, acc);
     tmem_wait_ld();
     if (fresh)
       for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-    for (int j0 = 0; j0 < BN; j0 += 32) {
-      uint32_t w[16];
+    for (int row = 0; row < BN; ++row) {
       __syncwarp();
-      tmem_ld16(p_tmem + j0 / 2, w);
-      tmem_wait_ld();
+      const uint32_t w = tmem_ld1(p_tmem + row / 2);
+      if (row >= seen) continue;
+      const float x = __uint_as_float(row & 1 ? w & 0xFFFF0000u : w << 16);
+      const uint8_t* at = v + (d0 / 64) * (BN * 128) + row * 128;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const int row = j0 + j;
-        if (row >= seen) continue;
-        const float x = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
-        const uint8_t* at = v + (d0 / 64) * (BN * 128) + row * 128;
-        for (int i = 0; i < 32; i += 2) {
-          const uint32_t y = *reinterpret_cast<const uint32_t*>(at + (((d0 % 64 + i) * 2) ^ ((row & 7) << 4)));
-          acc[i] = fmaf(x, __uint_as_float(y << 16), acc[i]);
-          acc[i + 1] = fmaf(x, __uint_as_float(y & 0xFFFF0000u), acc[i + 1]);
-        }
+      for (int i = 0; i < 32; i += 2) {
+        const uint32_t y = *reinterpret_cast<const uint32_t*>(at + (((d0 % 64 + i) * 2) ^ ((row & 7) << 4)));
+        acc[i] = fmaf(x, __uint_as_float(y << 16), acc[i]);
+        acc[i + 1] = fmaf(x, __uint_as_float(y & 0xFFFF0000u), acc[i + 1]);
       }
     }
     __syncwarp();
@@ -206,15 +205,16 @@ struct Softmax {
   }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
+template <int D, Mode M>
+__global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
     attn_prefill_kernel(const __grid_constant__ AttnPrefillParams p, const __grid_constant__ Maps maps) {
-  using C = Cfg<D, NT>;
-  constexpr int BN = C::BN;
+  using C = Cfg<D, M>;
+  constexpr int BN = C::BN, NT = C::NT, NQ = C::NQ;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* ring = smem + NT * C::kQTile;
+  uint8_t* ring = smem + NQ * C::kQTile;
   uint8_t* misc = ring + C::kSlots * C::kSlot;
+  __shared__ float2 s_stat[M == kKeys ? 2 : 1][M == kKeys ? 128 : 1];  // m c and l of the streams' rows
   volatile int* s_abort = reinterpret_cast<volatile int*>(misc);
   volatile int* s_bad = reinterpret_cast<volatile int*>(misc + 4);  // [2] V tile (counted from j_masked, % 2) holds a non-finite value
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + 12);
@@ -230,8 +230,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
   const auto p_half = [&](int b) { return bars + 88 + 8 * b; };
   const auto turn = [&](int a) { return bars + 104 + 8 * a; };
   const auto pv_half = [&](int a) { return bars + 120 + 8 * a; };
-  const auto kv_full = [&](int s) { return bars + 136 + 8 * s; };
-  const auto kv_free = [&](int s) { return bars + 136 + 8 * C::kSlots + 8 * s; };
+  const uint32_t merged = bars + 136;
+  const auto kv_full = [&](int s) { return bars + 144 + 8 * s; };
+  const auto kv_free = [&](int s) { return bars + 144 + 8 * C::kSlots + 8 * s; };
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int G = p.group, Ppt = 128 / G;  // positions per row tile
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
 
   if (warp == 0) {
     Item it;
-    const bool found = find_item(p, slot, NT * Ppt, it);
+    const bool found = find_item(p, slot, NQ * Ppt, it);
     if (lane == 0) {
       *s_found = found;
       if (found) *s_item = it;
@@ -249,11 +250,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
       check_offsets(p.cu_k, p.n_seqs, p.total_k, p.hdr, lane, 32);
     }
   } else if (warp == C::kWarpMma) {
-    tmem_alloc(smem_u32(s_tmem), C::kTmemCols);
+    tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   } else if (warp == C::kWarpTma && lane == 0) {
     *s_abort = 0;
     mbar_init(q_full, 1);
+    mbar_init(merged, 8);
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
       mbar_init(p_half(b), 4);
@@ -262,11 +264,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
       mbar_init(checked(b), 1);
       mbar_init(turn(b), 1);
       mbar_init(pv_half(b), 1);
-      mbar_init(check(b), NT);
+      mbar_init(check(b), NQ);
     }
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(kv_full(s), 1);
-      mbar_init(kv_free(s), NT);
+      mbar_init(kv_free(s), NQ);
     }
     fence_barrier_init();
     prefetch_tmap(&maps.q);
@@ -284,29 +286,29 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
     // keys that the first and the last position of this CTA see
     const int first_seen = p.causal ? min(max(it.pos0 + 1 + it.off, 0), it.lk) : it.lk;
     const int last_seen = p.causal ? min(max(it.pos0 + it.n_pos + it.off, 0), it.lk) : it.lk;
-    const int nj = (last_seen + BN - 1) / BN, steps = NT * nj;
+    const int nj = (last_seen + BN - 1) / BN, steps = NQ * nj;
     const int j_masked = first_seen / BN;  // tiles from here on are not seen whole by every row
-    // the place of K tile j and V tile j in the ring's order
-    const auto k_idx = [&](int j) { return NT == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
-    const auto v_idx = [&](int j) { return NT == 2 ? 2 * j + 1 : (j == nj - 1 ? 2 * j + 1 : 2 * j + 2); };
+    // Step n: key tile n / NQ, stream n % NT, the stream's step n / NT. The ring's order is the steps' order of
+    // use: K0 V0 K1 V1 ... with two row tiles (each used by two steps), else K0 K1 V0 K2 V1 ...
+    const auto k_idx = [&](int j) { return NQ == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
+    const auto v_idx = [&](int j) { return NQ == 2 ? 2 * j + 1 : (j == nj - 1 ? 2 * j + 1 : 2 * j + 2); };
 
     if (warp >= C::kSoftWarps) {
     if (NT == 2) regs_for_issue();
     if (warp == C::kWarpTma) {
       // ------------------------------------------------------------------ TMA producer
       if (lane == 0 && steps) {
-        mbar_arrive_expect_tx(q_full, (uint32_t)(NT * C::kChunks * Ppt * G * 128));
-        for (int a = 0; a < NT; ++a)
+        mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * C::kChunks * Ppt * G * 128));
+        for (int a = 0; a < NQ; ++a)
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_3d(smem_u32(smem) + a * C::kQTile + c * 16384, &maps.q, c * 64, kvh * G, it.q_row + a * Ppt, q_full);
         int issued = 0;
         for (; issued < 2 * nj; ++issued) {
           const int i = issued, s = i % C::kSlots;
           if (i >= C::kSlots && !mbar_wait(kv_free(s), ((i / C::kSlots) & 1) ^ 1, s_abort)) break;
-          // entry i of the order K0 V0 K1 V1 ... (NT = 2) or K0 K1 V0 K2 V1 ... (NT = 1)
           bool is_v;
           int j;
-          if (NT == 2) {
+          if (NQ == 2) {
             is_v = i & 1;
             j = i / 2;
           } else if (i == 2 * nj - 1) {
@@ -333,14 +335,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
       constexpr uint32_t kSChunk = BN * 128 / 16, kQChunk = 16384 / 16;
       const int n0 = warp - C::kWarpMma, a = n0 % NT;
       const uint32_t idesc_s = idesc_f16(128, BN, false), idesc_o = idesc_f16(128, D, false) | kIdescBMn;
-      const uint64_t qd = sw128_desc(smem_u32(smem) + a * C::kQTile);
+      const uint64_t qd = sw128_desc(smem_u32(smem) + n0 % NQ * C::kQTile);
       const auto wait = [&](uint32_t bar, int parity) { return __all_sync(~0u, mbar_wait(bar, parity & 1, s_abort)); };
       const auto have_k = [&](int n) {
-        const int i = k_idx(n / NT);
+        const int i = k_idx(n / NQ);
         return wait(kv_full(i % C::kSlots), i / C::kSlots);
       };
       const auto scores = [&](int n) {
-        const int j = n / NT, s = k_idx(j) % C::kSlots;
+        const int j = n / NQ, s = k_idx(j) % C::kSlots;
         tc_fence_after();
         const uint64_t kd = sw128_desc(smem_u32(ring) + s * C::kSlot);
 #pragma unroll
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
       bool ok = n0 < steps && wait(q_full, 0) && have_k(n0);
       if (ok) scores(n0);
       for (int n = n0; ok && n < steps; n += 2) {
-        const int j = n / NT, i = v_idx(j), s = i % C::kSlots;
+        const int j = n / NQ, i = v_idx(j), s = i % C::kSlots;
         const bool more = n + 2 < steps;
         if (!(ok = wait(kv_full(s), i / C::kSlots) && (!more || have_k(n + 2)) && wait(p_half(n & 1), n >> 1))) break;
         if (n > 0 && !(ok = wait(turn(n0), n0 ? n >> 1 : (n >> 1) - 1))) break;
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
           }
           if (!skip)
             umma_f16_ts_mn_k64_elect(tmem + C::kOCol + a * D, tmem + (n & 1) * BN + kb * 32, vd + kb * (64 * 128 / 16),
-                                     idesc_o, j + kb != 0);
+                                     idesc_o, n / NT + kb != 0);
         }
         if (!ok) break;
         umma_commit_elect(pv_done(a));
@@ -407,12 +409,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
       if (NT == 2) regs_for_softmax();
       const int a = warp / 4, row = threadIdx.x & 127;
       const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
-      const int pos = a * Ppt + row / G, head = kvh * G + row % G;
+      const int pos = a % NQ * Ppt + row / G, head = kvh * G + row % G;
       const bool valid = row < Ppt * G && pos < it.n_pos;
       // keys this row sees (rows of no position: all, so that they add no compares)
       const int seen = !valid ? nj * BN : p.causal ? min(max(it.pos0 + pos + 1 + it.off, 0), it.lk) : it.lk;
       Softmax<D> soft(p.scale * kLog2e);
-      const auto grow = [&](float mx, bool first, uint32_t ot, uint32_t bar, int parity) {
+      const uint32_t ot = lanes + C::kOCol + a * D;
+      const auto grow = [&](float mx, bool first, uint32_t bar, int parity) {
         if (!__any_sync(~0u, mx > soft.m + soft.grown)) return true;
         const float f = soft.raise(mx);
         if (first) return true;
@@ -422,9 +425,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
         return true;
       };
       bool ok = true;
-      for (int j = 0; j < nj; ++j) {
-        const int n = j * NT + a;
-        const uint32_t st = lanes + (n & 1) * BN, ot = lanes + C::kOCol + a * D;
+      for (int n = a; n < steps; n += NT) {
+        const int j = n / NQ, k = n / NT;  // key tile, step of this stream
+        const uint32_t st = lanes + (n & 1) * BN;
         if (!(ok = __all_sync(~0u, mbar_wait(s_full(n & 1), (n >> 1) & 1, s_abort)))) break;
         tc_fence_after();
         if (BN == 128 && j < j_masked) {
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
           tmem_wait_ld32(s0 + 32);
           tmem_ld32(st + 64, s1);
           tmem_ld32(st + 96, s1 + 32);
-          if (!(ok = grow(max_of<64>(s0), j == 0, ot, pv_done(a), j - 1))) break;
+          if (!(ok = grow(max_of<64>(s0), k == 0, pv_done(a), k - 1))) break;
           soft.template weights<64>(s0, st);
           tmem_wait_ld32(s1);
           tmem_wait_ld32(s1 + 32);
@@ -446,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_half(n & 1));
-          if (!(ok = grow(mx, false, ot, pv_half(a), j))) break;
+          if (!(ok = grow(mx, false, pv_half(a), k))) break;
           soft.template weights<64>(s1, st + 32);
           tmem_wait_st();
           tc_fence_before();
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
 #pragma unroll
             for (int i = 0; i < BN; ++i) s[i] = i < lim ? s[i] : -INFINITY;
           }
-          if (!(ok = grow(max_of<BN>(s), j == 0, ot, pv_done(a), j - 1))) break;
+          if (!(ok = grow(max_of<BN>(s), k == 0, pv_done(a), k - 1))) break;
           soft.template weights<BN>(s, st);
         }
         tmem_wait_st();
@@ -475,10 +478,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
           if (s_bad[x & 1]) {
             const int i = v_idx(j);
             ok = mbar_wait(kv_full(i % C::kSlots), (i / C::kSlots) & 1, s_abort) &&
-                 (j == 0 || mbar_wait(pv_done(a), (j - 1) & 1, s_abort));
+                 (k == 0 || mbar_wait(pv_done(a), (k - 1) & 1, s_abort));
             if (!(ok = __all_sync(~0u, ok))) break;
             tc_fence_after();
-            add_seen<D, BN>(ot, st, ring + (i % C::kSlots) * C::kSlot, lim, j == 0);
+            add_seen<D, BN>(ot, st, ring + (i % C::kSlots) * C::kSlot, lim, k == 0);
           }
         }
         tc_fence_before();
@@ -488,33 +491,67 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
           mbar_arrive(p_ready(n & 1));
         }
       }
-      if (nj && ok) ok = __all_sync(~0u, mbar_wait(pv_done(a), (nj - 1) & 1, s_abort));
+      const int mine = (steps - a + NT - 1) / NT;  // steps of this stream
+      if (mine && ok) ok = __all_sync(~0u, mbar_wait(pv_done(a), (mine - 1) & 1, s_abort));
+      // the factor of O (and of the other stream's O) in the output, and the row's log sum
+      float f = 0.f, f2 = 0.f, lse = -INFINITY;
+      const float l = soft.sum();
+      if (M == kKeys) {
+        // both streams' O belong to the same rows (the same lanes): each warpgroup writes half the columns
+        const float mc = l == 0.f ? -INFINITY : soft.mc;
+        s_stat[a][row] = make_float2(mc, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(merged);
+        __syncwarp();
+        if (ok) ok = __all_sync(~0u, mbar_wait(merged, 0, s_abort));
+        const float2 other = s_stat[1 - a][row];
+        const float top = fmaxf(mc, other.x);
+        if (l != 0.f || other.y != 0.f) {
+          const float w = l == 0.f ? 0.f : ex2(mc - top), w2 = other.y == 0.f ? 0.f : ex2(other.x - top);
+          const float sum = fmaf(w, l, w2 * other.y);
+          f = w / sum;
+          f2 = w2 / sum;
+          lse = top * kLn2 + logf(sum);
+        }
+      } else if (l != 0.f) {
+        f = 1.f / l;
+        lse = soft.mc * kLn2 + logf(l);
+      }
       if (ok) {
         tc_fence_after();
-        const float l = soft.sum();
-        const bool none = nj == 0 || l == 0.f;
-        const float inv = none ? 0.f : 1.f / l;
+        constexpr int kCols = M == kKeys ? D / 2 : D;
+        const int col0 = M == kKeys ? a * kCols : 0;
         const int64_t t = it.q_row + pos;
-        uint16_t* out = p.o + (t * p.hq + head) * D;
+        uint16_t* out = p.o + (t * p.hq + head) * D + col0;
 #pragma unroll
-        for (int i = 0; i < D; i += 32) {
-          float o[32];
-          if (nj) {
-            tmem_ld32(lanes + C::kOCol + a * D + i, o);
-            tmem_wait_ld();
+        for (int i = 0; i < kCols; i += 32) {
+          float o[32], o2[32];
+          if (steps) {
+            tmem_ld32(ot + col0 + i, o);
+            if (M == kKeys) tmem_ld32(lanes + C::kOCol + (1 - a) * D + col0 + i, o2);
+            tmem_wait_ld32(o);
+            if (M == kKeys) tmem_wait_ld32(o2);
           }
           if (valid) {
 #pragma unroll
             for (int x = 0; x < 32; x += 8) {
               uint32_t w[4];
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                w[y] = none ? 0u : bf16x2_rn(o[x + 2 * y] * inv, o[x + 2 * y + 1] * inv);
+              for (int y = 0; y < 4; ++y) {
+                // a factor of 0: nothing was written there
+                float u = f == 0.f ? 0.f : o[x + 2 * y] * f, v = f == 0.f ? 0.f : o[x + 2 * y + 1] * f;
+                if (M == kKeys && f2 != 0.f) {
+                  u = fmaf(o2[x + 2 * y], f2, u);
+                  v = fmaf(o2[x + 2 * y + 1], f2, v);
+                }
+                w[y] = bf16x2_rn(u, v);
+              }
               *reinterpret_cast<uint4*>(out + i + x) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
-        if (valid && p.lse) p.lse[t * p.hq + head] = none ? -INFINITY : soft.mc * kLn2 + logf(l);
+        if (valid && p.lse && (M != kKeys || a == 0)) p.lse[t * p.hq + head] = lse;
       }
     }
   }
@@ -523,7 +560,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kPerSm)
   __syncthreads();
   if (warp == C::kWarpMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+    tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && *s_abort) set_device_status(p.hdr, MOE_ERR_DEVICE_TIMEOUT);
 }
@@ -536,16 +573,16 @@ bool make_map(CUtensorMap* m, const moe_heads_view& v, int d, int heads, int tok
   return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v.p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, int NT>
+template <int D, Mode M>
 cudaError_t launch(const AttnPrefillParams& p, cudaStream_t s) {
-  using C = Cfg<D, NT>;
-  static cudaError_t attr = cudaFuncSetAttribute(attn_prefill_kernel<D, NT>,
+  using C = Cfg<D, M>;
+  static cudaError_t attr = cudaFuncSetAttribute(attn_prefill_kernel<D, M>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (attr != cudaSuccess) return attr;
-  if (NT == 2) {  // the register split waits for ever unless the launch brings what it hands out
+  if (C::NT == 2) {  // the register split waits for ever unless the launch brings what it hands out
     static int regs = [] {
       cudaFuncAttributes a;
-      return cudaFuncGetAttributes(&a, attn_prefill_kernel<D, NT>) == cudaSuccess ? a.numRegs : 0;
+      return cudaFuncGetAttributes(&a, attn_prefill_kernel<D, M>) == cudaSuccess ? a.numRegs : 0;
     }();
     if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
   }
@@ -558,9 +595,9 @@ cudaError_t launch(const AttnPrefillParams& p, cudaStream_t s) {
       !make_map(&maps.v, keys ? p.v : p.q, D, keys ? p.hkv : p.hq, keys ? p.total_k : p.total_q, 1, C::BN))
     return cudaErrorInvalidValue;
   // every sequence has at most one ragged tile
-  const int64_t tiles = (int64_t)p.total_q / (NT * ppt) + (p.n_seqs < p.total_q ? p.n_seqs : p.total_q);
+  const int64_t tiles = (int64_t)p.total_q / (C::NQ * ppt) + (p.n_seqs < p.total_q ? p.n_seqs : p.total_q);
   if (tiles * p.hkv > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  attn_prefill_kernel<D, NT><<<(unsigned)(tiles * p.hkv), C::kThreads, C::kSmem, s>>>(p, maps);
+  attn_prefill_kernel<D, M><<<(unsigned)(tiles * p.hkv), C::kThreads, C::kSmem, s>>>(p, maps);
   return cudaGetLastError();
 }
 
@@ -577,11 +614,13 @@ int num_sms() {
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int d, cudaStream_t s) {
-  // two row tiles per CTA halve the K and V traffic; one fills the GPU with half the rows
+  // Two row tiles per CTA halve the K and V traffic; one row tile with its keys split halves the longest
+  // CTA. Measured at 16/2 heads of 128: 2048 tokens (0.8 CTAs of two row tiles per SM) 35.6 against 26.8 us
+  // split, 3000 tokens (1.2) 47.4 against 48.8 us, 16384 tokens 748 against 804 us.
   const bool two = (int64_t)p.total_q / (2 * (128 / p.group)) * p.hkv >= num_sms();
-  if (d == 64) return two ? launch<64, 2>(p, s) : launch<64, 1>(p, s);
-  if (d == 128) return two ? launch<128, 2>(p, s) : launch<128, 1>(p, s);
-  return launch<256, 1>(p, s);
+  if (d == 64) return two ? launch<64, kRows>(p, s) : launch<64, kKeys>(p, s);
+  if (d == 128) return two ? launch<128, kRows>(p, s) : launch<128, kKeys>(p, s);
+  return launch<256, kOne>(p, s);
 }
 
 }  // namespace moe

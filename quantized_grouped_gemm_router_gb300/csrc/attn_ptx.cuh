@@ -58,6 +58,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
         "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
       : "r"(taddr));
 }
+// One column; the value has arrived.
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
+  return r;
+}
 // Waits for the loads in flight; the 32 values take part so that no use of them moves ahead of the wait.
 __device__ __forceinline__ void tmem_wait_ld32(float* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
