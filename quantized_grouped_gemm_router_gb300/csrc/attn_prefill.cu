@@ -7,14 +7,17 @@
 //
 //  * Rows. The G query heads of one key-value head read the same keys, so a 128-row tile is 128 / G
 //    positions x G heads: a K or V tile serves all of them, and the diagonal of a causal mask spans
-//    few positions. One CTA holds NT tiles of rows (each with its own softmax warps).
-//  * Steps. Step n is (key tile n / NT, row tile n % NT); its scores go to S buffer n % 2. An MMA warp
-//    issues S of its first step, then for every second step n: P(n) V, S(n + 2). The tensor cores thus
-//    work on one step while the softmax of the other runs, with two row tiles (NT = 2) as with one.
-//    There are two MMA warps: the issue of an MMA waits for the ones before it, and a warp's waits for
-//    its operands (about 400 cycles a step, against 1024 of MMAs at D = 128) pass while the other
-//    warp's MMAs run. They take turns, a step each: mixed, both steps' scores would be done at the same
-//    time, and both softmaxes would run while the tensor cores idle.
+//    few positions.
+//  * Items. One CTA per SM stays and draws items: two row tiles over the same keys (kRows); one row tile
+//    whose even and odd key tiles are two streams, each with its own O, m and l, added at the end (kKeys);
+//    or one row tile (kOne, D = 256). Each sequence's last rows come first: under a causal mask they see
+//    the most keys. The next item's copies and first scores run while the last one's output is written.
+//  * Steps. Step n's scores go to S buffer n % 2. An MMA warp issues S of its first step, then for every
+//    second step n: P(n) V, S(n + 2). The tensor cores thus work on one step while the softmax of the
+//    other runs. There are two MMA warps: the issue of an MMA waits for the ones before it, and a warp's
+//    waits for its operands (about 400 cycles a step, against 1024 of MMAs at D = 128) pass while the
+//    other warp's MMAs run. They take turns, a step each: mixed, both steps' scores would be done at the
+//    same time, and both softmaxes would run while the tensor cores idle.
 //  * Rescaling. O is scaled down only when a row's maximum has grown by more than 2^8 since the last
 //    time (weights up to 2^8 are as exact in bf16, and l and O have fp32's range): softmax warps read O
 //    back on few tiles.
@@ -22,7 +25,11 @@
 //    their weight is 0; but 0 times a NaN or infinity in V is not 0, so a warp checks the V tiles that
 //    some row does not see whole, and a tile with such a value is multiplied by the softmax warps,
 //    seen keys only (rare, and bounded by one tile's work).
-//  * K and V tiles are one ring, filled by TMA in the order in which the MMA warp frees them.
+//  * K and V tiles are one ring, filled by TMA in the order in which the MMA warps free them.
+//
+// Bound by the chain S -> softmax -> P V of the two streams: a step takes about 1500 cycles, 1024 of them
+// the tensor cores' own. Measured (GB300): 16384 tokens, 16/2 heads of 128, causal: 0.74 ms, 1.48 PFLOP/s (78%
+// of a cuBLAS bf16 GEMM's burst rate); 1021 tokens on 8192, heads of 256: 0.130 ms, 1.12 PFLOP/s.
 #include "attn_device.cuh"
 #include "attn_ptx.cuh"
 
@@ -50,14 +57,14 @@ struct Cfg {
   static constexpr int kChunks = D / 64;               // 128-byte columns of a row
   static constexpr int kQTile = kChunks * 16384;       // one row tile
   static constexpr int kSlot = BN * D * 2;             // one K or V tile
-  static constexpr int kRoom = (M == kKeys ? 222 : 224) * 1024 - NQ * kQTile;  // kKeys: the streams' statistics
+  static constexpr int kRoom = (M == kKeys ? 220 : 224) * 1024 - NQ * kQTile;  // kKeys: the streams' statistics
   static constexpr int kSlots = kRoom / kSlot < 8 ? kRoom / kSlot : 8;
-  static constexpr int kSmem = NQ * kQTile + kSlots * kSlot + 1024 + 512;  // + alignment + barriers
+  static constexpr int kSmem = NQ * kQTile + kSlots * kSlot + 1024;  // + alignment
   static constexpr int kSoftWarps = 4 * NT;
   static constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 2, kWarpCheck = kSoftWarps + 3;  // two MMA warps
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
   static constexpr uint32_t kOCol = 2 * BN;            // S buffers at 0 and BN, O tiles behind them
-  static_assert(kOCol + NT * D <= 512 && kSlots >= 4 && kSmem <= 232448, "on-chip memory");
+  static_assert(kOCol + NT * D <= 512 && kSlots >= 4 && kSmem + (M == kKeys ? 4608 : 512) <= 232448, "on-chip memory");
 };
 
 struct Maps {
@@ -66,6 +73,7 @@ struct Maps {
 
 // What a CTA works on.
 struct Item {
+  int head;          // key-value head, -1: there is no item
   int q_row, n_pos;  // first query row (absolute) and positions of this CTA
   int pos0;          // the first position within the sequence
   int k_row, lk;     // first key row and keys of the sequence
@@ -78,10 +86,16 @@ __device__ __forceinline__ bool find_item(const AttnPrefillParams& p, int slot, 
   const int lane = threadIdx.x & 31;
   for (int base = 0; base < p.n_seqs; base += 32) {
     const int i = base + lane;
-    int q0 = 0, n = 0;
+    int q0 = 0, n = 0, k0 = 0, k1 = 0;
     if (i < p.n_seqs) {
-      q0 = min(max(__ldg(p.cu_q + i), 0), p.total_q);
-      n = min(max(__ldg(p.cu_q + i + 1), q0), p.total_q) - q0;
+      q0 = __ldg(p.cu_q + i);
+      n = __ldg(p.cu_q + i + 1);
+      k0 = __ldg(p.cu_k + i);
+      k1 = __ldg(p.cu_k + i + 1);
+      q0 = min(max(q0, 0), p.total_q);
+      n = min(max(n, q0), p.total_q) - q0;
+      k0 = min(max(k0, 0), p.total_k);
+      k1 = min(max(k1, k0), p.total_k);
     }
     const int tiles = (n + P - 1) / P;
     int sum = tiles;
@@ -95,12 +109,11 @@ __device__ __forceinline__ bool find_item(const AttnPrefillParams& p, int slot, 
       const int src = __ffs(m) - 1;
       const int mine = tiles - 1 - (slot - (sum - tiles));  // meaningful in lane src only
       const int tile = __shfl_sync(~0u, mine, src), lq = __shfl_sync(~0u, n, src);
-      const int s = base + src;
       it.pos0 = tile * P;
       it.q_row = __shfl_sync(~0u, q0, src) + it.pos0;
       it.n_pos = min(P, lq - it.pos0);
-      it.k_row = min(max(__ldg(p.cu_k + s), 0), p.total_k);
-      it.lk = min(max(__ldg(p.cu_k + s + 1), it.k_row), p.total_k) - it.k_row;
+      it.k_row = __shfl_sync(~0u, k0, src);
+      it.lk = __shfl_sync(~0u, k1, src) - it.k_row;
       it.off = it.lk - lq;
       return true;
     }
@@ -109,36 +122,43 @@ __device__ __forceinline__ bool find_item(const AttnPrefillParams& p, int slot, 
   return false;
 }
 
-// Adds seen weights x V to this thread's row of O, key by key: for V tiles that hold a NaN or an
-// infinity some row does not see. P: this row's bf16 weights in tensor memory.
-template <int D, int BN>
-__device__ __forceinline__ void add_seen(uint32_t o_tmem, uint32_t p_tmem, const uint8_t* v, int seen, bool fresh) {
+// Adds seen weights x V to this thread's row of O, key by key, for 64 keys: for V tiles that hold a NaN or
+// an infinity some row does not see. p_tmem: this row's bf16 weights; chunk: bytes between the 64-value
+// columns of V.
+template <int D>
+__device__ __forceinline__ void add_seen(uint32_t o_tmem, uint32_t p_tmem, const uint8_t* v, int chunk, int seen, bool fresh) {
 #pragma unroll 1
-  for (int d0 = 0; d0 < D; d0 += 32) {
-    float acc[32];
-    tmem_ld32(o_tmem + d0, acc);
+  for (int d0 = 0; d0 < D; d0 += 16) {
+    uint32_t acc[16];
+    __syncwarp();
+    tmem_ld16(o_tmem + d0, acc);
     tmem_wait_ld();
     if (fresh)
-      for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-    for (int row = 0; row < BN; ++row) {
+      for (int i = 0; i < 16; ++i) acc[i] = 0u;
+#pragma unroll 1
+    for (int row = 0; row < 64; ++row) {
       __syncwarp();
       const uint32_t w = tmem_ld1(p_tmem + row / 2);
       if (row >= seen) continue;
       const float x = __uint_as_float(row & 1 ? w & 0xFFFF0000u : w << 16);
-      const uint8_t* at = v + (d0 / 64) * (BN * 128) + row * 128;
+      const uint8_t* at = v + (d0 / 64) * chunk + row * 128;
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
+      for (int i = 0; i < 16; i += 2) {
         const uint32_t y = *reinterpret_cast<const uint32_t*>(at + (((d0 % 64 + i) * 2) ^ ((row & 7) << 4)));
-        acc[i] = fmaf(x, __uint_as_float(y << 16), acc[i]);
-        acc[i + 1] = fmaf(x, __uint_as_float(y & 0xFFFF0000u), acc[i + 1]);
+        acc[i] = __float_as_uint(fmaf(x, __uint_as_float(y << 16), __uint_as_float(acc[i])));
+        acc[i + 1] = __float_as_uint(fmaf(x, __uint_as_float(y & 0xFFFF0000u), __uint_as_float(acc[i + 1])));
       }
     }
     __syncwarp();
-    tmem_st32(o_tmem + d0, reinterpret_cast<uint32_t*>(acc));
+    tmem_st16(o_tmem + d0, acc);
     tmem_wait_st();
   }
 }
 
+__device__ __forceinline__ void unsee(float* s, int lim) {  // of 64 scores those from lim on
+#pragma unroll
+  for (int i = 0; i < 64; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+}
 template <int N>
 __device__ __forceinline__ float max_of(const float* s) {
   float m[4] = {s[0], s[1], s[2], s[3]};
@@ -168,8 +188,8 @@ struct Softmax {
     return f;
   }
   __device__ __forceinline__ void scale_o(uint32_t ot, float f) const {
-#pragma unroll
-    for (int i = 0; i < D; i += 16) {  // few values at a time: the scores are live
+#pragma unroll 1
+    for (int i = 0; i < D; i += 16) {  // few values at a time: the scores are live; rarely run
       uint32_t o[16];
       tmem_ld16(ot + i, o);
       tmem_wait_ld();
@@ -178,12 +198,11 @@ struct Softmax {
       tmem_st16(ot + i, o);
     }
   }
-  // The weights of N scores, as bf16 to tensor memory.
-  template <int N>
+  // The weights of 64 scores, as bf16 to tensor memory.
   __device__ __forceinline__ void weights(const float* s, uint32_t to) {
     const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
 #pragma unroll
-    for (int i = 0; i < N; i += 32) {
+    for (int i = 0; i < 64; i += 32) {
       uint32_t w[16];
 #pragma unroll
       for (int x = 0; x < 32; x += 2) {
@@ -209,302 +228,385 @@ template <int D, Mode M>
 __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
     attn_prefill_kernel(const __grid_constant__ AttnPrefillParams p, const __grid_constant__ Maps maps) {
   using C = Cfg<D, M>;
-  constexpr int BN = C::BN, NT = C::NT, NQ = C::NQ;
+  constexpr int BN = C::BN, NT = C::NT, NQ = C::NQ, kSlots = C::kSlots;
   extern __shared__ uint8_t raw[];
+  __shared__ float2 s_stat[M == kKeys ? 2 : 1][M == kKeys ? 128 : 1];  // m c and l of the streams' rows
+  __shared__ Item s_item[2];
+  __shared__ int s_abort_flag, s_bad_flag[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ __align__(8) uint64_t s_bar[25 + (NQ == 1 ? 3 : 2) * kSlots];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = smem + NQ * C::kQTile;
-  uint8_t* misc = ring + C::kSlots * C::kSlot;
-  __shared__ float2 s_stat[M == kKeys ? 2 : 1][M == kKeys ? 128 : 1];  // m c and l of the streams' rows
-  volatile int* s_abort = reinterpret_cast<volatile int*>(misc);
-  volatile int* s_bad = reinterpret_cast<volatile int*>(misc + 4);  // [2] V tile (counted from j_masked, % 2) holds a non-finite value
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + 12);
-  Item* s_item = reinterpret_cast<Item*>(misc + 16);
-  int* s_found = reinterpret_cast<int*>(misc + 48);
-  const uint32_t bars = smem_u32(misc + 64);
-  const uint32_t q_full = bars;
-  const auto s_full = [&](int b) { return bars + 8 + 8 * b; };
-  const auto p_ready = [&](int b) { return bars + 24 + 8 * b; };
-  const auto pv_done = [&](int a) { return bars + 40 + 8 * a; };
-  const auto checked = [&](int b) { return bars + 56 + 8 * b; };
-  const auto check = [&](int b) { return bars + 72 + 8 * b; };
-  const auto p_half = [&](int b) { return bars + 88 + 8 * b; };
-  const auto turn = [&](int a) { return bars + 104 + 8 * a; };
-  const auto pv_half = [&](int a) { return bars + 120 + 8 * a; };
-  const uint32_t merged = bars + 136;
-  const auto kv_full = [&](int s) { return bars + 144 + 8 * s; };
-  const auto kv_free = [&](int s) { return bars + 144 + 8 * C::kSlots + 8 * s; };
+  volatile int* s_abort = &s_abort_flag;
+  volatile int* s_bad = s_bad_flag;  // [2] V tile (the count of tiles not seen whole, % 2) holds a non-finite value
+  const uint32_t bars = smem_u32(s_bar);
+  const uint32_t q_full = bars, q_free = bars + 8, merged = bars + 16;
+  const auto pair = [&](int which, int b) { return bars + 24 + 16 * which + 8 * b; };
+  const auto s_full = [&](int b) { return pair(0, b); };    // scores of a step are there
+  const auto p_half = [&](int b) { return pair(1, b); };    // the first half of its weights
+  const auto p_ready = [&](int b) { return pair(2, b); };   // all of them
+  const auto pv_half = [&](int a) { return pair(3, a); };   // stream a's O holds the first half's product
+  const auto pv_done = [&](int a) { return pair(4, a); };   // and the second's
+  const auto check = [&](int b) { return pair(5, b); };     // a V tile may be checked
+  const auto checked = [&](int b) { return pair(6, b); };   // s_bad[b] is set
+  const auto turn = [&](int i) { return pair(7, i); };      // MMA warp i may issue
+  const auto o_free = [&](int a) { return pair(8, a); };    // stream a's O has been read
+  const auto item_full = [&](int x) { return pair(9, x); };
+  const auto item_free = [&](int x) { return pair(10, x); };
+  const auto kv_free = [&](int s) { return bars + 200 + 8 * s; };
+  // a ring slot's copy is there: for both MMA warps (two row tiles: both use every copy), else for the one
+  // that uses it, which thus sees every phase of a barrier
+  const auto kv_full = [&](int i, int s) { return bars + 200 + 8 * kSlots * (NQ == 1 ? 1 + i : 1) + 8 * s; };
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int G = p.group, Ppt = 128 / G;  // positions per row tile
-  const int kvh = blockIdx.x % p.hkv, slot = blockIdx.x / p.hkv;
 
-  if (warp == 0) {
+  const auto item_at = [&](int idx) {  // all lanes of a warp
     Item it;
-    const bool found = find_item(p, slot, NQ * Ppt, it);
-    if (lane == 0) {
-      *s_found = found;
-      if (found) *s_item = it;
-    }
-    if (blockIdx.x == 0) {
-      check_offsets(p.cu_q, p.n_seqs, p.total_q, p.hdr, lane, 32);
-      check_offsets(p.cu_k, p.n_seqs, p.total_k, p.hdr, lane, 32);
-    }
-  } else if (warp == C::kWarpMma) {
-    tmem_alloc(smem_u32(s_tmem), 512);
+    it.head = find_item(p, idx / p.hkv, NQ * Ppt, it) ? idx % p.hkv : -1;
+    return it;
+  };
+  Item it;  // the TMA warp's first one
+  if (warp == C::kWarpMma) {
+    tmem_alloc(smem_u32(&s_tmem), 512);
     tmem_relinquish();
-  } else if (warp == C::kWarpTma && lane == 0) {
+  } else if (warp == C::kWarpCheck && lane == 0) {
     *s_abort = 0;
     mbar_init(q_full, 1);
+    mbar_init(q_free, 2);
     mbar_init(merged, 8);
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
       mbar_init(p_half(b), 4);
       mbar_init(p_ready(b), 4);
+      mbar_init(pv_half(b), 1);
       mbar_init(pv_done(b), 1);
+      mbar_init(check(b), NQ);
       mbar_init(checked(b), 1);
       mbar_init(turn(b), 1);
-      mbar_init(pv_half(b), 1);
-      mbar_init(check(b), NQ);
+      mbar_init(o_free(b), M == kKeys ? 8 : 4);
+      mbar_init(item_full(b), 1);
+      mbar_init(item_free(b), C::kSoftWarps + 3);
     }
-    for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(kv_full(s), 1);
+    for (int s = 0; s < kSlots; ++s) {
+      for (int i = 0; i < 3 - NQ; ++i) mbar_init(kv_full(i, s), 1);
       mbar_init(kv_free(s), NQ);
     }
     fence_barrier_init();
-    prefetch_tmap(&maps.q);
-    prefetch_tmap(&maps.k);
-    prefetch_tmap(&maps.v);
+  } else if (warp == C::kWarpTma) {
+    if (lane == 0) {
+      prefetch_tmap(&maps.q);
+      prefetch_tmap(&maps.k);
+      prefetch_tmap(&maps.v);
+    }
+    it = item_at(blockIdx.x);
+    if (blockIdx.x == 0) {
+      check_offsets(p.cu_q, p.n_seqs, p.total_q, p.hdr, lane, 32);
+      check_offsets(p.cu_k, p.n_seqs, p.total_k, p.hdr, lane, 32);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
-  const bool found = *s_found;
+  const uint32_t tmem = s_tmem;
 
-  if (found) {
-    const Item it = *s_item;
-    // keys that the first and the last position of this CTA see
-    const int first_seen = p.causal ? min(max(it.pos0 + 1 + it.off, 0), it.lk) : it.lk;
-    const int last_seen = p.causal ? min(max(it.pos0 + it.n_pos + it.off, 0), it.lk) : it.lk;
-    const int nj = (last_seen + BN - 1) / BN, steps = NQ * nj;
-    const int j_masked = first_seen / BN;  // tiles from here on are not seen whole by every row
-    // Step n: key tile n / NQ, stream n % NT, the stream's step n / NT. The ring's order is the steps' order of
-    // use: K0 V0 K1 V1 ... with two row tiles (each used by two steps), else K0 K1 V0 K2 V1 ...
-    const auto k_idx = [&](int j) { return NQ == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
-    const auto v_idx = [&](int j) { return NQ == 2 ? 2 * j + 1 : (j == nj - 1 ? 2 * j + 1 : 2 * j + 2); };
+  // Every role walks the same items with the same running counts: r (ring entries used), nb (steps before
+  // this item: the global step number gives a step's S buffer, MMA warp, stream and barrier phases), x0
+  // (V tiles checked). Step n of an item: key tile n / NQ; global number nb + n. With two row tiles the
+  // ring's order is K0 V0 K1 V1 ... (each used by two steps), else K0 K1 V0 K2 V1 ...
+  const auto wait = [&](uint32_t bar, int parity) { return __all_sync(~0u, mbar_wait(bar, parity & 1, s_abort)); };
+  // the t-th item of this CTA; the slot is handed back
+  const auto take_item = [&](int t, Item& it) {
+    if (!wait(item_full(t & 1), t >> 1)) return false;
+    it = s_item[t & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_free(t & 1));
+    return it.head >= 0;
+  };
+  struct Span {
+    int nj, steps, masked;  // key tiles, steps, the first tile that not every row sees whole
+  };
+  const auto span = [&](const Item& it) {
+    const int first = p.causal ? min(max(it.pos0 + 1 + it.off, 0), it.lk) : it.lk;         // keys the first position sees
+    const int last = p.causal ? min(max(it.pos0 + it.n_pos + it.off, 0), it.lk) : it.lk;   // and the last
+    const int nj = (last + BN - 1) / BN;
+    return Span{nj, NQ * nj, first / BN};
+  };
+  const auto k_at = [&](int j) { return NQ == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
+  const auto v_at = [&](int j, int nj) { return NQ == 2 ? 2 * j + 1 : (j == nj - 1 ? 2 * j + 1 : 2 * j + 2); };
 
-    if (warp >= C::kSoftWarps) {
+  struct Entry {
+    bool v;
+    int j;
+  };
+  const auto tile_at = [](int i, int nj) {  // what the i-th entry holds
+    if (NQ == 2) return Entry{(i & 1) != 0, i / 2};
+    if (i == 2 * nj - 1) return Entry{true, nj - 1};
+    const bool v = i >= 2 && !(i & 1);
+    return Entry{v, v ? i / 2 - 1 : (i + 1) / 2};
+  };
+
+  if (warp >= C::kSoftWarps) {
     if (NT == 2) regs_for_issue();
     if (warp == C::kWarpTma) {
-      // ------------------------------------------------------------------ TMA producer
-      if (lane == 0 && steps) {
-        mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * C::kChunks * Ppt * G * 128));
-        for (int a = 0; a < NQ; ++a)
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d(smem_u32(smem) + a * C::kQTile + c * 16384, &maps.q, c * 64, kvh * G, it.q_row + a * Ppt, q_full);
-        int issued = 0;
-        for (; issued < 2 * nj; ++issued) {
-          const int i = issued, s = i % C::kSlots;
-          if (i >= C::kSlots && !mbar_wait(kv_free(s), ((i / C::kSlots) & 1) ^ 1, s_abort)) break;
-          bool is_v;
-          int j;
-          if (NQ == 2) {
-            is_v = i & 1;
-            j = i / 2;
-          } else if (i == 2 * nj - 1) {
-            is_v = true;
-            j = nj - 1;
-          } else {
-            is_v = i >= 2 && !(i & 1);
-            j = is_v ? i / 2 - 1 : (i + 1) / 2;
+      // ------------------------------------------------------------------ items and copies
+      int r = 0, nb = 0, q_used = 0;
+      bool ok = true;
+      for (int t = 0;; ++t) {
+        if (t >= 2 && !(ok = wait(item_free(t & 1), (t >> 1) + 1))) break;
+        if (lane == 0) {
+          s_item[t & 1] = it;
+          mbar_arrive(item_full(t & 1));
+        }
+        __syncwarp();
+        if (it.head < 0) {
+          // every CTA draws its last item before it arrives here: the last one puts the counts back
+          if (lane == 0 && atomicAdd(&p.hdr->pad[1], 1) == (int)gridDim.x - 1) {
+            p.hdr->pad[0] = 0;
+            p.hdr->pad[1] = 0;
           }
-          mbar_arrive_expect_tx(kv_full(s), (uint32_t)C::kSlot);
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d(smem_u32(ring) + s * C::kSlot + c * (BN * 128), is_v ? &maps.v : &maps.k, c * 64, kvh,
-                        it.k_row + j * BN, kv_full(s));
+          break;
         }
-        if (*s_abort) {  // copies in flight must land before the CTA's memory is given up
-          int none = 0;
-          mbar_wait(q_full, 0, &none);
-          for (int i = max(0, issued - C::kSlots); i < issued; ++i)
-            mbar_wait(kv_full(i % C::kSlots), (i / C::kSlots) & 1, &none);
+        int next = 0;
+        if (lane == 0) {
+          const Span sp = span(it);
+          if (sp.nj) {
+            ok = q_used == 0 || mbar_wait(q_free, (q_used & 1) ^ 1, s_abort);
+            if (ok) {
+              mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * C::kChunks * Ppt * G * 128));
+              for (int a = 0; a < NQ; ++a)
+                for (int c = 0; c < C::kChunks; ++c)
+                  tma_load_3d(smem_u32(smem) + a * C::kQTile + c * 16384, &maps.q, c * 64, it.head * G, it.q_row + a * Ppt,
+                              q_full);
+              ++q_used;
+            }
+          }
+          for (int i = 0; ok && i < 2 * sp.nj; ++i, ++r) {
+            const int s = r % kSlots;
+            if (r >= kSlots && !(ok = mbar_wait(kv_free(s), ((r / kSlots) & 1) ^ 1, s_abort))) break;
+            const Entry en = tile_at(i, sp.nj);
+            const uint32_t full = kv_full((nb + en.j) & 1, s);
+            mbar_arrive_expect_tx(full, (uint32_t)C::kSlot);
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_load_3d(smem_u32(ring) + s * C::kSlot + c * (BN * 128), en.v ? &maps.v : &maps.k, c * 64, it.head,
+                          it.k_row + en.j * BN, full);
+          }
+          nb += sp.steps;
+          next = atomicAdd(&p.hdr->pad[0], 1);  // drawn when all copies have been issued: the next free CTA's item
         }
+        if (!(ok = __all_sync(~0u, ok))) break;
+        it = item_at(gridDim.x + __shfl_sync(~0u, next, 0));
+      }
+      if (lane == 0 && *s_abort) {
+        // copies in flight must land before the CTA's memory is given up: nothing tells which barriers they
+        // complete any more, so give them their time (a copy takes microseconds)
+        const long long t0 = clock64();
+        while (clock64() - t0 < 20000000) __nanosleep(1000);
       }
     } else if (warp < C::kWarpMma + 2) {
-      // ------------------------------------------------------------------ MMA issuer of the steps n0, n0 + 2, ...
+      // ------------------------------------------------------------------ MMA issuer of every second step
       constexpr uint32_t kSChunk = BN * 128 / 16, kQChunk = 16384 / 16;
-      const int n0 = warp - C::kWarpMma, a = n0 % NT;
+      const int me = warp - C::kWarpMma, a = me % NT;
       const uint32_t idesc_s = idesc_f16(128, BN, false), idesc_o = idesc_f16(128, D, false) | kIdescBMn;
-      const uint64_t qd = sw128_desc(smem_u32(smem) + n0 % NQ * C::kQTile);
-      const auto wait = [&](uint32_t bar, int parity) { return __all_sync(~0u, mbar_wait(bar, parity & 1, s_abort)); };
-      const auto have_k = [&](int n) {
-        const int i = k_idx(n / NQ);
-        return wait(kv_full(i % C::kSlots), i / C::kSlots);
-      };
-      const auto scores = [&](int n) {
-        const int j = n / NQ, s = k_idx(j) % C::kSlots;
-        tc_fence_after();
-        const uint64_t kd = sw128_desc(smem_u32(ring) + s * C::kSlot);
+      const uint64_t qd = sw128_desc(smem_u32(smem) + me % NQ * C::kQTile);
+      int r = 0, nb = 0, x0 = 0, used = 0;  // used: items with keys before this one
+      uint32_t phases = 0;                  // of kv_full, a bit per slot
+      bool ok = true;
+      for (int t = 0; ok && take_item(t, it); ++t) {
+        const Span sp = span(it);
+        if (sp.nj == 0) continue;
+        const auto have = [&](int i) {  // ring entry r + i; each of this warp's entries once
+          const int s = (r + i) % kSlots;
+          const bool there = wait(kv_full(me, s), phases >> s);
+          phases ^= 1u << s;
+          return there;
+        };
+        const auto scores = [&](int n) {
+          const int j = n / NQ, s = (r + k_at(j)) % kSlots, b = (nb + n) & 1;
+          tc_fence_after();
+          const uint64_t kd = sw128_desc(smem_u32(ring) + s * C::kSlot);
 #pragma unroll
-        for (int c = 0; c < C::kChunks; ++c)
-          umma_f16_ss_k64_elect(tmem + (n & 1) * BN, qd + c * kQChunk, kd + c * kSChunk, idesc_s, c != 0);
-        umma_commit_elect(s_full(n & 1));
-        umma_commit_elect(kv_free(s));
-        // every copy before V tile j's into its slot has arrived (it is an earlier one than K tile j's), and
-        // this warp has read s_bad of tile j - 2: the check of V tile j may begin
-        if (j >= j_masked && lane == 0) mbar_arrive(check((j - j_masked) & 1));
-        __syncwarp();
-      };
-      bool ok = n0 < steps && wait(q_full, 0) && have_k(n0);
-      if (ok) scores(n0);
-      for (int n = n0; ok && n < steps; n += 2) {
-        const int j = n / NQ, i = v_idx(j), s = i % C::kSlots;
-        const bool more = n + 2 < steps;
-        if (!(ok = wait(kv_full(s), i / C::kSlots) && (!more || have_k(n + 2)) && wait(p_half(n & 1), n >> 1))) break;
-        if (n > 0 && !(ok = wait(turn(n0), n0 ? n >> 1 : (n >> 1) - 1))) break;
-        tc_fence_after();
-        const bool skip = j >= j_masked && s_bad[(j - j_masked) & 1];  // the softmax warps add this product
-        const uint64_t vd = sw128_mn_desc(smem_u32(ring) + s * C::kSlot, BN * 128);
-#pragma unroll
-        for (int kb = 0; kb < BN / 64; ++kb) {
-          if (kb == BN / 128) {
-            if (BN == 128) umma_commit_elect(pv_half(a));
-            if (!(ok = wait(p_ready(n & 1), n >> 1))) break;
-            tc_fence_after();
-          }
-          if (!skip)
-            umma_f16_ts_mn_k64_elect(tmem + C::kOCol + a * D, tmem + (n & 1) * BN + kb * 32, vd + kb * (64 * 128 / 16),
-                                     idesc_o, n / NT + kb != 0);
+          for (int c = 0; c < C::kChunks; ++c)
+            umma_f16_ss_k64_elect(tmem + b * BN, qd + c * kQChunk, kd + c * kSChunk, idesc_s, c != 0);
+          umma_commit_elect(s_full(b));
+          umma_commit_elect(kv_free(s));
+          if (n + 2 >= sp.steps) umma_commit_elect(q_free);
+        };
+        // V tile of step n, if not every row sees it whole, to the warp that checks it: it has arrived, and s_bad of
+        // two tiles before has been read (by this warp, or before its last turn)
+        const auto offer = [&](int n) {
+          const int j = n / NQ;
+          if (j < sp.masked) return true;
+          if (!have(v_at(j, sp.nj))) return false;
+          if (lane == 0) mbar_arrive(check((x0 + j - sp.masked) & 1));
+          __syncwarp();
+          return true;
+        };
+        const int n0 = (me - nb) & 1;
+        if (!(ok = wait(q_full, used))) break;
+        if (n0 >= sp.steps) {  // a single step, the other warp's
+          if (lane == 0) mbar_arrive(q_free);
+        } else if ((ok = have(k_at(n0 / NQ)))) {
+          scores(n0);
+          ok = offer(n0);
         }
-        if (!ok) break;
-        umma_commit_elect(pv_done(a));
-        umma_commit_elect(kv_free(s));
-        if (more) scores(n + 2);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(turn(1 - n0));
+        for (int n = n0; ok && n < sp.steps; n += 2) {
+          const int j = n / NQ, g = nb + n, s = (r + v_at(j, sp.nj)) % kSlots;
+          const bool more = n + 2 < sp.steps;
+          if (!(ok = (j >= sp.masked || have(v_at(j, sp.nj))) && (!more || have(k_at((n + 2) / NQ))) &&
+                     wait(p_half(g & 1), g >> 1)))
+            break;
+          if (n < NT && used && !(ok = wait(o_free(a), used - 1))) break;
+          if (g > 0 && !(ok = wait(turn(me), me ? g >> 1 : (g >> 1) - 1))) break;
+          tc_fence_after();
+          const bool skip = j >= sp.masked && s_bad[(x0 + j - sp.masked) & 1];  // the softmax warps add this product
+          const uint64_t vd = sw128_mn_desc(smem_u32(ring) + s * C::kSlot, BN * 128);
+#pragma unroll
+          for (int kb = 0; kb < BN / 64; ++kb) {
+            if (kb == BN / 128) {
+              if (BN == 128) umma_commit_elect(pv_half(a));
+              if (!(ok = wait(p_ready(g & 1), g >> 1))) break;
+              tc_fence_after();
+            }
+            if (!skip)
+              umma_f16_ts_mn_k64_elect(tmem + C::kOCol + a * D, tmem + (g & 1) * BN + kb * 32, vd + kb * (64 * 128 / 16),
+                                       idesc_o, n / NT + kb != 0);
+          }
+          if (!ok) break;
+          umma_commit_elect(pv_done(a));
+          umma_commit_elect(kv_free(s));
+          if (more) scores(n + 2);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(turn(1 - me));
+          __syncwarp();
+          if (more && !(ok = offer(n + 2))) break;
+        }
+        r += 2 * sp.nj;
+        nb += sp.steps;
+        x0 += sp.nj - sp.masked;
+        ++used;
       }
     } else if (warp == C::kWarpCheck) {
       // ------------------------------------------------------------------ V tiles not seen whole
-      for (int j = j_masked; j < nj; ++j) {
-        const int i = v_idx(j), s = i % C::kSlots, x = j - j_masked, b = x & 1;
-        if (!__all_sync(~0u, mbar_wait(check(b), (x >> 1) & 1, s_abort) && mbar_wait(kv_full(s), (i / C::kSlots) & 1, s_abort))) break;
-        const uint4* v = reinterpret_cast<const uint4*>(ring + s * C::kSlot);
-        uint32_t hit = 0;
+      int r = 0, x = 0;
+      bool ok = true;
+      for (int t = 0; ok && take_item(t, it); ++t) {
+        const Span sp = span(it);
+        for (int j = sp.masked; j < sp.nj; ++j, ++x) {
+          const int s = (r + v_at(j, sp.nj)) % kSlots, b = x & 1;
+          if (!(ok = wait(check(b), x >> 1))) break;
+          const uint4* v = reinterpret_cast<const uint4*>(ring + s * C::kSlot);
+          uint32_t hit = 0;
 #pragma unroll 8
-        for (int y = lane; y < C::kSlot / 16; y += 32) {
-          const uint4 w = v[y];
-          const uint32_t e = 0x7F807F80u, one = 0x00800080u;  // exponent 255: + 1 carries into the sign's place
-          hit |= ((w.x & e) + one) | ((w.y & e) + one) | ((w.z & e) + one) | ((w.w & e) + one);
+          for (int y = lane; y < C::kSlot / 16; y += 32) {
+            const uint4 w = v[y];
+            const uint32_t e = 0x7F807F80u, one = 0x00800080u;  // exponent 255: + 1 carries into the sign's place
+            hit |= ((w.x & e) + one) | ((w.y & e) + one) | ((w.z & e) + one) | ((w.w & e) + one);
+          }
+          const bool bad = __any_sync(~0u, hit & 0x80008000u);
+          if (lane == 0) {
+            s_bad[b] = bad;
+            mbar_arrive(checked(b));
+          }
         }
-        const bool bad = __any_sync(~0u, hit & 0x80008000u);
-        if (lane == 0) {
-          s_bad[b] = bad;
-          mbar_arrive(checked(b));
-        }
+        r += 2 * sp.nj;
       }
     }
-    } else {
-      // ------------------------------------------------------------------ softmax of row tile a
-      if (NT == 2) regs_for_softmax();
-      const int a = warp / 4, row = threadIdx.x & 127;
-      const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
-      const int pos = a % NQ * Ppt + row / G, head = kvh * G + row % G;
+  } else {
+    // ------------------------------------------------------------------ softmax of stream a
+    if (NT == 2) regs_for_softmax();
+    const int a = warp / 4, row = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
+    const uint32_t ot = lanes + C::kOCol + a * D;
+    int r = 0, nb = 0, x0 = 0, used = 0;
+    bool ok = true;
+    for (int t = 0; ok && take_item(t, it); ++t) {
+      const Span sp = span(it);
+      const int pos = a % NQ * Ppt + row / G, head = it.head * G + row % G;
       const bool valid = row < Ppt * G && pos < it.n_pos;
       // keys this row sees (rows of no position: all, so that they add no compares)
-      const int seen = !valid ? nj * BN : p.causal ? min(max(it.pos0 + pos + 1 + it.off, 0), it.lk) : it.lk;
+      const int seen = !valid ? sp.nj * BN : p.causal ? min(max(it.pos0 + pos + 1 + it.off, 0), it.lk) : it.lk;
       Softmax<D> soft(p.scale * kLog2e);
-      const uint32_t ot = lanes + C::kOCol + a * D;
       const auto grow = [&](float mx, bool first, uint32_t bar, int parity) {
         if (!__any_sync(~0u, mx > soft.m + soft.grown)) return true;
         const float f = soft.raise(mx);
         if (first) return true;
-        if (!__all_sync(~0u, mbar_wait(bar, parity & 1, s_abort))) return false;  // O is at rest
+        if (!wait(bar, parity)) return false;  // O is at rest
         tc_fence_after();
         soft.scale_o(ot, f);
         return true;
       };
-      bool ok = true;
-      for (int n = a; n < steps; n += NT) {
-        const int j = n / NQ, k = n / NT;  // key tile, step of this stream
-        const uint32_t st = lanes + (n & 1) * BN;
-        if (!(ok = __all_sync(~0u, mbar_wait(s_full(n & 1), (n >> 1) & 1, s_abort)))) break;
+      int last = -1;  // this stream's last step's number within the stream, over all items
+      for (int n = NT == 2 ? (a - nb) & 1 : 0; n < sp.steps; n += NT) {
+        const int j = n / NQ, g = nb + n, b = g & 1, k = NT == 2 ? g >> 1 : g;
+        const bool first = n < NT;
+        const uint32_t st = lanes + b * BN;
+        last = k;
+        if (!(ok = wait(s_full(b), g >> 1))) break;
         tc_fence_after();
-        if (BN == 128 && j < j_masked) {
-          // seen whole by every row: two halves, the second one's scores on their way while the first one's
-          // weights are made, the first one's product under way while the second one's are
-          float s0[64], s1[64];
-          tmem_ld32(st, s0);
-          tmem_ld32(st + 32, s0 + 32);
-          tmem_wait_ld32(s0);
-          tmem_wait_ld32(s0 + 32);
+        // Two halves (BN = 128): the second one's scores are on their way while the first one's weights are
+        // made, the first one's product is under way while the second one's are.
+        const bool masked = j >= sp.masked;
+        const int lim = seen - j * BN, x = x0 + j - sp.masked;
+        float s0[64], s1[64], mx = -INFINITY;
+        bool bad = false;
+        tmem_ld32(st, s0);
+        tmem_ld32(st + 32, s0 + 32);
+        tmem_wait_ld32(s0);
+        tmem_wait_ld32(s0 + 32);
+        if (BN == 128) {
           tmem_ld32(st + 64, s1);
           tmem_ld32(st + 96, s1 + 32);
-          if (!(ok = grow(max_of<64>(s0), k == 0, pv_done(a), k - 1))) break;
-          soft.template weights<64>(s0, st);
+        }
+        if (masked) unsee(s0, lim);
+        if (!(ok = grow(max_of<64>(s0), first, pv_done(a), k - 1))) break;
+        soft.weights(s0, st);
+        if (BN == 128) {
           tmem_wait_ld32(s1);
           tmem_wait_ld32(s1 + 32);
-          const float mx = max_of<64>(s1);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_half(n & 1));
-          if (!(ok = grow(mx, false, pv_half(a), k))) break;
-          soft.template weights<64>(s1, st + 32);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_ready(n & 1));
-          continue;
-        }
-        const int lim = seen - j * BN;
-        {
-          float s[BN];
-#pragma unroll
-          for (int i = 0; i < BN; i += 32) tmem_ld32(st + i, s + i);
-#pragma unroll
-          for (int i = 0; i < BN; i += 32) tmem_wait_ld32(s + i);
-          if (j >= j_masked) {
-#pragma unroll
-            for (int i = 0; i < BN; ++i) s[i] = i < lim ? s[i] : -INFINITY;
-          }
-          if (!(ok = grow(max_of<BN>(s), k == 0, pv_done(a), k - 1))) break;
-          soft.template weights<BN>(s, st);
+          if (masked) unsee(s1, lim - 64);
+          mx = max_of<64>(s1);
         }
         tmem_wait_st();
-        if (j >= j_masked) {
-          const int x = j - j_masked;
-          if (!(ok = __all_sync(~0u, mbar_wait(checked(x & 1), (x >> 1) & 1, s_abort)))) break;
-          if (s_bad[x & 1]) {
-            const int i = v_idx(j);
-            ok = mbar_wait(kv_full(i % C::kSlots), (i / C::kSlots) & 1, s_abort) &&
-                 (k == 0 || mbar_wait(pv_done(a), (k - 1) & 1, s_abort));
-            if (!(ok = __all_sync(~0u, ok))) break;
+        if (masked) {
+          if (!(ok = wait(checked(x & 1), x >> 1))) break;
+          bad = s_bad[x & 1];
+          if (bad) {
+            // O at rest: its last product, or (a new item's first) read by every warp
+            if (!(ok = first ? used == 0 || wait(o_free(a), used - 1) : wait(pv_done(a), k - 1))) break;
             tc_fence_after();
-            add_seen<D, BN>(ot, st, ring + (i % C::kSlots) * C::kSlot, lim, k == 0);
+            add_seen<D>(ot, st, ring + (r + v_at(j, sp.nj)) % kSlots * C::kSlot, BN * 128, lim, first);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(p_half(n & 1));
-          mbar_arrive(p_ready(n & 1));
+        if (lane == 0) mbar_arrive(p_half(b));
+        if (BN == 128) {
+          if (!(ok = grow(mx, false, pv_half(a), k))) break;
+          soft.weights(s1, st + 32);
+          tmem_wait_st();
+          if (bad)
+            add_seen<D>(ot, st + 32, ring + (r + v_at(j, sp.nj)) % kSlots * C::kSlot + 64 * 128, BN * 128, lim - 64, false);
+          tc_fence_before();
+          __syncwarp();
         }
+        if (lane == 0) mbar_arrive(p_ready(b));
       }
-      const int mine = (steps - a + NT - 1) / NT;  // steps of this stream
-      if (mine && ok) ok = __all_sync(~0u, mbar_wait(pv_done(a), (mine - 1) & 1, s_abort));
+      if (ok && last >= 0) ok = wait(pv_done(a), last);
       // the factor of O (and of the other stream's O) in the output, and the row's log sum
       float f = 0.f, f2 = 0.f, lse = -INFINITY;
       const float l = soft.sum();
-      if (M == kKeys) {
+      if (M == kKeys && sp.nj) {
         // both streams' O belong to the same rows (the same lanes): each warpgroup writes half the columns
         const float mc = l == 0.f ? -INFINITY : soft.mc;
+        if (ok && used) ok = wait(o_free(a), used - 1);  // the other warpgroup has read the last item's statistics
         s_stat[a][row] = make_float2(mc, l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(merged);
         __syncwarp();
-        if (ok) ok = __all_sync(~0u, mbar_wait(merged, 0, s_abort));
+        if (ok) ok = wait(merged, used);
         const float2 other = s_stat[1 - a][row];
         const float top = fmaxf(mc, other.x);
         if (l != 0.f || other.y != 0.f) {
@@ -518,41 +620,49 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         f = 1.f / l;
         lse = soft.mc * kLn2 + logf(l);
       }
-      if (ok) {
-        tc_fence_after();
-        constexpr int kCols = M == kKeys ? D / 2 : D;
-        const int col0 = M == kKeys ? a * kCols : 0;
-        const int64_t t = it.q_row + pos;
-        uint16_t* out = p.o + (t * p.hq + head) * D + col0;
-#pragma unroll
-        for (int i = 0; i < kCols; i += 32) {
-          float o[32], o2[32];
-          if (steps) {
-            tmem_ld32(ot + col0 + i, o);
-            if (M == kKeys) tmem_ld32(lanes + C::kOCol + (1 - a) * D + col0 + i, o2);
-            tmem_wait_ld32(o);
-            if (M == kKeys) tmem_wait_ld32(o2);
-          }
-          if (valid) {
-#pragma unroll
-            for (int x = 0; x < 32; x += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                // a factor of 0: nothing was written there
-                float u = f == 0.f ? 0.f : o[x + 2 * y] * f, v = f == 0.f ? 0.f : o[x + 2 * y + 1] * f;
-                if (M == kKeys && f2 != 0.f) {
-                  u = fmaf(o2[x + 2 * y], f2, u);
-                  v = fmaf(o2[x + 2 * y + 1], f2, v);
-                }
-                w[y] = bf16x2_rn(u, v);
-              }
-              *reinterpret_cast<uint4*>(out + i + x) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (!ok) break;
+      tc_fence_after();
+      constexpr int kCols = M == kKeys ? D / 2 : D;
+      const int col0 = M == kKeys ? a * kCols : 0;
+      const int64_t token = it.q_row + pos;
+      uint16_t* out = p.o + (token * p.hq + head) * D + col0;
+#pragma unroll 1
+      for (int i = 0; i < kCols; i += 16) {  // not unrolled: this code runs once per item, from a cold instruction cache
+        uint32_t o[16], o2[16];
+        if (sp.nj) {
+          tmem_ld16(ot + col0 + i, o);
+          if (M == kKeys) tmem_ld16(lanes + C::kOCol + (1 - a) * D + col0 + i, o2);
+          tmem_wait_ld();
+          if (i + 16 == kCols) {  // O may be overwritten
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(o_free(a));
+              if (M == kKeys) mbar_arrive(o_free(1 - a));
             }
           }
         }
-        if (valid && p.lse && (M != kKeys || a == 0)) p.lse[t * p.hq + head] = lse;
+        uint32_t w[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          // a factor of 0: nothing was written there
+          float u = f == 0.f ? 0.f : __uint_as_float(o[2 * y]) * f, v = f == 0.f ? 0.f : __uint_as_float(o[2 * y + 1]) * f;
+          if (M == kKeys && f2 != 0.f) {
+            u = fmaf(__uint_as_float(o2[2 * y]), f2, u);
+            v = fmaf(__uint_as_float(o2[2 * y + 1]), f2, v);
+          }
+          w[y] = bf16x2_rn(u, v);
+        }
+        if (valid) {
+          *reinterpret_cast<uint4*>(out + i) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(out + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
       }
+      if (valid && p.lse && (M != kKeys || a == 0)) p.lse[token * p.hq + head] = lse;
+      r += 2 * sp.nj;
+      nb += sp.steps;
+      x0 += max(sp.nj - sp.masked, 0);
+      used += sp.nj > 0;
     }
   }
 
@@ -563,6 +673,16 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && *s_abort) set_device_status(p.hdr, MOE_ERR_DEVICE_TIMEOUT);
+}
+
+int num_sms() {
+  static int n = [] {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      v = 1;
+    return v > 0 ? v : 1;
+  }();
+  return n;
 }
 
 // [tokens, heads, d] rows as (d, heads, tokens); one box is 64 values x box_heads x box_tokens.
@@ -595,29 +715,20 @@ cudaError_t launch(const AttnPrefillParams& p, cudaStream_t s) {
       !make_map(&maps.v, keys ? p.v : p.q, D, keys ? p.hkv : p.hq, keys ? p.total_k : p.total_q, 1, C::BN))
     return cudaErrorInvalidValue;
   // every sequence has at most one ragged tile
-  const int64_t tiles = (int64_t)p.total_q / (C::NQ * ppt) + (p.n_seqs < p.total_q ? p.n_seqs : p.total_q);
-  if (tiles * p.hkv > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  attn_prefill_kernel<D, M><<<(unsigned)(tiles * p.hkv), C::kThreads, C::kSmem, s>>>(p, maps);
+  const int64_t items = ((int64_t)p.total_q / (C::NQ * ppt) + (p.n_seqs < p.total_q ? p.n_seqs : p.total_q)) * p.hkv;
+  if (items > 0x40000000) return cudaErrorInvalidValue;
+  attn_prefill_kernel<D, M><<<(unsigned)(items < num_sms() ? items : num_sms()), C::kThreads, C::kSmem, s>>>(p, maps);
   return cudaGetLastError();
-}
-
-int num_sms() {
-  static int n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      v = 1;
-    return v > 0 ? v : 1;
-  }();
-  return n;
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int d, cudaStream_t s) {
-  // Two row tiles per CTA halve the K and V traffic; one row tile with its keys split halves the longest
-  // CTA. Measured at 16/2 heads of 128: 2048 tokens (0.8 CTAs of two row tiles per SM) 35.6 against 26.8 us
-  // split, 3000 tokens (1.2) 47.4 against 48.8 us, 16384 tokens 748 against 804 us.
-  const bool two = (int64_t)p.total_q / (2 * (128 / p.group)) * p.hkv >= num_sms();
+  // Two row tiles per CTA halve the K and V traffic and the items; one row tile with its keys split halves the
+  // longest item. Measured at 16/2 heads of 128: 2048 tokens (0.8 items of two row tiles per SM) 37.2 against
+  // 27.8 us split, 3000 tokens (1.2) 46.0 against 44.5, 4096 tokens (1.7) 59.4 against 67.9, 16384 tokens 745
+  // against 803 us.
+  const bool two = 5 * ((int64_t)p.total_q / (2 * (128 / p.group)) * p.hkv) >= 7 * (int64_t)num_sms();
   if (d == 64) return two ? launch<64, kRows>(p, s) : launch<64, kKeys>(p, s);
   if (d == 128) return two ? launch<128, kRows>(p, s) : launch<128, kKeys>(p, s);
   return launch<256, kOne>(p, s);
