@@ -36,7 +36,7 @@
 namespace moe {
 namespace {
 
-// With two row tiles the warpgroups share the block's registers out: 168 x 384 at launch, then 72 for
+// The warpgroups share the block's registers out: 168 x 384 at launch, then 72 for
 // the four issuing warps and 216 for each softmax thread (2 x 128 x 216 + 128 x 72 = 168 x 384).
 constexpr int kLaunchRegs = 168;
 __device__ __forceinline__ void regs_for_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
@@ -46,25 +46,28 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;
 
 // What a CTA's streams of steps are: two row tiles over the same keys, two halves of one row tile's keys
-// (even and odd tiles), or one row tile alone (D = 256: tensor memory holds one O).
+// (even and odd tiles), or one row tile alone (D = 256: tensor memory holds one O). In kOne both softmax
+// warpgroups work on every step, half of its keys each, and Q is copied to tensor memory: with 64 keys to a
+// tile, S = Q K^T reads three bytes of shared memory for each byte of K otherwise, and waits for them.
 enum Mode { kRows, kKeys, kOne };
 
 template <int D, Mode M>
 struct Cfg {
-  static constexpr int NT = M == kOne ? 1 : 2;         // streams: softmax warpgroups, O tiles
+  static constexpr int NT = M == kOne ? 1 : 2;         // streams of steps, O tiles
   static constexpr int NQ = M == kRows ? 2 : 1;        // row tiles
   static constexpr int BN = D == 256 ? 64 : 128;       // keys per tile
   static constexpr int kChunks = D / 64;               // 128-byte columns of a row
   static constexpr int kQTile = kChunks * 16384;       // one row tile
   static constexpr int kSlot = BN * D * 2;             // one K or V tile
-  static constexpr int kRoom = (M == kKeys ? 220 : 224) * 1024 - NQ * kQTile;  // kKeys: the streams' statistics
+  static constexpr int kRoom = 224 * 1024 - NQ * kQTile;  // all but the last 3 KB, which the kernel's own variables take
   static constexpr int kSlots = kRoom / kSlot < 8 ? kRoom / kSlot : 8;
-  static constexpr int kSmem = NQ * kQTile + kSlots * kSlot + 1024;  // + alignment
-  static constexpr int kSoftWarps = 4 * NT;
+  static constexpr int kSmem = NQ * kQTile + kSlots * kSlot;
+  static constexpr int kSoftWarps = 8;                 // a warpgroup per stream; kOne: one per half of a tile's keys
   static constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 2, kWarpCheck = kSoftWarps + 3;  // two MMA warps
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
   static constexpr uint32_t kOCol = 2 * BN;            // S buffers at 0 and BN, O tiles behind them
-  static_assert(kOCol + NT * D <= 512 && kSlots >= 4 && kSmem + (M == kKeys ? 4608 : 512) <= 232448, "on-chip memory");
+  static constexpr uint32_t kQCol = kOCol + D;         // kOne: Q
+  static_assert(kOCol + NT * D + (M == kOne ? D / 2 : 0) <= 512 && kSlots >= 4 && kSmem + 3072 <= 232448, "on-chip memory");
 };
 
 struct Maps {
@@ -155,9 +158,10 @@ __device__ __forceinline__ void add_seen(uint32_t o_tmem, uint32_t p_tmem, const
   }
 }
 
-__device__ __forceinline__ void unsee(float* s, int lim) {  // of 64 scores those from lim on
+template <int N>
+__device__ __forceinline__ void unsee(float* s, int lim) {  // of N scores those from lim on
 #pragma unroll
-  for (int i = 0; i < 64; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+  for (int i = 0; i < N; ++i) s[i] = i < lim ? s[i] : -INFINITY;
 }
 template <int N>
 __device__ __forceinline__ float max_of(const float* s) {
@@ -169,7 +173,6 @@ __device__ __forceinline__ float max_of(const float* s) {
 
 // One row's running softmax. Weights are relative to m, which follows the maximum only when that has
 // grown by more than 2^8.
-template <int D>
 struct Softmax {
   float c, grown;            // scale log2 e; the growth of a score that m follows
   float m = -INFINITY, mc = 0.f;  // mc = c m, 0 while m = -inf
@@ -187,9 +190,10 @@ struct Softmax {
     l[1] = mul2(l[1], f2);
     return f;
   }
+  template <int N>
   __device__ __forceinline__ void scale_o(uint32_t ot, float f) const {
 #pragma unroll 1
-    for (int i = 0; i < D; i += 16) {  // few values at a time: the scores are live; rarely run
+    for (int i = 0; i < N; i += 16) {  // few values at a time: the scores are live; rarely run
       uint32_t o[16];
       tmem_ld16(ot + i, o);
       tmem_wait_ld();
@@ -198,11 +202,12 @@ struct Softmax {
       tmem_st16(ot + i, o);
     }
   }
-  // The weights of 64 scores, as bf16 to tensor memory.
+  // The weights of N scores, as bf16 to tensor memory.
+  template <int N>
   __device__ __forceinline__ void weights(const float* s, uint32_t to) {
     const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
 #pragma unroll
-    for (int i = 0; i < 64; i += 32) {
+    for (int i = 0; i < N; i += 32) {
       uint32_t w[16];
 #pragma unroll
       for (int x = 0; x < 32; x += 2) {
@@ -229,13 +234,13 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
     attn_prefill_kernel(const __grid_constant__ AttnPrefillParams p, const __grid_constant__ Maps maps) {
   using C = Cfg<D, M>;
   constexpr int BN = C::BN, NT = C::NT, NQ = C::NQ, kSlots = C::kSlots;
-  extern __shared__ uint8_t raw[];
+  extern __shared__ __align__(1024) uint8_t smem[];  // the 128-byte swizzle repeats every 1024 bytes
   __shared__ float2 s_stat[M == kKeys ? 2 : 1][M == kKeys ? 128 : 1];  // m c and l of the streams' rows
+  __shared__ float s_half[2][2][M == kOne ? 128 : 1];  // kOne: the row maxima of half a tile's keys, of two steps
   __shared__ Item s_item[2];
   __shared__ int s_abort_flag, s_bad_flag[2];
   __shared__ uint32_t s_tmem;
-  __shared__ __align__(8) uint64_t s_bar[25 + (NQ == 1 ? 3 : 2) * kSlots];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  __shared__ __align__(8) uint64_t s_bar[30 + (NQ == 1 ? 3 : 2) * kSlots];
   uint8_t* ring = smem + NQ * C::kQTile;
   volatile int* s_abort = &s_abort_flag;
   volatile int* s_bad = s_bad_flag;  // [2] V tile (the count of tiles not seen whole, % 2) holds a non-finite value
@@ -253,10 +258,12 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
   const auto o_free = [&](int a) { return pair(8, a); };    // stream a's O has been read
   const auto item_full = [&](int x) { return pair(9, x); };
   const auto item_free = [&](int x) { return pair(10, x); };
-  const auto kv_free = [&](int s) { return bars + 200 + 8 * s; };
+  const uint32_t q_there = bars + 200;                              // kOne: Q is in tensor memory
+  const auto halves = [&](int w) { return bars + 208 + 8 * w; };    // kOne: the two warps of 32 rows have exchanged
+  const auto kv_free = [&](int s) { return bars + 240 + 8 * s; };
   // a ring slot's copy is there: for both MMA warps (two row tiles: both use every copy), else for the one
   // that uses it, which thus sees every phase of a barrier
-  const auto kv_full = [&](int i, int s) { return bars + 200 + 8 * kSlots * (NQ == 1 ? 1 + i : 1) + 8 * s; };
+  const auto kv_full = [&](int i, int s) { return bars + 240 + 8 * kSlots * (NQ == 1 ? 1 + i : 1) + 8 * s; };
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int G = p.group, Ppt = 128 / G;  // positions per row tile
@@ -273,18 +280,20 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
   } else if (warp == C::kWarpCheck && lane == 0) {
     *s_abort = 0;
     mbar_init(q_full, 1);
-    mbar_init(q_free, 2);
+    mbar_init(q_free, M == kOne ? 8 : 2);
+    mbar_init(q_there, 8);
+    for (int w = 0; w < 4; ++w) mbar_init(halves(w), 2);
     mbar_init(merged, 8);
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
-      mbar_init(p_half(b), 4);
-      mbar_init(p_ready(b), 4);
+      mbar_init(p_half(b), M == kOne ? 8 : 4);
+      mbar_init(p_ready(b), M == kOne ? 8 : 4);
       mbar_init(pv_half(b), 1);
       mbar_init(pv_done(b), 1);
       mbar_init(check(b), NQ);
       mbar_init(checked(b), 1);
       mbar_init(turn(b), 1);
-      mbar_init(o_free(b), M == kKeys ? 8 : 4);
+      mbar_init(o_free(b), M == kRows ? 4 : 8);
       mbar_init(item_full(b), 1);
       mbar_init(item_free(b), C::kSoftWarps + 3);
     }
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
   };
 
   if (warp >= C::kSoftWarps) {
-    if (NT == 2) regs_for_issue();
+    regs_for_issue();
     if (warp == C::kWarpTma) {
       // ------------------------------------------------------------------ items and copies
       int r = 0, nb = 0, q_used = 0;
@@ -427,10 +436,13 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
           const uint64_t kd = sw128_desc(smem_u32(ring) + s * C::kSlot);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
-            umma_f16_ss_k64_elect(tmem + b * BN, qd + c * kQChunk, kd + c * kSChunk, idesc_s, c != 0);
+            if (M == kOne)
+              umma_f16_ts_k64_elect(tmem + b * BN, tmem + C::kQCol + c * 32, kd + c * kSChunk, idesc_s, c != 0);
+            else
+              umma_f16_ss_k64_elect(tmem + b * BN, qd + c * kQChunk, kd + c * kSChunk, idesc_s, c != 0);
           umma_commit_elect(s_full(b));
           umma_commit_elect(kv_free(s));
-          if (n + 2 >= sp.steps) umma_commit_elect(q_free);
+          if (M != kOne && n + 2 >= sp.steps) umma_commit_elect(q_free);
         };
         // V tile of step n, if not every row sees it whole, to the warp that checks it: it has arrived, and s_bad of
         // two tiles before has been read (by this warp, or before its last turn)
@@ -443,9 +455,9 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
           return true;
         };
         const int n0 = (me - nb) & 1;
-        if (!(ok = wait(q_full, used))) break;
+        if (!(ok = wait(M == kOne ? q_there : q_full, used))) break;
         if (n0 >= sp.steps) {  // a single step, the other warp's
-          if (lane == 0) mbar_arrive(q_free);
+          if (M != kOne && lane == 0) mbar_arrive(q_free);
         } else if ((ok = have(k_at(n0 / NQ)))) {
           scores(n0);
           ok = offer(n0);
@@ -514,12 +526,28 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
       }
     }
   } else {
-    // ------------------------------------------------------------------ softmax of stream a
-    if (NT == 2) regs_for_softmax();
-    const int a = warp / 4, row = threadIdx.x & 127;
+    // ------------------------------------------------------------------ softmax of stream a, or of half the keys
+    regs_for_softmax();
+    const int wg = warp / 4, a = wg % NT, row = threadIdx.x & 127;
+    constexpr int kCols = M == kRows ? D : D / 2;  // of O, that this warpgroup scales (kOne) and writes
+    const int col0 = M == kRows ? 0 : wg * kCols;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
     const uint32_t ot = lanes + C::kOCol + a * D;
     int r = 0, nb = 0, x0 = 0, used = 0;
+    int exchanged = 0;  // kOne
+    // kOne: this thread's value and the other half's of the same row
+    const auto exchange = [&](float mine, float& other) {
+      const int b = exchanged & 1;
+      s_half[b][wg][row] = mine;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(halves(warp & 3));
+      if (!wait(halves(warp & 3), exchanged)) return false;
+      tc_fence_after();
+      other = s_half[b][1 - wg][row];
+      ++exchanged;
+      return true;
+    };
     bool ok = true;
     for (int t = 0; ok && take_item(t, it); ++t) {
       const Span sp = span(it);
@@ -527,16 +555,35 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
       const bool valid = row < Ppt * G && pos < it.n_pos;
       // keys this row sees (rows of no position: all, so that they add no compares)
       const int seen = !valid ? sp.nj * BN : p.causal ? min(max(it.pos0 + pos + 1 + it.off, 0), it.lk) : it.lk;
-      Softmax<D> soft(p.scale * kLog2e);
+      Softmax soft(p.scale * kLog2e);
       const auto grow = [&](float mx, bool first, uint32_t bar, int parity) {
         if (!__any_sync(~0u, mx > soft.m + soft.grown)) return true;
         const float f = soft.raise(mx);
         if (first) return true;
         if (!wait(bar, parity)) return false;  // O is at rest
         tc_fence_after();
-        soft.scale_o(ot, f);
+        soft.template scale_o<M == kOne ? kCols : D>(ot + (M == kOne ? col0 : 0), f);
         return true;
       };
+      if (M == kOne && sp.nj) {
+        // Q to tensor memory (every S of the last item has been made: its last scores have been read)
+        if (!(ok = wait(q_full, used))) break;
+#pragma unroll
+        for (int c = 0; c < C::kChunks / 2; ++c) {
+          const uint8_t* q = smem + (wg * (C::kChunks / 2) + c) * 16384 + row * 128;
+          uint4 v[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] = *reinterpret_cast<const uint4*>(q + ((x ^ (row & 7)) << 4));
+          tmem_st32(lanes + C::kQCol + (wg * (C::kChunks / 2) + c) * 32, reinterpret_cast<const uint32_t*>(v));
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(q_there);
+          mbar_arrive(q_free);
+        }
+      }
       int last = -1;  // this stream's last step's number within the stream, over all items
       for (int n = NT == 2 ? (a - nb) & 1 : 0; n < sp.steps; n += NT) {
         const int j = n / NQ, g = nb + n, b = g & 1, k = NT == 2 ? g >> 1 : g;
@@ -549,6 +596,33 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         // made, the first one's product is under way while the second one's are.
         const bool masked = j >= sp.masked;
         const int lim = seen - j * BN, x = x0 + j - sp.masked;
+        if constexpr (M == kOne) {
+          float s[32], other;
+          tmem_ld32(st + wg * 32, s);
+          tmem_wait_ld32(s);
+          if (masked) unsee<32>(s, lim - wg * 32);
+          const float mine = max_of<32>(s);
+          if (!(ok = exchange(mine, other) && grow(fmaxf(mine, other), first, pv_done(a), k - 1))) break;
+          soft.template weights<32>(s, st + wg * 16);
+          tmem_wait_st();
+          if (masked) {
+            if (!(ok = wait(checked(x & 1), x >> 1))) break;
+            if (s_bad[x & 1]) {
+              // both halves' weights are there, and O is at rest
+              if (!(ok = exchange(0.f, other) && (first ? used == 0 || wait(o_free(a), used - 1) : wait(pv_done(a), k - 1)))) break;
+              tc_fence_after();
+              add_seen<kCols>(ot + col0, st, ring + (r + v_at(j, sp.nj)) % kSlots * C::kSlot + wg * (C::kChunks / 2) * (BN * 128),
+                              BN * 128, lim, first);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(p_half(b));
+            mbar_arrive(p_ready(b));
+          }
+          continue;
+        }
         float s0[64], s1[64], mx = -INFINITY;
         bool bad = false;
         tmem_ld32(st, s0);
@@ -559,13 +633,13 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
           tmem_ld32(st + 64, s1);
           tmem_ld32(st + 96, s1 + 32);
         }
-        if (masked) unsee(s0, lim);
+        if (masked) unsee<64>(s0, lim);
         if (!(ok = grow(max_of<64>(s0), first, pv_done(a), k - 1))) break;
-        soft.weights(s0, st);
+        soft.template weights<64>(s0, st);
         if (BN == 128) {
           tmem_wait_ld32(s1);
           tmem_wait_ld32(s1 + 32);
-          if (masked) unsee(s1, lim - 64);
+          if (masked) unsee<64>(s1, lim - 64);
           mx = max_of<64>(s1);
         }
         tmem_wait_st();
@@ -584,7 +658,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         if (lane == 0) mbar_arrive(p_half(b));
         if (BN == 128) {
           if (!(ok = grow(mx, false, pv_half(a), k))) break;
-          soft.weights(s1, st + 32);
+          soft.template weights<64>(s1, st + 32);
           tmem_wait_st();
           if (bad)
             add_seen<D>(ot, st + 32, ring + (r + v_at(j, sp.nj)) % kSlots * C::kSlot + 64 * 128, BN * 128, lim - 64, false);
@@ -596,7 +670,8 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
       if (ok && last >= 0) ok = wait(pv_done(a), last);
       // the factor of O (and of the other stream's O) in the output, and the row's log sum
       float f = 0.f, f2 = 0.f, lse = -INFINITY;
-      const float l = soft.sum();
+      float l = soft.sum(), l_other;
+      if (M == kOne && sp.nj && ok && (ok = exchange(l, l_other))) l = wg ? l_other + l : l + l_other;
       if (M == kKeys && sp.nj) {
         // both streams' O belong to the same rows (the same lanes): each warpgroup writes half the columns
         const float mc = l == 0.f ? -INFINITY : soft.mc;
@@ -622,8 +697,6 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
       }
       if (!ok) break;
       tc_fence_after();
-      constexpr int kCols = M == kKeys ? D / 2 : D;
-      const int col0 = M == kKeys ? a * kCols : 0;
       const int64_t token = it.q_row + pos;
       uint16_t* out = p.o + (token * p.hq + head) * D + col0;
 #pragma unroll 1
@@ -658,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
           *reinterpret_cast<uint4*>(out + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
-      if (valid && p.lse && (M != kKeys || a == 0)) p.lse[token * p.hq + head] = lse;
+      if (valid && p.lse && (M == kRows || wg == 0)) p.lse[token * p.hq + head] = lse;
       r += 2 * sp.nj;
       nb += sp.steps;
       x0 += max(sp.nj - sp.masked, 0);
@@ -699,13 +772,12 @@ cudaError_t launch(const AttnPrefillParams& p, cudaStream_t s) {
   static cudaError_t attr = cudaFuncSetAttribute(attn_prefill_kernel<D, M>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (attr != cudaSuccess) return attr;
-  if (C::NT == 2) {  // the register split waits for ever unless the launch brings what it hands out
-    static int regs = [] {
-      cudaFuncAttributes a;
-      return cudaFuncGetAttributes(&a, attn_prefill_kernel<D, M>) == cudaSuccess ? a.numRegs : 0;
-    }();
-    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  }
+  // the register split waits for ever unless the launch brings what it hands out
+  static int regs = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, attn_prefill_kernel<D, M>) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
   const int ppt = 128 / p.group;
   Maps maps;
   // without keys no tile of K or V is read: any valid map will do
