@@ -74,7 +74,7 @@ struct AttnDecodeParams {
   float* lse;
   WsHeader* hdr;
   int4* splits;    // [kAttnMaxCtas] the head that begins in a CTA and ends in a later one: sequence, unit, CTAs (0: none)
-  float* parts;    // [kAttnMaxCtas][2] partial results of a CTA: 16 rows of d + 4 values, 16 m, 16 l
+  float* parts;    // [kAttnMaxCtas][2] partial results of a CTA: 16 rows of d values, 16 m, 16 l
   float* scratch;  // [kAttnMaxCtas * kAttnMaxWarps] partial rows of a warp
 };
 
@@ -86,7 +86,7 @@ struct AttnWs {
 };
 inline AttnWs attn_ws(const moe_attn_dims& d) {
   AttnWs w;
-  const size_t rows = (size_t)16 * (d.head_dim + 4) * 4;
+  const size_t rows = (size_t)16 * d.head_dim * 4;
   w.splits = sizeof(WsHeader);
   w.parts = w.splits + kAttnMaxCtas * sizeof(int4);
   w.scratch = w.parts + (size_t)kAttnMaxCtas * 2 * (rows + 128);

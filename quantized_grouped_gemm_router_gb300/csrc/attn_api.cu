@@ -138,9 +138,9 @@ int moe_attn_decode(const moe_kv_cache* cache, moe_heads_view q, const int32_t* 
     return MOE_ERR_INVALID_ARG;
   if (!aligned(lens, 4) || !aligned(page_table, 4) || !aligned(lse, 4) || !aligned(o, 16)) return MOE_ERR_MISALIGNED;
   if ((st = check_attn_ws(ws, ws_bytes, cache->dims)) || (st = check_view(q, cache->dims.head_dim))) return st;
-  // the kernel numbers the 16-row tiles of all sequences and heads in 31 bits
+  // the kernel numbers the 16-row tiles of all sequences and heads, and a few slots more a head, in 31 bits
   const int64_t units = cache->dims.n_kv_heads * ((cache->dims.n_q_heads / cache->dims.n_kv_heads + 15) / 16);
-  if (((int64_t)table_width * cache->page_size + 15) / 16 >= ((int64_t)1 << 31) / (units * n_seqs))
+  if (((int64_t)table_width * cache->page_size + 15) / 16 + 8 >= ((int64_t)1 << 31) / (units * n_seqs))
     return MOE_ERR_UNSUPPORTED_SHAPE;
   AttnDecodeParams p;
   p.q = q;

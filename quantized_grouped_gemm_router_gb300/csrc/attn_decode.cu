@@ -41,11 +41,21 @@ struct Cfg {
   static constexpr int kTile = 2 * TR * RB;         // K rows, then V rows
   static constexpr int kStages = 192 * 1024 / (NW * kTile);
   static constexpr int kRing = kStages * kTile;     // per warp
-  static constexpr int kStride = D + 4;             // floats between the heads of a partial O (bank spread)
-  static constexpr int kPart = 16 * kStride + 32;   // floats of a CTA's partial result: O, then 16 m and 16 l
+  static constexpr int kPartRows = 8 * NH * D;      // floats of a partial O
+  static constexpr int kPart = 16 * D + 32;         // a CTA's partial result in the workspace: O, then 16 m and 16 l
+  // A partial O that a warp leaves behind when it goes on to another sequence or head stays in the ring stage
+  // that it has just used up, which the ring then does without; with two stages it goes to the workspace.
+  static constexpr bool kHold = kStages >= 3 && kPartRows * 4 <= kTile;
   static constexpr int kSmem = NW * kRing;
-  static_assert(8 * NH * kStride * 4 <= kRing, "a partial O fits its warp's ring");
+  static_assert(kPartRows * 4 <= kRing, "a partial O fits its warp's ring");
 };
+
+// Where a partial O has value d of head h: heads follow each other, their columns turned so that the rows
+// of a store spread over the banks; groups of four values stay together.
+template <int D>
+__device__ __forceinline__ int part_at(int h, int d) {
+  return h * D + (d ^ ((h & 7) << 2));
+}
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -111,10 +121,14 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t w) {
 
 // The tiles in order: sequences, each with `units` (key-value head, 16 query heads of its group) in
 // turn, each with the sequence's tiles. Lengths are read 32 sequences at a time, one per lane. Every
-// member but len32 is the same in all lanes.
+// member but len32 is the same in all lanes. Work is dealt out in slots: a slot per tile, and kPad slots
+// behind each unit's tiles that stand for the cost of going on to another one (query rows, a partial
+// result: about as long as that many tiles take a warp), so that warps with such a change get fewer tiles.
+constexpr int kPad = 2;
 template <int TR>
 struct Walk {
   int b, u, t, len, nt;  // sequence, unit, tile; the sequence's length and tiles
+  int at;                // the tile's slot
   int base, len32;       // this lane's length: of sequence base + lane
 
   __device__ __forceinline__ static int length(const AttnDecodeParams& p, int b) {
@@ -131,39 +145,52 @@ struct Walk {
     len = __shfl_sync(~0u, len32, lane);
     nt = (len + TR - 1) / TR;
   }
-  // the tile `at` (counted from the group's first)
-  __device__ __forceinline__ void start(const AttnDecodeParams& p, int g, int at, int units) {
+  // The first tile in slots lo .. hi - 1; lo is in group g, whose slots begin at `before`. False: none.
+  __device__ __forceinline__ bool start(const AttnDecodeParams& p, int g, int before, int lo, int hi, int units) {
+    if (lo >= hi) return false;
     group(p, g);
     const int lane = threadIdx.x & 31;
-    const int tiles = (len32 + TR - 1) / TR;
-    int sum = tiles * units;
+    const int slots = unit_slots(len32) * units;
+    int sum = slots;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
       const int y = __shfl_up_sync(~0u, sum, x);
       if (lane >= x) sum += y;
     }
-    const int src = __ffs(__ballot_sync(~0u, sum > at)) - 1;
-    at -= __shfl_sync(~0u, sum - tiles * units, src);
+    int off = lo - before;
+    const int src = __ffs(__ballot_sync(~0u, sum > off)) - 1;
+    off -= __shfl_sync(~0u, sum - slots, src);
     seq(src);
-    u = at / nt;
-    t = at % nt;
+    u = off / (nt + kPad);
+    t = off % (nt + kPad);
+    at = lo;
+    return t < nt || skip(p, hi, units);
   }
-  __device__ __forceinline__ void next(const AttnDecodeParams& p, int units) {
-    if (++t < nt) return;
+  __device__ __forceinline__ static int unit_slots(int len) { return len > 0 ? (len + TR - 1) / TR + kPad : 0; }
+  // From tile t of its unit, or a slot behind its tiles, to the next unit's first tile.
+  __device__ __forceinline__ bool skip(const AttnDecodeParams& p, int hi, int units) {
+    at += nt + kPad - t;
+    if (at >= hi) return false;
     t = 0;
-    if (++u < units) return;
+    if (++u < units) return true;
     u = 0;
     unsigned rest = __ballot_sync(~0u, len32 > 0) & ~((2u << (b - base)) - 1);
     while (!rest) {
-      if (base + 32 >= p.n_seqs) return;  // past the last tile
+      if (base + 32 >= p.n_seqs) return false;  // past the last tile
       group(p, base / 32 + 1);
       rest = __ballot_sync(~0u, len32 > 0);
     }
     seq(__ffs(rest) - 1);
+    return true;
+  }
+  __device__ __forceinline__ bool next(const AttnDecodeParams& p, int hi, int units) {
+    if (++t < nt) return ++at < hi;
+    --t;
+    return skip(p, hi, units);
   }
 };
 
-// A partial result of a warp: of the tiles of unit u of sequence b, which are nt tiles from number
+// A partial result of a warp: of the tiles of unit u of sequence b, which are nt tiles from slot
 // `begin` of all on; whether the first and the last of them are in it.
 struct PartInfo {
   int b, u, begin, nt, first, last;  // b = -1: none
@@ -227,7 +254,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
   using C = Cfg<D, E4M3, NH>;
   constexpr int RB = C::RB, TR = C::TR, NW = C::NW, TH = 32 * NW;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_before[kMaxGroups + 1];  // tiles before each group of 32 sequences
+  __shared__ int s_before[kMaxGroups + 1];  // slots before each group of 32 sequences
   __shared__ PartInfo s_part[2 * NW];
   __shared__ float s_ml[2 * NW][32];
   __shared__ int s_order[2 * NW];  // the partial results there are, in tile order
@@ -235,6 +262,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int nhb = (p.group + 15) / 16, units = p.hkv * nhb;
   pdl_launch_dependents();
+  pdl_wait();
 
   // ---- the tiles of all sequences
   const int groups = (p.n_seqs + 31) / 32;
@@ -251,10 +279,10 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
       if (p.lse)
         for (int h = lane; h < p.hq; h += 32) p.lse[e * p.hq + h] = -INFINITY;
     }
-    int tiles = (n + TR - 1) / TR;
+    int slots = Walk<TR>::unit_slots(n);
 #pragma unroll
-    for (int x = 16; x; x >>= 1) tiles += __shfl_xor_sync(~0u, tiles, x);
-    if (lane == 0) s_before[g + 1] = tiles * units;
+    for (int x = 16; x; x >>= 1) slots += __shfl_xor_sync(~0u, slots, x);
+    if (lane == 0) s_before[g + 1] = slots * units;
   }
   if (threadIdx.x < 2 * NW) s_part[threadIdx.x].b = -1;
   if (threadIdx.x == 0) s_before[0] = 0;
@@ -283,24 +311,24 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
     __syncthreads();
   }
   const unsigned total = s_before[groups];
-  const unsigned per = max((total + gridDim.x * NW - 1) / (gridDim.x * NW), 1u);  // tiles per warp
+  const unsigned per = max((total + gridDim.x * NW - 1) / (gridDim.x * NW), 1u);  // slots per warp
   const unsigned lo = min((blockIdx.x * NW + warp) * per, total), hi = min(lo + per, total);
-  const int n = (int)(hi - lo);
   if (threadIdx.x == 0) p.splits[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (blockIdx.x * NW * per >= total) return;
 
   uint8_t* ring = smem + warp * C::kRing;
   const uint32_t ring_s = smem_u32(ring);
-  float* scratch = p.scratch + (int64_t)(blockIdx.x * NW + warp) * (16 * C::kStride);
+  float* scratch = p.scratch + (int64_t)(blockIdx.x * NW + warp) * (16 * D);
 
-  if (n > 0) {
+  {
     int g = 0;
     for (int x = lane; x < groups; x += 32) g += s_before[x + 1] <= (int)lo;
 #pragma unroll
     for (int x = 16; x; x >>= 1) g += __shfl_xor_sync(~0u, g, x);
     Walk<TR> w, ld;
-    w.start(p, g, (int)lo - s_before[g], units);
+    bool any = w.start(p, g, s_before[g], (int)lo, (int)hi, units);
     ld = w;
+    if (any) {
 
     // ---- copies: the pages of the next tile to copy are already in `page`
     const int row = lane & (TR - 1);  // the tile row whose place this lane looks up
@@ -314,9 +342,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
     const uint8_t* kc = static_cast<const uint8_t*>(p.kc) + (lane % CPR) * 16;
     const uint8_t* vc = static_cast<const uint8_t*>(p.vc) + (lane % CPR) * 16;
     int page = page_of();
-    int left = n;  // tiles not yet copied
+    bool left = true;  // there is a tile to copy
     const auto issue = [&](int stage) {
-      if (left > 0) {
+      if (left) {
         const int pos = ld.t * TR + row;
         int cell = -1;  // this lane's cache row
         if (pos < ld.len) {
@@ -335,10 +363,8 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
           cp16(at, kc + off, all || c >= 0);
           cp16(at + TR * RB, vc + off, all || c >= 0);
         }
-        if (--left > 0) {
-          ld.next(p, units);
-          page = page_of();
-        }
+        left = ld.next(p, (int)hi, units);
+        if (left) page = page_of();
       }
       cp_commit();
     };
@@ -369,9 +395,21 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
     load_q(w);
     bool fresh = true, from_start = false;
     int out = 0, stage = 0, fill = C::kStages - 1;
-    for (int i = 0; i < n; ++i) {
-      issue(fill);
-      if (++fill == C::kStages) fill = 0;
+    int held = -1;      // kHold: the stage that keeps a partial O
+    bool rest = false;  // kHold: nothing to issue this time, the ring has just lost a stage
+    const auto after = [&](int x) {
+      x = x + 1 == C::kStages ? 0 : x + 1;
+      if (C::kHold && x == held) x = x + 1 == C::kStages ? 0 : x + 1;
+      return x;
+    };
+    while (any) {
+      if (C::kHold && rest) {
+        cp_commit();
+        rest = false;
+      } else {
+        issue(fill);
+        fill = after(fill);
+      }
       const int kvh = w.u / nhb, h0 = (w.u % nhb) * 16, heads = min(16, p.group - h0);
       if (fresh) {
         // ---- a new sequence or head; its query rows have been loaded
@@ -465,10 +503,8 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
       const bool to_end = w.t == w.nt - 1;
       const int lim = w.len - w.t * TR;
       Walk<TR> nx = w;
-      if (i < n - 1) {
-        nx.next(p, units);
-        if (to_end) load_q(nx);  // while the rest of this tile is worked on
-      }
+      any = nx.next(p, (int)hi, units);
+      if (any && to_end) load_q(nx);  // while the rest of this tile is worked on
       if (lim < TR) {
 #pragma unroll
         for (int kb = 0; kb < TR / 16; ++kb)
@@ -578,13 +614,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
           }
         }
       }
-      if (++stage == C::kStages) stage = 0;
+      const int used = stage;
       __syncwarp();
 
       // ---- the end of a sequence's head, or of this warp's run
-      if (to_end || i == n - 1) {
-        const bool whole = to_end && from_start, mid = i < n - 1;
-        float* to = mid ? scratch : reinterpret_cast<float*>(ring);
+      if (to_end || !any) {
+        const bool whole = to_end && from_start, mid = any;
+        float* to = !mid ? reinterpret_cast<float*>(ring + (C::kHold && held == 0 ? C::kTile : 0))
+                    : C::kHold ? reinterpret_cast<float*>(ring + used * C::kTile) : scratch;
         if (!whole && !mid) {
           cp_wait<0>();  // the ring is idle: every copy has landed and been used
           __syncwarp();
@@ -620,7 +657,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
                 const int d = !E4M3     ? 16 * x + g8 + 8 * (y >> 1)
                               : D == 64 ? 8 * g8 + 2 * x + (y >> 1)
                                         : 128 * (x / 8) + 16 * slot + 2 * (x % 8) + (y >> 1);
-                if (h < heads) to[h * C::kStride + d] = o[nh][x][y];
+                if (h < heads) to[part_at<D>(h, d)] = o[nh][x][y];
               }
           } else if (!E4M3) {
 #pragma unroll
@@ -645,14 +682,21 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
           }
         }
         if (!whole) {
-          if (lane == 0) s_part[warp * 2 + out] = PartInfo{w.b, w.u, (int)lo + i - w.t, w.nt, from_start, to_end, to};
+          if (lane == 0) s_part[warp * 2 + out] = PartInfo{w.b, w.u, w.at - w.t, w.nt, from_start, to_end, to};
           ++out;
+          if (C::kHold && mid) {
+            held = used;
+            rest = true;
+            fill = after(used);
+          }
         }
         fresh = true;
       }
+      stage = after(used);
       w = nx;
     }
     cp_wait<0>();
+    }
   }
   __syncthreads();
 
@@ -677,17 +721,17 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
       Sum4 sum;
       sum.add(0, 1, cnt, [&](int i, float4& x, float& xm, float& xl) {
         const int y = s_order[at + i];
-        x = *reinterpret_cast<const float4*>(s_part[y].o + h * C::kStride + c * 4);
+        x = *reinterpret_cast<const float4*>(s_part[y].o + part_at<D>(h, c * 4));
         xm = s_ml[y][h];
         xl = s_ml[y][16 + h];
       });
       if (first && last) {
         sum.finish<D>(p, (int64_t)b * p.hq + kvh * p.group + h0 + h, c, E4M3 ? __ldg(p.v_scale + kvh) : 1.f);
       } else {
-        *reinterpret_cast<float4*>(to + h * C::kStride + c * 4) = sum.acc;
+        *reinterpret_cast<float4*>(to + part_at<D>(h, c * 4)) = sum.acc;
         if (c == 0) {
-          to[16 * C::kStride + h] = sum.m;
-          to[16 * C::kStride + 16 + h] = sum.l;
+          to[16 * D + h] = sum.m;
+          to[16 * D + 16 + h] = sum.l;
         }
       }
     }
@@ -705,6 +749,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   constexpr int V = D / 4, R = 256 / V;
   __shared__ float4 s_acc[R][V];
   __shared__ float s_ml[R][2];
+  pdl_launch_dependents();
   pdl_wait();
   const int4 split = p.splits[blockIdx.x];
   const int n = split.z;
@@ -716,9 +761,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   sum.add(r, R, n, [&](int i, float4& x, float& xm, float& xl) {
     // CTA blockIdx.x + i: its partial of a head that begins there (1) or before (0)
     const float* o = p.parts + (int64_t)((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * C::kPart;
-    x = *reinterpret_cast<const float4*>(o + h * C::kStride + c * 4);
-    xm = o[16 * C::kStride + h];
-    xl = o[16 * C::kStride + 16 + h];
+    x = *reinterpret_cast<const float4*>(o + part_at<D>(h, c * 4));
+    xm = o[16 * D + h];
+    xl = o[16 * D + 16 + h];
   });
   s_acc[r][c] = sum.acc;
   if (c == 0) {
@@ -752,8 +797,8 @@ cudaError_t launch(const AttnDecodeParams& p, cudaStream_t s) {
   static cudaError_t attr = cudaFuncSetAttribute(attn_decode_kernel<D, E4M3, NH>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (attr != cudaSuccess) return attr;
-  attn_decode_kernel<D, E4M3, NH><<<num_sms(), 32 * C::NW, C::kSmem, s>>>(p);
-  const cudaError_t err = cudaGetLastError();
+  const cudaError_t err =
+      launch_pdl(attn_decode_kernel<D, E4M3, NH>, dim3(num_sms()), 32 * C::NW, (size_t)C::kSmem, 1, s, p);
   if (err != cudaSuccess) return err;
   return launch_pdl(attn_join_kernel<D, E4M3, NH>, dim3(num_sms(), p.group < 16 ? p.group : 16), 256, 0, 1, s, p);
 }
