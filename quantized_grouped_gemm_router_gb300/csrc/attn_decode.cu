@@ -10,8 +10,8 @@
 //    The other partial results are joined by weight 2^(m - max m), in tile order: those of one CTA
 //    through shared memory, those of several CTAs by a second kernel, one CTA per head, which is
 //    launched early (programmatic dependent launch) and waits for the first.
-//  * Loads in flight. Each warp has a ring of its own, filled by 16-byte asynchronous copies two tiles
-//    ahead (8 warps x 2 x 8 KB per SM), with no barrier between warps. The page numbers of a tile are
+//  * Loads in flight. Each warp has a ring of its own, filled by 16-byte asynchronous copies a tile
+//    ahead (8 warps x 8 KB per SM), with no barrier between warps. The page numbers of a tile are
 //    read one tile earlier still. Rows past a sequence's end are filled with zeros, so what lies there
 //    is never used.
 //
@@ -36,16 +36,15 @@ template <int D, bool E4M3, int NH>
 struct Cfg {
   static constexpr int RB = D * (E4M3 ? 1 : 2);     // bytes of a cache row
   static constexpr int TR = RB <= 128 ? 32 : 16;    // rows of a tile
-  // warps: as many as the registers allow where a tile takes most instructions for its bytes
+  // Warps and ring stages: one tile ahead per warp, about 64 KB on their way per SM. More in flight is slower:
+  // 75 sequences of 8300 rows (heads of 128, bf16) take 110 us with two tiles ahead, 104 with one. 64-byte rows
+  // take most instructions for their bytes: 16 warps (43 against 55 us with 8).
   static constexpr int NW = RB == 512 ? (NH == 1 ? 6 : 4) : RB == 64 && NH == 1 ? 16 : 8;
   static constexpr int kTile = 2 * TR * RB;         // K rows, then V rows
-  static constexpr int kStages = 192 * 1024 / (NW * kTile);
+  static constexpr int kStages = 2;
   static constexpr int kRing = kStages * kTile;     // per warp
   static constexpr int kPartRows = 8 * NH * D;      // floats of a partial O
   static constexpr int kPart = 16 * D + 32;         // a CTA's partial result in the workspace: O, then 16 m and 16 l
-  // A partial O that a warp leaves behind when it goes on to another sequence or head stays in the ring stage
-  // that it has just used up, which the ring then does without; with two stages it goes to the workspace.
-  static constexpr bool kHold = kStages >= 3 && kPartRows * 4 <= kTile;
   static constexpr int kSmem = NW * kRing;
   static_assert(kPartRows * 4 <= kRing, "a partial O fits its warp's ring");
 };
@@ -311,10 +310,16 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
     __syncthreads();
   }
   const unsigned total = s_before[groups];
-  const unsigned per = max((total + gridDim.x * NW - 1) / (gridDim.x * NW), 1u);  // slots per warp
-  const unsigned lo = min((blockIdx.x * NW + warp) * per, total), hi = min(lo + per, total);
+  // warp x of all has `base` slots, one more if x < more
+  const unsigned warps = gridDim.x * NW, base = total / warps, more = total % warps;
+  const auto slot_of = [&](unsigned x) { return x * base + min(x, more); };
+  const auto cta_of = [&](unsigned slot) {
+    const unsigned x = slot < more * (base + 1) ? slot / (base + 1) : more + (slot - more * (base + 1)) / base;
+    return (int)(x / NW);
+  };
+  const unsigned lo = slot_of(blockIdx.x * NW + warp), hi = slot_of(blockIdx.x * NW + warp + 1);
   if (threadIdx.x == 0) p.splits[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (blockIdx.x * NW * per >= total) return;
+  if (slot_of(blockIdx.x * NW) >= total) return;
 
   uint8_t* ring = smem + warp * C::kRing;
   const uint32_t ring_s = smem_u32(ring);
@@ -395,21 +400,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
     load_q(w);
     bool fresh = true, from_start = false;
     int out = 0, stage = 0, fill = C::kStages - 1;
-    int held = -1;      // kHold: the stage that keeps a partial O
-    bool rest = false;  // kHold: nothing to issue this time, the ring has just lost a stage
-    const auto after = [&](int x) {
-      x = x + 1 == C::kStages ? 0 : x + 1;
-      if (C::kHold && x == held) x = x + 1 == C::kStages ? 0 : x + 1;
-      return x;
-    };
     while (any) {
-      if (C::kHold && rest) {
-        cp_commit();
-        rest = false;
-      } else {
-        issue(fill);
-        fill = after(fill);
-      }
+      issue(fill);
+      if (++fill == C::kStages) fill = 0;
       const int kvh = w.u / nhb, h0 = (w.u % nhb) * 16, heads = min(16, p.group - h0);
       if (fresh) {
         // ---- a new sequence or head; its query rows have been loaded
@@ -614,14 +607,13 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
           }
         }
       }
-      const int used = stage;
+      if (++stage == C::kStages) stage = 0;
       __syncwarp();
 
       // ---- the end of a sequence's head, or of this warp's run
       if (to_end || !any) {
         const bool whole = to_end && from_start, mid = any;
-        float* to = !mid ? reinterpret_cast<float*>(ring + (C::kHold && held == 0 ? C::kTile : 0))
-                    : C::kHold ? reinterpret_cast<float*>(ring + used * C::kTile) : scratch;
+        float* to = mid ? scratch : reinterpret_cast<float*>(ring);
         if (!whole && !mid) {
           cp_wait<0>();  // the ring is idle: every copy has landed and been used
           __syncwarp();
@@ -636,7 +628,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
             sum += __shfl_xor_sync(~0u, sum, 4);
             sum += __shfl_xor_sync(~0u, sum, 8);
             sum += __shfl_xor_sync(~0u, sum, 16);
-            inv[y] = sum == 0.f ? 0.f : (E4M3 ? __ldg(p.v_scale + kvh) : 1.f) / sum;
+            inv[y] = !whole || sum == 0.f ? 0.f : (E4M3 ? __ldg(p.v_scale + kvh) : 1.f) / sum;
             if (lane < 4 && h < heads) {
               if (!whole) {
                 s_ml[warp * 2 + out][h] = m[nh][y] == -INFINITY ? -INFINITY : mc[nh][y];
@@ -684,15 +676,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
         if (!whole) {
           if (lane == 0) s_part[warp * 2 + out] = PartInfo{w.b, w.u, w.at - w.t, w.nt, from_start, to_end, to};
           ++out;
-          if (C::kHold && mid) {
-            held = used;
-            rest = true;
-            fill = after(used);
-          }
         }
         fresh = true;
       }
-      stage = after(used);
       w = nx;
     }
     cp_wait<0>();
@@ -737,7 +723,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
     }
     at += cnt;
     // a head that begins here and goes on in the next CTAs, up to the one that holds its last tile
-    if (threadIdx.x == 0 && first && !last) p.splits[blockIdx.x] = make_int4(b, u, (int)(end / (per * NW)) - blockIdx.x + 1, 0);
+    if (threadIdx.x == 0 && first && !last) p.splits[blockIdx.x] = make_int4(b, u, cta_of(end) - (int)blockIdx.x + 1, 0);
   }
 }
 
