@@ -23,20 +23,6 @@ struct AttnPrefillParams {
   WsHeader* hdr;
 };
 
-struct KvAppendParams {
-  moe_heads_view k, v;
-  const int32_t* cu;
-  const int32_t* start;
-  const int32_t* table;
-  int table_width, n_seqs, total;
-  int hkv, d, page_size, n_pages, e4m3;
-  void* kc;
-  void* vc;
-  const float* k_scale;
-  const float* v_scale;
-  WsHeader* hdr;
-};
-
 // Division by an invariant: n / d = (t + ((n - t) >> s1)) >> s2 with t = the high half of m n, for every
 // 32-bit n (Granlund and Montgomery, Division by Invariant Integers using Multiplication).
 struct FastDiv {
@@ -55,6 +41,24 @@ struct FastDiv {
     return (t + ((n - t) >> s1)) >> s2;
   }
 #endif
+};
+
+struct KvAppendParams {
+  moe_heads_view k, v;
+  const int32_t* cu;
+  const int32_t* start;
+  const int32_t* table;
+  int table_width, n_seqs, total;
+  int hkv, d, page_size, n_pages, e4m3;
+  void* kc;
+  void* vc;
+  const float* k_scale;
+  const float* v_scale;
+  WsHeader* hdr;
+  FastDiv page_div;
+  // set at launch: heads head0 .. head0 + heads - 1, threads to a token, tokens to a block, log2(d / 8)
+  int head0, heads, tpt, tokens, log_dp;
+  FastDiv div_tpt;
 };
 
 struct AttnDecodeParams {

@@ -121,6 +121,7 @@ int moe_kv_append(const moe_kv_cache* cache, moe_heads_view k, moe_heads_view v,
   p.page_size = cache->page_size;
   p.n_pages = cache->n_pages;
   p.e4m3 = cache->format == MOE_KV_E4M3;
+  p.page_div = FastDiv(cache->page_size);
   p.kc = cache->k;
   p.vc = cache->v;
   p.k_scale = cache->k_scale;

@@ -411,7 +411,7 @@ def test_cache_far_offsets(m, fp8):
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("new,start,page", [([1], [0], 16), ([3, 0, 40, 1], [5, 9, 14, 0], 16), ([1] * 70, list(range(70)), 32),
                                             ([200, 7], [1000, 3], 7)], ids=["one", "ragged", "tokens", "long"])
-@pytest.mark.parametrize("hkv,d", [(2, 128), (1, 64), (3, 256), (5, 64)])
+@pytest.mark.parametrize("hkv,d", [(2, 128), (1, 64), (3, 256), (5, 64), (8, 128), (40, 128)])
 def test_append(m, hkv, d, new, start, page, fp8):
     dims = m.AttnDims(hkv, hkv, d)
     lens = [a + b for a, b in zip(new, start)]
