@@ -371,14 +371,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
           mbar_arrive(item_full(t & 1));
         }
         __syncwarp();
-        if (it.head < 0) {
-          // every CTA draws its last item before it arrives here: the last one puts the counts back
-          if (lane == 0 && atomicAdd(&p.hdr->pad[1], 1) == (int)gridDim.x - 1) {
-            p.hdr->pad[0] = 0;
-            p.hdr->pad[1] = 0;
-          }
-          break;
-        }
+        if (it.head < 0) break;
         int next = 0;
         if (lane == 0) {
           const Span sp = span(it);
@@ -408,6 +401,11 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         }
         if (!(ok = __all_sync(~0u, ok))) break;
         it = item_at(gridDim.x + __shfl_sync(~0u, next, 0));
+      }
+      // this CTA draws no more (after a wait that gave up, too): the last one to say so puts the counts back
+      if (lane == 0 && atomicAdd(&p.hdr->pad[1], 1) == (int)gridDim.x - 1) {
+        p.hdr->pad[0] = 0;
+        p.hdr->pad[1] = 0;
       }
       if (lane == 0 && *s_abort) {
         // copies in flight must land before the CTA's memory is given up: nothing tells which barriers they
