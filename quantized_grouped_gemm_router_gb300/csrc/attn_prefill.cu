@@ -699,15 +699,26 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const int64_t token = it.q_row + pos;
+      // kKeys: both streams' O, or that of the only one that had a step
+      const bool both = M == kKeys && sp.steps > 1;
+      const bool others = M == kKeys && sp.steps == 1 && last < 0;
+      const uint32_t other_o = lanes + C::kOCol + (NT - 1 - a) * D;
+      const uint32_t src = (others ? other_o : ot) + col0;
+      const float fa = others ? f2 : f;
+      const uint64_t ff = pack2(fa, fa), ff2 = pack2(f2, f2);
       uint16_t* out = p.o + (token * p.hq + head) * D + col0;
+      constexpr int kPiece = M == kKeys || kCols < 64 ? 32 : 64;  // columns to a wait, as many as the registers hold
 #pragma unroll 1
-      for (int i = 0; i < kCols; i += 16) {  // not unrolled: this code runs once per item, from a cold instruction cache
-        uint32_t o[16], o2[16];
+      for (int i = 0; i < kCols; i += kPiece) {
+        float o[kPiece], o2[kPiece];
         if (sp.nj) {
-          tmem_ld16(ot + col0 + i, o);
-          if (M == kKeys) tmem_ld16(lanes + C::kOCol + (1 - a) * D + col0 + i, o2);
+#pragma unroll
+          for (int y = 0; y < kPiece; y += 32) {
+            tmem_ld32(src + i + y, o + y);
+            if (both) tmem_ld32(other_o + col0 + i + y, o2 + y);
+          }
           tmem_wait_ld();
-          if (i + 16 == kCols) {  // O may be overwritten
+          if (i + kPiece == kCols) {  // O may be overwritten
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -716,20 +727,25 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
             }
           }
         }
-        uint32_t w[8];
+        uint32_t w[kPiece / 2];
+        if (both) {
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          // a factor of 0: nothing was written there
-          float u = f == 0.f ? 0.f : __uint_as_float(o[2 * y]) * f, v = f == 0.f ? 0.f : __uint_as_float(o[2 * y + 1]) * f;
-          if (M == kKeys && f2 != 0.f) {
-            u = fmaf(__uint_as_float(o2[2 * y]), f2, u);
-            v = fmaf(__uint_as_float(o2[2 * y + 1]), f2, v);
+          for (int y = 0; y < kPiece / 2; ++y) {
+            float u, v;
+            unpack2(fma2(pack2(o2[2 * y], o2[2 * y + 1]), ff2, mul2(pack2(o[2 * y], o[2 * y + 1]), ff)), u, v);
+            w[y] = bf16x2_rn(u, v);
           }
-          w[y] = bf16x2_rn(u, v);
+        } else if (sp.nj) {
+#pragma unroll
+          for (int y = 0; y < kPiece / 2; ++y) w[y] = bf16x2_rn(o[2 * y] * fa, o[2 * y + 1] * fa);
+        } else {
+#pragma unroll
+          for (int y = 0; y < kPiece / 2; ++y) w[y] = 0u;
         }
         if (valid) {
-          *reinterpret_cast<uint4*>(out + i) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(out + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+          for (int y = 0; y < kPiece / 2; y += 4)
+            *reinterpret_cast<uint4*>(out + i + 2 * y) = make_uint4(w[y], w[y + 1], w[y + 2], w[y + 3]);
         }
       }
       if (valid && p.lse && (M == kRows || wg == 0)) p.lse[token * p.hq + head] = lse;
