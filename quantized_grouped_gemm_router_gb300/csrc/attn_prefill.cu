@@ -668,6 +668,9 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         }
         if (lane == 0) mbar_arrive(p_ready(b));
       }
+      // one stream: the last scores came after all products but the last two, and a wait tells a phase from the
+      // next one only
+      if (M == kOne && ok && last > 0) ok = wait(pv_done(a), last - 1);
       if (ok && last >= 0) ok = wait(pv_done(a), last);
       // the factor of O (and of the other stream's O) in the output, and the row's log sum
       float f = 0.f, f2 = 0.f, lse = -INFINITY;

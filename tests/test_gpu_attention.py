@@ -90,6 +90,14 @@ def test_prompt_many_tiles(m, d, n):
     prompt_case(m, (2, 2), d, [(n, n + 100)], False, seed=10, gain=4.0)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_whole_tiles(m, d):
+    """Every row sees every tile whole, and the last tiles count: nothing delays the end of an item."""
+    for n, gain in ((640, 4.0), (576, 4.0), (128, 4.0), (1280, 8.0)):
+        prompt_case(m, (2, 2), d, [(515, n)], False, seed=21, gain=gain)
+        prompt_case(m, (16, 2), d, [(70, n), (3, n)], False, seed=22, gain=gain)
+
+
 def test_prompt_many_sequences(m):
     prompt_case(m, (4, 2), 64, [(i % 4, (i * 7) % 9) for i in range(300)], True, seed=11)
 
