@@ -19,6 +19,7 @@ struct AttnPrefillParams {
   int causal;
   float scale;
   uint16_t* o;
+  int o_wide;  // o is 32-byte aligned
   float* lse;
   WsHeader* hdr;
 };

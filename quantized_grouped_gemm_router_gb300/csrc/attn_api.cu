@@ -91,6 +91,7 @@ int moe_attn_prefill(const moe_attn_dims* dims, moe_heads_view q, moe_heads_view
   p.causal = causal != 0;
   p.scale = scale;
   p.o = o;
+  p.o_wide = aligned(o, 32);
   p.lse = lse;
   p.hdr = static_cast<WsHeader*>(ws);
   return launch_attn_prefill(p, dims->head_dim, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

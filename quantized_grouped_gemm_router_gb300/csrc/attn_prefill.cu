@@ -51,6 +51,25 @@ constexpr float kRescaleLog2 = 8.f;
 // tile, S = Q K^T reads three bytes of shared memory for each byte of K otherwise, and waits for them.
 enum Mode { kRows, kKeys, kOne };
 
+// 16 values of an output row: a whole 32-byte sector at a time if the rows are aligned so. A warp's 32 rows are
+// 32 lines apart, and it is their number that such stores cost.
+__device__ __forceinline__ void st256(uint16_t* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// a + 0 x b, a pair of bf16 each.
+__device__ __forceinline__ uint32_t times0_add(uint32_t b, uint32_t a) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(a) : "r"(b), "r"(0));
+  return a;
+}
+
 template <int D, Mode M>
 struct Cfg {
   static constexpr int NT = M == kOne ? 1 : 2;         // streams of steps, O tiles
@@ -135,7 +154,7 @@ __device__ __forceinline__ void add_seen(uint32_t o_tmem, uint32_t p_tmem, const
     uint32_t acc[16];
     __syncwarp();
     tmem_ld16(o_tmem + d0, acc);
-    tmem_wait_ld();
+    tmem_wait_ld16(acc);
     if (fresh)
       for (int i = 0; i < 16; ++i) acc[i] = 0u;
 #pragma unroll 1
@@ -196,7 +215,7 @@ struct Softmax {
     for (int i = 0; i < N; i += 16) {  // few values at a time: the scores are live; rarely run
       uint32_t o[16];
       tmem_ld16(ot + i, o);
-      tmem_wait_ld();
+      tmem_wait_ld16(o);
 #pragma unroll
       for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
       tmem_st16(ot + i, o);
@@ -336,13 +355,13 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
     return it.head >= 0;
   };
   struct Span {
-    int nj, steps, masked;  // key tiles, steps, the first tile that not every row sees whole
+    int nj, steps, masked, first;  // key tiles, steps, the first tile that not every row sees whole; keys every row sees
   };
   const auto span = [&](const Item& it) {
     const int first = p.causal ? min(max(it.pos0 + 1 + it.off, 0), it.lk) : it.lk;         // keys the first position sees
     const int last = p.causal ? min(max(it.pos0 + it.n_pos + it.off, 0), it.lk) : it.lk;   // and the last
     const int nj = (last + BN - 1) / BN;
-    return Span{nj, NQ * nj, first / BN};
+    return Span{nj, NQ * nj, first / BN, first};
   };
   const auto k_at = [&](int j) { return NQ == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
   const auto v_at = [&](int j, int nj) { return NQ == 2 ? 2 * j + 1 : (j == nj - 1 ? 2 * j + 1 : 2 * j + 2); };
@@ -509,15 +528,24 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         for (int j = sp.masked; j < sp.nj; ++j, ++x) {
           const int s = (r + v_at(j, sp.nj)) % kSlots, b = x & 1;
           if (!(ok = wait(check(b), x >> 1))) break;
-          const uint4* v = reinterpret_cast<const uint4*>(ring + s * C::kSlot);
-          uint32_t hit = 0;
-#pragma unroll 8
-          for (int y = lane; y < C::kSlot / 16; y += 32) {
-            const uint4 w = v[y];
-            const uint32_t e = 0x7F807F80u, one = 0x00800080u;  // exponent 255: + 1 carries into the sign's place
-            hit |= ((w.x & e) + one) | ((w.y & e) + one) | ((w.z & e) + one) | ((w.w & e) + one);
+          // 0 times a NaN or an infinity is a NaN, 0 times all else is 0; 32 keys at a time, from the first that some
+          // row does not see
+          uint32_t h0 = 0, h1 = 0, h2 = 0, h3 = 0;
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c) {
+            const uint4* v = reinterpret_cast<const uint4*>(ring + s * C::kSlot + c * (BN * 128)) + lane;
+            for (int y = max(sp.first - j * BN, 0) / 32 * 256; y < BN * 8; y += 256) {
+#pragma unroll
+              for (int z = 0; z < 256; z += 32) {
+                const uint4 w = v[y + z];
+                h0 = times0_add(w.x, h0);
+                h1 = times0_add(w.y, h1);
+                h2 = times0_add(w.z, h2);
+                h3 = times0_add(w.w, h3);
+              }
+            }
           }
-          const bool bad = __any_sync(~0u, hit & 0x80008000u);
+          const bool bad = __any_sync(~0u, ((h0 | h1 | h2 | h3) & 0x7FFF7FFFu) != 0);
           if (lane == 0) {
             s_bad[b] = bad;
             mbar_arrive(checked(b));
@@ -720,7 +748,11 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
             tmem_ld32(src + i + y, o + y);
             if (both) tmem_ld32(other_o + col0 + i + y, o2 + y);
           }
-          tmem_wait_ld();
+#pragma unroll
+          for (int y = 0; y < kPiece; y += 32) {
+            tmem_wait_ld32(o + y);
+            if (both) tmem_wait_ld32(o2 + y);
+          }
           if (i + kPiece == kCols) {  // O may be overwritten
             tc_fence_before();
             __syncwarp();
@@ -747,8 +779,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         }
         if (valid) {
 #pragma unroll
-          for (int y = 0; y < kPiece / 2; y += 4)
-            *reinterpret_cast<uint4*>(out + i + 2 * y) = make_uint4(w[y], w[y + 1], w[y + 2], w[y + 3]);
+          for (int y = 0; y < kPiece / 2; y += 8) st256(out + i + 2 * y, w + y, p.o_wide);
         }
       }
       if (valid && p.lse && (M == kRows || wg == 0)) p.lse[token * p.hq + head] = lse;

@@ -75,6 +75,13 @@ __device__ __forceinline__ void tmem_wait_ld32(float* r) {
                : "memory");
   asm volatile("" : "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31]));
 }
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 // Four MMAs (K = 4 x 16) under one elected lane of a converged warp: an MMA's issue costs its warp tens
 // of cycles, most of them for the election and the operands' way to the uniform registers. Only the
 // first may start a fresh accumulator.
