@@ -700,12 +700,13 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
       // next one only
       if (M == kOne && ok && last > 0) ok = wait(pv_done(a), last - 1);
       if (ok && last >= 0) ok = wait(pv_done(a), last);
-      // the factor of O (and of the other stream's O) in the output, and the row's log sum
+      // the factor of O (kKeys: of the even tiles' O and the odd tiles') in the output, and the row's log sum
       float f = 0.f, f2 = 0.f, lse = -INFINITY;
       float l = soft.sum(), l_other;
       if (M == kOne && sp.nj && ok && (ok = exchange(l, l_other))) l = wg ? l_other + l : l + l_other;
       if (M == kKeys && sp.nj) {
-        // both streams' O belong to the same rows (the same lanes): each warpgroup writes half the columns
+        // both streams' O belong to the same rows (the same lanes): each warpgroup writes half the columns. Which
+        // stream had the even tiles depends on the items drawn before; the sums' order does not.
         const float mc = l == 0.f ? -INFINITY : soft.mc;
         if (ok && used) ok = wait(o_free(a), used - 1);  // the other warpgroup has read the last item's statistics
         s_stat[a][row] = make_float2(mc, l);
@@ -714,11 +715,11 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         if (lane == 0) mbar_arrive(merged);
         __syncwarp();
         if (ok) ok = wait(merged, used);
-        const float2 other = s_stat[1 - a][row];
-        const float top = fmaxf(mc, other.x);
-        if (l != 0.f || other.y != 0.f) {
-          const float w = l == 0.f ? 0.f : ex2(mc - top), w2 = other.y == 0.f ? 0.f : ex2(other.x - top);
-          const float sum = fmaf(w, l, w2 * other.y);
+        const float2 even = s_stat[nb & 1][row], odd = s_stat[1 - (nb & 1)][row];  // (m c, l)
+        const float top = fmaxf(even.x, odd.x);
+        if (even.y != 0.f || odd.y != 0.f) {
+          const float w = even.y == 0.f ? 0.f : ex2(even.x - top), w2 = odd.y == 0.f ? 0.f : ex2(odd.x - top);
+          const float sum = fmaf(w, even.y, w2 * odd.y);
           f = w / sum;
           f2 = w2 / sum;
           lse = top * kLn2 + logf(sum);
@@ -730,13 +731,10 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const int64_t token = it.q_row + pos;
-      // kKeys: both streams' O, or that of the only one that had a step
-      const bool both = M == kKeys && sp.steps > 1;
-      const bool others = M == kKeys && sp.steps == 1 && last < 0;
-      const uint32_t other_o = lanes + C::kOCol + (NT - 1 - a) * D;
-      const uint32_t src = (others ? other_o : ot) + col0;
-      const float fa = others ? f2 : f;
-      const uint64_t ff = pack2(fa, fa), ff2 = pack2(f2, f2);
+      const bool both = M == kKeys && sp.steps > 1;  // else the even tiles' O is all there is
+      const uint32_t src = (M == kKeys ? lanes + C::kOCol + (nb & 1) * D : ot) + col0;
+      const uint32_t src2 = lanes + C::kOCol + (1 - (nb & 1)) * D + col0;
+      const uint64_t ff = pack2(f, f), ff2 = pack2(f2, f2);
       uint16_t* out = p.o + (token * p.hq + head) * D + col0;
       constexpr int kPiece = M == kKeys || kCols < 64 ? 32 : 64;  // columns to a wait, as many as the registers hold
 #pragma unroll 1
@@ -746,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
 #pragma unroll
           for (int y = 0; y < kPiece; y += 32) {
             tmem_ld32(src + i + y, o + y);
-            if (both) tmem_ld32(other_o + col0 + i + y, o2 + y);
+            if (both) tmem_ld32(src2 + i + y, o2 + y);
           }
 #pragma unroll
           for (int y = 0; y < kPiece; y += 32) {
@@ -772,7 +770,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
           }
         } else if (sp.nj) {
 #pragma unroll
-          for (int y = 0; y < kPiece / 2; ++y) w[y] = bf16x2_rn(o[2 * y] * fa, o[2 * y + 1] * fa);
+          for (int y = 0; y < kPiece / 2; ++y) w[y] = bf16x2_rn(o[2 * y] * f, o[2 * y + 1] * f);
         } else {
 #pragma unroll
           for (int y = 0; y < kPiece / 2; ++y) w[y] = 0u;

@@ -98,6 +98,39 @@ def test_prompt_whole_tiles(m, d):
         prompt_case(m, (16, 2), d, [(70, n), (3, n)], False, seed=22, gain=gain)
 
 
+@pytest.mark.parametrize("heads,d,n", [((2, 2), 64, 200), ((16, 2), 128, 2600), ((4, 2), 256, 150)])
+def test_prompt_output_alignment(m, heads, d, n):
+    """Output rows on 16-byte boundaries that are no 32-byte ones."""
+    hq, hkv = heads
+    q, k, v = (x.view(torch.int16).cuda() for x in (rand(30, n, hq, d), rand(31, n, hkv, d), rand(32, n, hkv, d)))
+    dims = m.AttnDims(hq, hkv, d)
+    ws = m.attn_workspace(dims)
+    want = m.attn_prefill(dims, q, k, v, cu([n]), cu([n]), ws)
+    buf = torch.full((n * hq * d + 16,), 0x7FC0, dtype=torch.int16, device="cuda")
+    o = buf[8:-8].view(n, hq, d)
+    assert o.data_ptr() % 32 == 16
+    m.attn_prefill(dims, q, k, v, cu([n]), cu([n]), ws, o=o)
+    assert torch.equal(o, want)
+    assert (buf[:8] == 0x7FC0).all() and (buf[-8:] == 0x7FC0).all()
+
+
+@pytest.mark.parametrize("heads,d,lens,causal", [
+    ((16, 2), 128, [2600], True), ((8, 8), 64, [250] * 24, False), ((16, 2), 128, [300] * 30, True),
+    ((16, 2), 256, [300] * 30, True)])
+def test_prompt_same_bits(m, heads, d, lens, causal):
+    """Which SM computes what varies from call to call; the result does not."""
+    (hq, hkv), n = heads, sum(lens)
+    q, k, v = (x.view(torch.int16).cuda() for x in (rand(40, n, hq, d, gain=4.0), rand(41, n, hkv, d), rand(42, n, hkv, d)))
+    dims = m.AttnDims(hq, hkv, d)
+    ws, c = m.attn_workspace(dims), cu(lens)
+    first = None
+    for _ in range(20):
+        lse = torch.empty(n, hq, device="cuda")
+        got = m.attn_prefill(dims, q, k, v, c, c, ws, causal=causal, lse=lse), lse
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
 def test_prompt_many_sequences(m):
     prompt_case(m, (4, 2), 64, [(i % 4, (i * 7) % 9) for i in range(300)], True, seed=11)
 
