@@ -443,7 +443,8 @@ MOE_API size_t moe_attn_workspace_bytes(const moe_attn_dims* dims);
  * j <= i + Lk - Lq (causal != 0: the last query sees every key, as when a prompt continues on
  * earlier context) or always (causal == 0).
  * o: bf16 [total_q, n_q_heads, head_dim], contiguous, not overlapping the inputs. lse: fp32
- * [total_q, n_q_heads] or NULL. scale > 0 and finite.
+ * [total_q, n_q_heads] or NULL. scale > 0 and finite. The result of a call does not vary from run to
+ * run.
  */
 MOE_API int moe_attn_prefill(const moe_attn_dims* dims, moe_heads_view q, moe_heads_view k, moe_heads_view v,
                              const int32_t* cu_q, const int32_t* cu_k, int32_t n_seqs, int32_t total_q,
@@ -487,7 +488,9 @@ MOE_API int moe_kv_append(const moe_kv_cache* cache, moe_heads_view k, moe_heads
  * lens counts it; 0 gives an empty row). The work of all sequences is cut into equal runs of cache
  * rows, one per SM, so that a batch of uneven lengths and one long sequence alike fill the GPU;
  * cut sequences are joined in a fixed order (the result of a call does not vary from run to run).
- * o: bf16 [n_seqs, n_q_heads, head_dim]; lse: fp32 [n_seqs, n_q_heads] or NULL.
+ * o: bf16 [n_seqs, n_q_heads, head_dim], not overlapping q; lse: fp32 [n_seqs, n_q_heads] or NULL.
+ * n_seqs * n_kv_heads * ceil(heads per key-value head / 16) * (table_width * page_size / 16 + 8) must
+ * be below 2^31 (MOE_ERR_UNSUPPORTED_SHAPE).
  */
 MOE_API int moe_attn_decode(const moe_kv_cache* cache, moe_heads_view q, const int32_t* lens,
                             const int32_t* page_table, int32_t table_width, int32_t n_seqs, float scale, uint16_t* o,

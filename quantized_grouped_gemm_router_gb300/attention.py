@@ -87,6 +87,12 @@ def _ints(t: torch.Tensor, n: int | None, name: str) -> int:
     return t.data_ptr()
 
 
+def _ws(ws: torch.Tensor) -> int:
+    if ws.dtype is not torch.uint8 or not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA uint8 tensor (attn_workspace)")
+    return ws.data_ptr()
+
+
 def _lse(lse: torch.Tensor | None, rows: int, heads: int) -> int | None:
     if lse is None:
         return None
@@ -120,7 +126,7 @@ def attn_prefill(dims: AttnDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     _check(_fn("moe_attn_prefill")(ctypes.byref(dims), qv, kv, vv, _ints(cu_q, None, "cu_q"),
                                    _ints(cu_k, n + 1, "cu_k"), n, tq, tk,
                                    1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, o.data_ptr(),
-                                   _lse(lse, tq, hq), ws.data_ptr(), ws.numel(), _stream(q)), "moe_attn_prefill")
+                                   _lse(lse, tq, hq), _ws(ws), ws.numel(), _stream(q)), "moe_attn_prefill")
     return o
 
 
@@ -182,7 +188,7 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor
     if v.shape[0] != total:
         raise ValueError("k and v must have the same number of rows")
     _check(_fn("moe_kv_append")(ctypes.byref(cache._c), kv, vv, _ints(cu, n + 1, "cu"), _ints(start, n, "start"),
-                                _table(page_table, n), page_table.shape[1], n, total, ws.data_ptr(), ws.numel(),
+                                _table(page_table, n), page_table.shape[1], n, total, _ws(ws), ws.numel(),
                                 _stream(k)), "moe_kv_append")
 
 
@@ -197,6 +203,6 @@ def attn_decode(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, page_table:
     o = _out(o, q)
     _check(_fn("moe_attn_decode")(ctypes.byref(cache._c), qv, _ints(lens, n, "lens"), _table(page_table, n),
                                   page_table.shape[1], n, 1.0 / math.sqrt(d) if scale is None else scale,
-                                  o.data_ptr(), _lse(lse, n, hq), ws.data_ptr(), ws.numel(), _stream(q)),
+                                  o.data_ptr(), _lse(lse, n, hq), _ws(ws), ws.numel(), _stream(q)),
            "moe_attn_decode")
     return o

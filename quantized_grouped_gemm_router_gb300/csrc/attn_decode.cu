@@ -20,6 +20,12 @@
 // to 8 heads thus wastes no rows; up to 16 heads take two column blocks over the same fragments of K
 // and V. In e4m3 the codes become fp16 (exactly), the query row fp16 times a power of two, and the
 // softmax weights fp16; in bf16 all operands are bf16.
+//
+// Measured (GB300): long batches add cache rows at the copy rate of HBM (75 sequences of 8300 rows, 2 heads of
+// 128, bf16: 102 us, 6.2 TB/s, 92% of it); a call has 14 us beside that (18 in e4m3 at heads of 256): launch, three
+// dependent loads before the first rows, SMs that end up to 5 us apart, the two joins. So 64 sequences of up to
+// 16384 rows take 66 us (5.6 TB/s), one of 131071 rows 31 us (4.4 TB/s), 129 e4m3 sequences of up to 8191 rows of
+// 256 75 us (4.6 TB/s), one of 511 rows 8.4 us.
 #include <cuda_fp8.h>
 
 #include "attn_device.cuh"

@@ -28,8 +28,10 @@
 //  * K and V tiles are one ring, filled by TMA in the order in which the MMA warps free them.
 //
 // Bound by the chain S -> softmax -> P V of the two streams: a step takes about 1500 cycles, 1024 of them
-// the tensor cores' own. Measured (GB300): 16384 tokens, 16/2 heads of 128, causal: 0.74 ms, 1.48 PFLOP/s (78%
-// of a cuBLAS bf16 GEMM's burst rate); 1021 tokens on 8192, heads of 256: 0.130 ms, 1.12 PFLOP/s.
+// the tensor cores' own. Measured (GB300): 16384 tokens, 16/2 heads of 128, causal: 0.73 ms, 1.50 PFLOP/s (79%
+// of a cuBLAS bf16 GEMM's burst rate); 1021 tokens on 8192, heads of 256: 0.124 ms, 1.17 PFLOP/s (62%), bound by
+// the K and V copies from L2, 11 TB/s of them. Short sequences: an item costs 3 to 4 us beside its steps (start,
+// check, the last product, the output): 24 texts of 250 tokens, 8 heads of 64, both ways: 27 us.
 #include "attn_device.cuh"
 #include "attn_ptx.cuh"
 
@@ -847,8 +849,8 @@ cudaError_t launch(const AttnPrefillParams& p, cudaStream_t s) {
 cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int d, cudaStream_t s) {
   // Two row tiles per CTA halve the K and V traffic and the items; one row tile with its keys split halves the
   // longest item. Measured at 16/2 heads of 128: 2048 tokens (0.8 items of two row tiles per SM) 37.2 against
-  // 27.8 us split, 3000 tokens (1.2) 46.0 against 44.5, 4096 tokens (1.7) 59.4 against 67.9, 16384 tokens 745
-  // against 803 us.
+  // 27.8 us split, 3000 tokens (1.2) 46.0 against 44.5, 4096 tokens (1.7) 59.4 against 67.9, 16384 tokens 729
+  // against 803 us; 9 prompts in 4096 tokens (1.7) 28.6 against 36.4.
   const bool two = 5 * ((int64_t)p.total_q / (2 * (128 / p.group)) * p.hkv) >= 7 * (int64_t)num_sms();
   if (d == 64) return two ? launch<64, kRows>(p, s) : launch<64, kKeys>(p, s);
   if (d == 128) return two ? launch<128, kRows>(p, s) : launch<128, kKeys>(p, s);

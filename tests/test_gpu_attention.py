@@ -530,3 +530,41 @@ def test_prompt_then_tokens(m, fp8):
         o, lse = run_decode(m, cache, qn.view(torch.int16).cuda(), at, table, ws)
         vals = [[x[b, :n].double().transpose(0, 1) for x in (k, v)] for b, n in enumerate(at)]
         C.check(o, lse, decode_ref(qn, vals, 1 / math.sqrt(d)), 11 if fp8 else 8)
+
+
+def test_binding_refusals(m):
+    dims = m.AttnDims(4, 2, 64)
+    q, kv = (torch.zeros(5, h, 64, dtype=torch.int16, device="cuda") for h in (4, 2))
+    c, ws = cu([5]), m.attn_workspace(dims)
+    cache = m.KvCache.empty(dims, 4, 16)
+    table, lens = torch.zeros(5, 1, dtype=torch.int32, device="cuda"), ints([1] * 5)
+
+    def prefill(q=q, k=kv, v=kv, cu_q=c, cu_k=c, ws=ws, **kw):
+        m.attn_prefill(dims, q, k, v, cu_q, cu_k, ws, **kw)
+
+    def decode(q=q, lens=lens, table=table, ws=ws, **kw):
+        m.attn_decode(cache, q, lens, table, ws, **kw)
+
+    def append(k=kv, v=kv, cu_=c, start=ints([0]), table=table[:1], ws=ws):
+        m.kv_append(cache, k, v, cu_, start, table, ws)
+
+    prefill(), decode(), append()
+    for call in (prefill, decode, append):
+        for bad in (ws.cpu(), ws.view(torch.int16), ws[::2]):
+            with pytest.raises(ValueError):
+                call(ws=bad)
+        with pytest.raises(m.MoeError):
+            call(ws=ws[:128])
+    for kw in (dict(q=q[:, :3]), dict(q=q.float()), dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)), dict(v=kv[:4]),
+               dict(cu_k=cu([5, 0])), dict(cu_q=c.long()), dict(o=torch.empty_like(q[:4])), dict(o=q.cpu()),
+               dict(lse=torch.empty(4, 5, device="cuda").t()), dict(lse=torch.empty(5, 3, device="cuda"))):
+        with pytest.raises(ValueError):
+            prefill(**kw)
+    for kw in (dict(lens=lens[:4]), dict(table=table[:4]), dict(table=table[:, 0]), dict(q=q.cpu()),
+               dict(lens=lens.float()), dict(o=torch.empty(5, 64, 4, dtype=torch.int16, device="cuda"))):
+        with pytest.raises(ValueError):
+            decode(**kw)
+    for kw in (dict(k=kv[:4]), dict(start=ints([0, 0])), dict(table=table), dict(cu_=c.cpu())):
+        with pytest.raises(ValueError):
+            append(**kw)
+    assert status(m, ws) == 0
