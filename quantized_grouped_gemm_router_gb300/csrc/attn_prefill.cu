@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
   } else if (warp == C::kWarpCheck && lane == 0) {
     *s_abort = 0;
     mbar_init(q_full, 1);
-    mbar_init(q_free, M == kOne ? 8 : 2);
+    mbar_init(q_free, M == kOne ? 10 : 2);
     mbar_init(q_there, 8);
     for (int w = 0; w < 4; ++w) mbar_init(halves(w), 2);
     mbar_init(merged, 8);
@@ -478,6 +478,8 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         };
         const int n0 = (me - nb) & 1;
         if (!(ok = wait(M == kOne ? q_there : q_full, used))) break;
+        if (M == kOne && lane == 0) mbar_arrive(q_free);  // (a warp without a step must not miss a phase)
+        __syncwarp();
         if (n0 >= sp.steps) {  // a single step, the other warp's
           if (M != kOne && lane == 0) mbar_arrive(q_free);
         } else if ((ok = have(k_at(n0 / NQ)))) {
@@ -646,6 +648,10 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
                               BN * 128, lim, first);
             }
           }
+          // The end of the item waits for the last product. A wait tells a phase from the next one only, and these
+          // scores came after all products but the last two: the one before the last is waited for here, while
+          // the last one cannot have been made.
+          if (n > 0 && n == sp.steps - 1 && !(ok = wait(pv_done(a), k - 1))) break;
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -698,9 +704,6 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         }
         if (lane == 0) mbar_arrive(p_ready(b));
       }
-      // one stream: the last scores came after all products but the last two, and a wait tells a phase from the
-      // next one only
-      if (M == kOne && ok && last > 0) ok = wait(pv_done(a), last - 1);
       if (ok && last >= 0) ok = wait(pv_done(a), last);
       // the factor of O (kKeys: of the even tiles' O and the odd tiles') in the output, and the row's log sum
       float f = 0.f, f2 = 0.f, lse = -INFINITY;
