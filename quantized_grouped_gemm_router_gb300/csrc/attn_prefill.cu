@@ -589,6 +589,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
       // keys this row sees (rows of no position: all, so that they add no compares)
       const int seen = !valid ? sp.nj * BN : p.causal ? min(max(it.pos0 + pos + 1 + it.off, 0), it.lk) : it.lk;
       Softmax soft(p.scale * kLog2e);
+      if (!valid) soft.grown = INFINITY;  // what such a row holds decides nothing for the others of its warp
       const auto grow = [&](float mx, bool first, uint32_t bar, int parity) {
         if (!__any_sync(~0u, mx > soft.m + soft.grown)) return true;
         const float f = soft.raise(mx);

@@ -131,6 +131,24 @@ def test_prompt_same_bits(m, heads, d, lens, causal):
         assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
 
 
+@pytest.mark.parametrize("heads", [(7, 1), (16, 2), (4, 4)], ids=str)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_neighbours(m, heads, d):
+    """A sequence's bits do not depend on the queries of the next one, nor on what ran before."""
+    (hq, hkv), lens = heads, [300, 77]
+    q, k, v = rand(50, 377, hq, d), rand(51, 377, hkv, d), rand(52, 377, hkv, d)
+    k *= torch.linspace(0.2, 3.0, 377).to(torch.bfloat16)[:, None, None]  # maxima that grow
+    dims, c = m.AttnDims(hq, hkv, d), cu(lens)
+    ws = m.attn_workspace(dims)
+    outs = []
+    for gain in (1.0, 1000.0, -1000.0):
+        q2 = q.clone()
+        q2[300:] *= gain
+        x, y, z = (t.view(torch.int16).cuda() for t in (q2, k, v))
+        outs.append(m.attn_prefill(dims, x, y, z, c, c, ws)[:300].clone())
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
 def test_prompt_many_sequences(m):
     prompt_case(m, (4, 2), 64, [(i % 4, (i * 7) % 9) for i in range(300)], True, seed=11)
 
