@@ -50,7 +50,8 @@ constexpr float kRescaleLog2 = 8.f;
 // What a CTA's streams of steps are: two row tiles over the same keys, two halves of one row tile's keys
 // (even and odd tiles), or one row tile alone (D = 256: tensor memory holds one O). In kOne both softmax
 // warpgroups work on every step, half of its keys each, and Q is copied to tensor memory: with 64 keys to a
-// tile, S = Q K^T reads three bytes of shared memory for each byte of K otherwise, and waits for them.
+// tile, S = Q K^T reads three bytes of shared memory for each byte of K otherwise, and waits for them. Q passes
+// through the ring, so that seven K and V tiles have room, not five (2% at 4096 tokens).
 enum Mode { kRows, kKeys, kOne };
 
 // 16 values of an output row: a whole 32-byte sector at a time if the rows are aligned so. A warp's 32 rows are
@@ -79,10 +80,12 @@ struct Cfg {
   static constexpr int BN = D == 256 ? 64 : 128;       // keys per tile
   static constexpr int kChunks = D / 64;               // 128-byte columns of a row
   static constexpr int kQTile = kChunks * 16384;       // one row tile
+  static constexpr int kQBytes = M == kOne ? 0 : NQ * kQTile;  // kOne: Q passes through two entries of the ring
+  static constexpr int kQEntries = M == kOne ? 2 : 0;
   static constexpr int kSlot = BN * D * 2;             // one K or V tile
-  static constexpr int kRoom = 224 * 1024 - NQ * kQTile;  // all but the last 3 KB, which the kernel's own variables take
+  static constexpr int kRoom = 224 * 1024 - kQBytes;  // all but the last 3 KB, which the kernel's own variables take
   static constexpr int kSlots = kRoom / kSlot < 8 ? kRoom / kSlot : 8;
-  static constexpr int kSmem = NQ * kQTile + kSlots * kSlot;
+  static constexpr int kSmem = kQBytes + kSlots * kSlot;
   static constexpr int kSoftWarps = 8;                 // a warpgroup per stream; kOne: one per half of a tile's keys
   static constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 2, kWarpCheck = kSoftWarps + 3;  // two MMA warps
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
   __shared__ int s_abort_flag, s_bad_flag[2];
   __shared__ uint32_t s_tmem;
   __shared__ __align__(8) uint64_t s_bar[30 + (NQ == 1 ? 3 : 2) * kSlots];
-  uint8_t* ring = smem + NQ * C::kQTile;
+  uint8_t* ring = smem + C::kQBytes;
   volatile int* s_abort = &s_abort_flag;
   volatile int* s_bad = s_bad_flag;  // [2] V tile (the count of tiles not seen whole, % 2) holds a non-finite value
   const uint32_t bars = smem_u32(s_bar);
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
   } else if (warp == C::kWarpCheck && lane == 0) {
     *s_abort = 0;
     mbar_init(q_full, 1);
-    mbar_init(q_free, M == kOne ? 10 : 2);
+    mbar_init(q_free, 2);
     mbar_init(q_there, 8);
     for (int w = 0; w < 4; ++w) mbar_init(halves(w), 2);
     mbar_init(merged, 8);
@@ -401,9 +404,16 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
             if (ok) {
               mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * C::kChunks * Ppt * G * 128));
               for (int a = 0; a < NQ; ++a)
-                for (int c = 0; c < C::kChunks; ++c)
-                  tma_load_3d(smem_u32(smem) + a * C::kQTile + c * 16384, &maps.q, c * 64, it.head * G, it.q_row + a * Ppt,
-                              q_full);
+                for (int c = 0; c < C::kChunks; ++c) {
+                  uint32_t to = smem_u32(smem) + a * C::kQTile + c * 16384;
+                  if (M == kOne) {
+                    const int s = r % kSlots;
+                    if (r >= kSlots && !(ok = mbar_wait(kv_free(s), ((r / kSlots) & 1) ^ 1, s_abort))) break;
+                    to = smem_u32(ring) + s * C::kSlot + (c & 1) * 16384;
+                    r += c & 1;
+                  }
+                  tma_load_3d(to, &maps.q, c * 64, it.head * G, it.q_row + a * Ppt, q_full);
+                }
               ++q_used;
             }
           }
@@ -478,7 +488,13 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         };
         const int n0 = (me - nb) & 1;
         if (!(ok = wait(M == kOne ? q_there : q_full, used))) break;
-        if (M == kOne && lane == 0) mbar_arrive(q_free);  // (a warp without a step must not miss a phase)
+        if (M == kOne) {
+          if (lane == 0) {
+            mbar_arrive(q_free);  // (a warp without a step must not miss a phase)
+            mbar_arrive(kv_free((r + me) % kSlots));
+          }
+          r += C::kQEntries;
+        }
         __syncwarp();
         if (n0 >= sp.steps) {  // a single step, the other warp's
           if (M != kOne && lane == 0) mbar_arrive(q_free);
@@ -529,6 +545,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
       bool ok = true;
       for (int t = 0; ok && take_item(t, it); ++t) {
         const Span sp = span(it);
+        if (sp.nj) r += C::kQEntries;
         for (int j = sp.masked; j < sp.nj; ++j, ++x) {
           const int s = (r + v_at(j, sp.nj)) % kSlots, b = x & 1;
           if (!(ok = wait(check(b), x >> 1))) break;
@@ -604,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         if (!(ok = wait(q_full, used))) break;
 #pragma unroll
         for (int c = 0; c < C::kChunks / 2; ++c) {
-          const uint8_t* q = smem + (wg * (C::kChunks / 2) + c) * 16384 + row * 128;
+          const uint8_t* q = ring + (r + wg) % kSlots * C::kSlot + c * 16384 + row * 128;
           uint4 v[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) v[x] = *reinterpret_cast<const uint4*>(q + ((x ^ (row & 7)) << 4));
@@ -613,10 +630,8 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(q_there);
-          mbar_arrive(q_free);
-        }
+        if (lane == 0) mbar_arrive(q_there);
+        r += C::kQEntries;
       }
       int last = -1;  // this stream's last step's number within the stream, over all items
       for (int n = NT == 2 ? (a - nb) & 1 : 0; n < sp.steps; n += NT) {
