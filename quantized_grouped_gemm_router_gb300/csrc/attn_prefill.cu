@@ -15,7 +15,7 @@
 //  * Steps. Step n's scores go to S buffer n % 2. An MMA warp issues S of its first step, then for every
 //    second step n: P(n) V, S(n + 2). The tensor cores thus work on one step while the softmax of the
 //    other runs. There are two MMA warps: the issue of an MMA waits for the ones before it, and a warp's
-//    waits for its operands (about 400 cycles a step, against 1024 of MMAs at D = 128) pass while the
+//    waits for its operands (about 400 cycles a step, against 1170 of MMAs at D = 128) pass while the
 //    other warp's MMAs run. They take turns, a step each: mixed, both steps' scores would be done at the
 //    same time, and both softmaxes would run while the tensor cores idle.
 //  * Rescaling. O is scaled down only when a row's maximum has grown by more than 2^8 since the last
@@ -27,10 +27,11 @@
 //    seen keys only (rare, and bounded by one tile's work).
 //  * K and V tiles are one ring, filled by TMA in the order in which the MMA warps free them.
 //
-// Bound by the chain S -> softmax -> P V of the two streams: a step takes about 1500 cycles, 1024 of them
-// the tensor cores' own. Measured (GB300): 16384 tokens, 16/2 heads of 128, causal: 0.73 ms, 1.50 PFLOP/s (79%
-// of a cuBLAS bf16 GEMM's burst rate); 1021 tokens on 8192, heads of 256: 0.124 ms, 1.17 PFLOP/s (62%), bound by
-// the K and V copies from L2, 11 TB/s of them. Short sequences: an item costs 3 to 4 us beside its steps (start,
+// Bound by the chain S -> softmax -> P V of the two streams: at D = 128 a step takes about 1500 cycles, 1170 of
+// them the tensor cores' own. Measured (GB300): 16384 tokens, 16/2 heads of 128, causal: 0.73 ms, 1.50 PFLOP/s (79%
+// of a cuBLAS bf16 GEMM's burst rate); 1021 tokens on 8192, heads of 256: 0.123 ms, 1.18 PFLOP/s (62%),
+// bound by the MMAs of 64-key tiles: one of 64 columns takes 67 cycles, as one of 128 does (one of 256 takes 129),
+// so that 64 keys take 1600. Short sequences: an item costs 3 to 4 us beside its steps (start,
 // check, the last product, the output): 24 texts of 250 tokens, 8 heads of 64, both ways: 27 us.
 #include "attn_device.cuh"
 #include "attn_ptx.cuh"
