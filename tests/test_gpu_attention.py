@@ -213,6 +213,32 @@ def test_prompt_nonfinite_unseen(m, d, bad):
     assert not torch.isfinite(got[190:, 2:, 3]).any()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_nonfinite_many_heads(m, d):
+    """The same with more row tiles than SMs: single bad values, first rows before them compared."""
+    lens, h = [(620, 620), (404, 404)], 64
+    n = 1024
+    q, k, v = rand(4, n, h, d), rand(5, n, h, d), rand(6, n, h, d)
+    at = [17, 128, 255, 256, 383, 500, 619]
+    sel = torch.arange(0, h, 9)                                 # heads compared; the reference takes a while
+    ref = C.prefill(q[:, sel].double(), k[:, sel].double(), v[:, sel].double(), lens, 1 / math.sqrt(d), True)
+    vb = v.clone()
+    for i, x in enumerate(at):
+        vb[x, :, i] = (math.nan, math.inf, -math.inf)[i % 3]    # one column each
+    vb[620 + 400:] = math.nan
+    o, lse = run_prefill(m, m.AttnDims(h, h, d), *(x.view(torch.int16).cuda() for x in (q, k, vb)), lens, True)
+    o, lse = o[:, sel.cuda()], lse[:, sel.cuda()]
+    got = C.values(o)
+    for i, x in enumerate(at):
+        assert not torch.isfinite(got[x:620, :, i]).any() and torch.isfinite(got[:x, :, i]).all()
+    clean = torch.ones(n, 1, d, dtype=torch.bool)
+    for i, x in enumerate(at):
+        clean[x:620, :, i] = False
+    clean[620 + 400:] = False
+    fixed = torch.where(clean, got, ref[0]).to(torch.bfloat16).view(torch.int16)
+    C.check(fixed, lse, ref, 8)
+
+
 def test_prompt_nonfinite_both_ways(m):
     """Without causality the tail of a tile still belongs to another sequence."""
     lens, d = [(70, 70), (30, 30)], 128
