@@ -868,10 +868,17 @@ cudaError_t launch(const AttnPrefillParams& p, cudaStream_t s) {
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int d, cudaStream_t s) {
   // Two row tiles per CTA halve the K and V traffic and the items; one row tile with its keys split halves the
-  // longest item. Measured at 16/2 heads of 128: 2048 tokens (0.8 items of two row tiles per SM) 37.2 against
-  // 27.8 us split, 3000 tokens (1.2) 46.0 against 44.5, 4096 tokens (1.7) 59.4 against 67.9, 16384 tokens 729
-  // against 803 us; 9 prompts in 4096 tokens (1.7) 28.6 against 36.4.
-  const bool two = 5 * ((int64_t)p.total_q / (2 * (128 / p.group)) * p.hkv) >= 7 * (int64_t)num_sms();
+  // longest item. Measured at 16/2 heads of 128, one prompt: 2048 tokens (0.8 items of two row tiles per SM) 37.2
+  // against 27.8 us split, 3000 tokens (1.2) 44.4 against 42.6, 4096 tokens (1.7) 59.4 against 67.9, 16384 tokens 729
+  // against 803 us. Several sequences have shorter items, and the two streams of a split one wait for each other
+  // at its end: 16 prompts in 1600 tokens (0.8) 12.5 against 13.2, 24 in 3000 (1.3) 16.3 against 20.1; below 0.75 items
+  // per SM the split fills them better (8 in 1000 tokens, 0.4: 13.7 against 10.3). Under a causal mask that holds for
+  // items of few positions; one of 256 works for half its time on keys that half its rows do not see (24 prompts
+  // in 6001 tokens, 8/8 heads: 33.3 against 26.6).
+  const int rows = 2 * (128 / p.group);  // positions of an item of two row tiles
+  const int64_t sms = num_sms(), each = (p.total_q + p.n_seqs - 1) / p.n_seqs;
+  const bool two = 10 * ((int64_t)p.total_q / rows * p.hkv) >= 13 * sms ||
+                   (p.n_seqs > 1 && (!p.causal || rows <= 64) && 4 * ((each + rows - 1) / rows * p.n_seqs * p.hkv) >= 3 * sms);
   if (d == 64) return two ? launch<64, kRows>(p, s) : launch<64, kKeys>(p, s);
   if (d == 128) return two ? launch<128, kRows>(p, s) : launch<128, kKeys>(p, s);
   return launch<256, kOne>(p, s);
