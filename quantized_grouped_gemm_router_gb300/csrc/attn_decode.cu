@@ -48,6 +48,9 @@ struct Cfg {
   static constexpr int NW = RB == 512 ? (NH == 1 ? 6 : 4) : RB == 64 && NH == 1 ? 16 : 8;
   static constexpr int kTile = 2 * TR * RB;         // K rows, then V rows
   static constexpr int kStages = 2;
+  // Weights are relative to 2^-kUp times the maximum's: fp16 has 11 bits down to 2^-14 only, so that e4m3 takes them
+  // up to 2^15 (with the growth of 2^8) and keeps those of 2^-21 of the largest as exact as the others.
+  static constexpr float kUp = E4M3 ? 7.f : 0.f;
   static constexpr int kRing = kStages * kTile;     // per warp
   static constexpr int kPartRows = 8 * NH * D;      // floats of a partial O
   static constexpr int kPart = 16 * D + 32;         // a CTA's partial result in the workspace: O, then 16 m and 16 l
@@ -528,14 +531,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
           mx[nh][y] = x;
-          grown |= x * cr[nh][y] > mc[nh][y] + kRescaleLog2 || (m[nh][y] == -INFINITY && x > m[nh][y]);
+          grown |= x * cr[nh][y] > mc[nh][y] + kRescaleLog2 + C::kUp || (m[nh][y] == -INFINITY && x > m[nh][y]);
         }
       if (__any_sync(~0u, grown)) {
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float m2 = fmaxf(m[nh][y], mx[nh][y]), mc2 = m2 == -INFINITY ? 0.f : m2 * cr[nh][y];
+            const float m2 = fmaxf(m[nh][y], mx[nh][y]), mc2 = m2 == -INFINITY ? 0.f : m2 * cr[nh][y] - C::kUp;
             const float f = m[nh][y] == -INFINITY ? 0.f : ex2(mc[nh][y] - mc2);
             m[nh][y] = m2;
             mc[nh][y] = mc2;

@@ -425,6 +425,29 @@ def test_token_large_and_small_queries(m, fp8):
         C.check(o, lse, decode_ref(q, vals, scale), 11 if fp8 else 8, f"{size}")
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_token_small_weights(m, fp8):
+    """Values behind weights of 2^-20 of the largest, whose own value is zero."""
+    d, n, page = 64, 40, 16
+    level = torch.full((n,), 0.4375)
+    level[11] = 1.0
+    k = level[None, :, None].expand(1, n, d).double()
+    v = (torch.arange(n * d) % 29 - 14).reshape(1, n, d).double() / 8
+    v[0, 11] = 0.0
+    to = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    cells = [torch.zeros(3, 1, page, d, dtype=to) for _ in range(2)]
+    for c, x in zip(cells, (k, v)):
+        for i in range(n):
+            c[i // page, 0, i % page] = x[0, i].to(to)
+        assert torch.equal(torch.cat([c[i // page, 0, i % page][None] for i in range(n)]).double(), x[0])  # exact codes
+    one = (torch.ones(1, device="cuda"),) * 2
+    cache = m.KvCache(m.AttnDims(8, 1, d), *(c.view(torch.uint8 if fp8 else torch.int16).cuda() for c in cells),
+                      *(one if fp8 else ()))
+    q = torch.full((1, 8, d), 3.125).to(torch.bfloat16)   # scores 25 and 10.94
+    o, lse = run_decode(m, cache, q.view(torch.int16).cuda(), [n], ints([[0, 1, 2]]))
+    C.check(o, lse, decode_ref(q, [[k, v]], 1 / math.sqrt(d)), 11 if fp8 else 8)
+
+
 def test_token_workspace_reused(m):
     """One workspace over calls of different batches; same call, same bits; another stream; a graph."""
     dims = m.AttnDims(16, 2, 128)
