@@ -210,8 +210,10 @@ struct Sum4 {
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 
-  // Adds the partial results first, first + step, ... below n; kBatch of them in flight. get(i): partial i.
-  template <class Get>
+  // Adds the partial results first, first + step, ... below n; kBatch of them in flight. get(i): partial i. What is
+  // read past the last is a copy of it, with a weight of 0; INF: an infinity may be in it, and 0 times that is a NaN.
+  // (e4m3 has none; its 129 sequences of up to 8191 rows take 75.1 us without the zeros, 76.6 with them.)
+  template <bool INF, class Get>
   __device__ __forceinline__ void add(int first, int step, int n, Get get) {
     constexpr int kBatch = 8;
     for (int i0 = first; i0 < n; i0 += step * kBatch) {
@@ -222,6 +224,10 @@ struct Sum4 {
         const int j = i0 + i * step;
         get(min(j, n - 1), x[i], xm[i], xl[i]);
         if (j >= n) xm[i] = -INFINITY;
+        if (INF && j >= n) {
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          xl[i] = 0.f;
+        }
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) top = fmaxf(top, xm[i]);
@@ -714,7 +720,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, E4M3, NH>::NW, 1) attn_decode_kern
     for (int e = threadIdx.x; e < heads * (D / 4); e += TH) {
       const int h = e / (D / 4), c = e % (D / 4);
       Sum4 sum;
-      sum.add(0, 1, cnt, [&](int i, float4& x, float& xm, float& xl) {
+      sum.template add<!E4M3>(0, 1, cnt, [&](int i, float4& x, float& xm, float& xl) {
         const int y = s_order[at + i];
         x = *reinterpret_cast<const float4*>(s_part[y].o + part_at<D>(h, c * 4));
         xm = s_ml[y][h];
@@ -753,7 +759,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   if (h >= min(16, p.group - h0)) return;
   const int r = threadIdx.x / V, c = threadIdx.x % V;
   Sum4 sum;
-  sum.add(r, R, n, [&](int i, float4& x, float& xm, float& xl) {
+  sum.template add<!E4M3>(r, R, n, [&](int i, float4& x, float& xm, float& xl) {
     // CTA blockIdx.x + i: its partial of a head that begins there (1) or before (0)
     const float* o = p.parts + (int64_t)((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * C::kPart;
     x = *reinterpret_cast<const float4*>(o + part_at<D>(h, c * 4));
@@ -768,7 +774,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   __syncthreads();
   if (r) return;
   Sum4 all;
-  all.add(0, 1, min(R, n), [&](int i, float4& x, float& xm, float& xl) {
+  all.template add<!E4M3>(0, 1, min(R, n), [&](int i, float4& x, float& xm, float& xl) {
     x = s_acc[i][c];
     xm = s_ml[i][0];
     xl = s_ml[i][1];

@@ -635,3 +635,25 @@ def test_binding_refusals(m):
         with pytest.raises(ValueError):
             append(**kw)
     assert status(m, ws) == 0
+
+
+@pytest.mark.parametrize("lens", [[700], [20000], [0, 40, 9001, 3]], ids=str)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_token_infinite_values_seen(m, d, lens):
+    """An infinite value in a sequence that is cut over warps and SMs gives an infinite output, wherever it
+    lies (the last key too, which the last part holds), and changes no other column."""
+    dims, at = m.AttnDims(4, 2, d), max(range(len(lens)), key=lambda b: lens[b])
+    n = lens[at]
+    cache, table, vals = make_cache(m, dims, lens, 16, False, seed=31)
+    where = {0: n - 1, 5: 0, 6: n // 2, d - 1: n - 2}                 # column -> key
+    for i, (c, key) in enumerate(where.items()):
+        bad = math.inf if i % 2 == 0 else -math.inf
+        cache.v[table[at, key // 16].long(), :, key % 16, c] = -128 if bad < 0 else 0x7F80  # 0xFF80, 0x7F80
+        vals[at][1][:, key, c] = 0.0
+    q = rand(33, len(lens), 4, d, gain=0.5)
+    o, lse = run_decode(m, cache, q.view(torch.int16).cuda(), lens, table)
+    ref, got = decode_ref(q, vals, 1 / math.sqrt(d)), C.values(o)
+    for i, c in enumerate(where):
+        assert (got[at, :, c] == (math.inf if i % 2 == 0 else -math.inf)).all(), (c, got[at, :, c])
+        got[at, :, c] = ref[0][at, :, c]
+    C.check(got.to(torch.bfloat16).view(torch.int16), lse, ref, 8, f"{d} {lens}")
