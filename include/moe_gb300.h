@@ -47,7 +47,8 @@
  *   - State kept across calls: per-process caches set once (the driver entry point that encodes
  *     TMA descriptors, the SM count of the device, the kernels' shared-memory attributes) and,
  *     for moe_decode_noalloc only, a fixed device array; no call result depends on an earlier
- *     call. Calls on different streams with different workspaces may run concurrently
+ *     call. The caches hold for one device, the one current at the first call: a process uses the
+ *     library on that device only, with it current and with all pointers of a call on it. Calls on different streams with different workspaces may run concurrently
  *     (moe_decode_noalloc excepted: see there).
  */
 #ifndef MOE_GB300_H

@@ -2,7 +2,8 @@
 paged key-value cache (KvCache, kv_append) and one new token per sequence over it (attn_decode).
 
 As in the rest of the package, bf16 tensors are int16 bit patterns, calls are asynchronous on the
-current torch stream, and PyTorch supplies device memory only.
+current torch stream, and PyTorch supplies device memory only. All tensors of a call lie on the
+current device (ValueError otherwise): that is where the library launches.
 """
 from __future__ import annotations
 
@@ -52,10 +53,18 @@ def _fn(name: str):
     return f
 
 
-def _stream(t: torch.Tensor) -> int:
-    """The current stream of t's device, as a handle (without building a torch.cuda.Stream, which
+def _device(t: torch.Tensor, name: str) -> int:
+    """The current device, on which t has to lie."""
+    dev = t.get_device()  # -1 on the host
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return dev
+
+
+def _stream(dev: int) -> int:
+    """The current stream of a device, as a handle (without building a torch.cuda.Stream, which
     costs as much as a kernel launch)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def attn_workspace_bytes(dims: AttnDims) -> int:
@@ -70,10 +79,11 @@ def attn_workspace(dims: AttnDims, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _view(t: torch.Tensor, heads: int, d: int, name: str) -> HeadsView:
+# What follows checks that a tensor lies on device `dev`, the current one.
+def _view(t: torch.Tensor, heads: int, d: int, name: str, dev: int) -> HeadsView:
     shape = t.shape
-    if t.dtype is not torch.int16 or not t.is_cuda or len(shape) != 3 or shape[1] != heads or shape[2] != d:
-        raise ValueError(f"{name} must be a CUDA int16 tensor [tokens, {heads}, {d}]")
+    if t.dtype is not torch.int16 or t.get_device() != dev or len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name} must be an int16 tensor [tokens, {heads}, {d}] on the current CUDA device")
     s = t.stride()
     if s[2] != 1:
         raise ValueError(f"{name}: the values of one head must be contiguous")
@@ -81,32 +91,33 @@ def _view(t: torch.Tensor, heads: int, d: int, name: str) -> HeadsView:
     return HeadsView(t.data_ptr(), s[0] if shape[0] > 1 else d, s[1] if heads > 1 else d)
 
 
-def _ints(t: torch.Tensor, n: int | None, name: str) -> int:
-    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous() or (n is not None and t.numel() != n):
-        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor" + ("" if n is None else f" of {n}"))
+def _ints(t: torch.Tensor, n: int | None, name: str, dev: int) -> int:
+    if t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous int32 tensor" + ("" if n is None else f" of {n}") +
+                         " on the current CUDA device")
     return t.data_ptr()
 
 
-def _ws(ws: torch.Tensor) -> int:
-    if ws.dtype is not torch.uint8 or not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("ws must be a contiguous CUDA uint8 tensor (attn_workspace)")
+def _ws(ws: torch.Tensor, dev: int) -> int:
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 tensor on the current CUDA device (attn_workspace)")
     return ws.data_ptr()
 
 
-def _lse(lse: torch.Tensor | None, rows: int, heads: int) -> int | None:
+def _lse(lse: torch.Tensor | None, rows: int, heads: int, dev: int) -> int | None:
     if lse is None:
         return None
-    if lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous() or lse.shape != (rows, heads):
-        raise ValueError(f"lse must be a contiguous CUDA float32 tensor [{rows}, {heads}]")
+    if lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous() or lse.shape != (rows, heads):
+        raise ValueError(f"lse must be a contiguous float32 tensor [{rows}, {heads}] on the current CUDA device")
     return lse.data_ptr()
 
 
-def _out(o: torch.Tensor | None, q: torch.Tensor) -> torch.Tensor:
+def _out(o: torch.Tensor | None, q: torch.Tensor, dev: int) -> torch.Tensor:
     if o is None:
         return torch.empty_like(q, memory_format=torch.contiguous_format)
     rows, heads, d = q.shape
-    if o.dtype is not torch.int16 or not o.is_cuda or not o.is_contiguous() or o.shape != (rows, heads, d):
-        raise ValueError(f"o must be a contiguous CUDA int16 tensor [{rows}, {heads}, {d}]")
+    if o.dtype is not torch.int16 or o.get_device() != dev or not o.is_contiguous() or o.shape != (rows, heads, d):
+        raise ValueError(f"o must be a contiguous int16 tensor [{rows}, {heads}, {d}] on the current CUDA device")
     return o
 
 
@@ -118,15 +129,16 @@ def attn_prefill(dims: AttnDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     int32 [n_seqs + 1] on the device. scale defaults to 1 / sqrt(head_dim). Returns o; lse, if
     given, receives the rows' log sums [total_q, n_q_heads]."""
     hq, hkv, d = dims.n_q_heads, dims.n_kv_heads, dims.head_dim
-    qv, kv, vv = _view(q, hq, d, "q"), _view(k, hkv, d, "k"), _view(v, hkv, d, "v")
+    dev = _device(q, "q")
+    qv, kv, vv = _view(q, hq, d, "q", dev), _view(k, hkv, d, "k", dev), _view(v, hkv, d, "v", dev)
     tq, tk, n = q.shape[0], k.shape[0], cu_q.numel() - 1
     if v.shape[0] != tk:
         raise ValueError("k and v must have the same number of rows")
-    o = _out(o, q)
-    _check(_fn("moe_attn_prefill")(ctypes.byref(dims), qv, kv, vv, _ints(cu_q, None, "cu_q"),
-                                   _ints(cu_k, n + 1, "cu_k"), n, tq, tk,
+    o = _out(o, q, dev)
+    _check(_fn("moe_attn_prefill")(ctypes.byref(dims), qv, kv, vv, _ints(cu_q, None, "cu_q", dev),
+                                   _ints(cu_k, n + 1, "cu_k", dev), n, tq, tk,
                                    1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, o.data_ptr(),
-                                   _lse(lse, tq, hq), _ws(ws), ws.numel(), _stream(q)), "moe_attn_prefill")
+                                   _lse(lse, tq, hq, dev), _ws(ws, dev), ws.numel(), _stream(dev)), "moe_attn_prefill")
     return o
 
 
@@ -150,6 +162,8 @@ class KvCache:
             _check_dev(s, torch.float32, name)
             if s.shape != (dims.n_kv_heads,):
                 raise ValueError(f"{name} must have {dims.n_kv_heads} values")
+        if any(t.get_device() != k.get_device() for t in ((v, k_scale, v_scale) if fp8 else (v,))):
+            raise ValueError("a cache's tensors must be on one device")
         self.dims, self.k, self.v, self.k_scale, self.v_scale = dims, k, v, k_scale, v_scale
         self._c = KvCacheC(dims, KV_E4M3 if fp8 else KV_BF16, k.shape[2], k.shape[0], k.data_ptr(), v.data_ptr(),
                            k_scale.data_ptr() if fp8 else None, v_scale.data_ptr() if fp8 else None)
@@ -172,10 +186,16 @@ class KvCache:
         return self._c
 
 
-def _table(page_table: torch.Tensor, n: int) -> int:
+def _cache(cache: KvCache, dev: int):
+    if cache.k.get_device() != dev:
+        raise ValueError("the cache must be on the current CUDA device")
+    return ctypes.byref(cache._c)
+
+
+def _table(page_table: torch.Tensor, n: int, dev: int) -> int:
     if page_table.dim() != 2 or page_table.shape[0] != n:
         raise ValueError(f"page_table must be [{n}, pages per sequence]")
-    return _ints(page_table, None, "page_table")
+    return _ints(page_table, None, "page_table", dev)
 
 
 def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, start: torch.Tensor,
@@ -183,13 +203,14 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor
     """moe_kv_append: row i of sequence b (rows cu[b] .. cu[b + 1] - 1 of k and v [total,
     n_kv_heads, head_dim]) is written at position start[b] + i of the cache."""
     dims = cache.dims
-    kv, vv = _view(k, dims.n_kv_heads, dims.head_dim, "k"), _view(v, dims.n_kv_heads, dims.head_dim, "v")
+    dev = _device(k, "k")
+    kv, vv = (_view(t, dims.n_kv_heads, dims.head_dim, name, dev) for t, name in ((k, "k"), (v, "v")))
     total, n = k.shape[0], start.numel()
     if v.shape[0] != total:
         raise ValueError("k and v must have the same number of rows")
-    _check(_fn("moe_kv_append")(ctypes.byref(cache._c), kv, vv, _ints(cu, n + 1, "cu"), _ints(start, n, "start"),
-                                _table(page_table, n), page_table.shape[1], n, total, _ws(ws), ws.numel(),
-                                _stream(k)), "moe_kv_append")
+    _check(_fn("moe_kv_append")(_cache(cache, dev), kv, vv, _ints(cu, n + 1, "cu", dev), _ints(start, n, "start", dev),
+                                _table(page_table, n, dev), page_table.shape[1], n, total, _ws(ws, dev), ws.numel(),
+                                _stream(dev)), "moe_kv_append")
 
 
 def attn_decode(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, page_table: torch.Tensor, ws: torch.Tensor, *,
@@ -199,10 +220,11 @@ def attn_decode(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, page_table:
     of sequence b. Returns o; lse, if given, receives the rows' log sums [n_seqs, n_q_heads]."""
     dims = cache.dims
     hq, d, n = dims.n_q_heads, dims.head_dim, q.shape[0]
-    qv = _view(q, hq, d, "q")
-    o = _out(o, q)
-    _check(_fn("moe_attn_decode")(ctypes.byref(cache._c), qv, _ints(lens, n, "lens"), _table(page_table, n),
+    dev = _device(q, "q")
+    qv = _view(q, hq, d, "q", dev)
+    o = _out(o, q, dev)
+    _check(_fn("moe_attn_decode")(_cache(cache, dev), qv, _ints(lens, n, "lens", dev), _table(page_table, n, dev),
                                   page_table.shape[1], n, 1.0 / math.sqrt(d) if scale is None else scale,
-                                  o.data_ptr(), _lse(lse, n, hq), _ws(ws), ws.numel(), _stream(q)),
+                                  o.data_ptr(), _lse(lse, n, hq, dev), _ws(ws, dev), ws.numel(), _stream(dev)),
            "moe_attn_decode")
     return o

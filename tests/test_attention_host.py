@@ -106,3 +106,64 @@ def test_binding_refuses_host_tensors(m):
         m.KvCache(dims, torch.zeros(3, 2, 16, 64, dtype=torch.int16), torch.zeros(3, 2, 16, 64, dtype=torch.int16))
     with pytest.raises(ValueError):
         m.KvCache(dims, torch.zeros(3, 2, 16, 64), torch.zeros(3, 2, 16, 64))
+
+
+class Placed(torch.Tensor):
+    """A host tensor that says it lies on CUDA device `place`."""
+    place = 0
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.place
+
+
+def place(t, dev):
+    t = t.as_subclass(Placed)
+    t.place = dev
+    return t
+
+
+def test_binding_refuses_other_devices(m, monkeypatch):
+    """Every tensor of a call lies on the current device; else nothing reaches the library."""
+    from quantized_grouped_gemm_router_gb300 import attention
+    reached = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(attention, "_fn", lambda name: lambda *a: reached.append(name) or 0)
+    dims, i16, i32 = m.AttnDims(4, 2, 64), torch.int16, torch.int32
+
+    def rows(h):
+        return torch.zeros(3, h, 64, dtype=i16)
+
+    def cells():
+        return torch.zeros(3, 2, 16, 64, dtype=torch.uint8)
+
+    def calls():
+        """name -> (call, its tensors)"""
+        ws, lse = torch.zeros(256, dtype=torch.uint8), torch.zeros(3, 4)
+        cu, table = torch.tensor([0, 3], dtype=i32), torch.zeros(1, 2, dtype=i32)
+        kv = dict(k=cells(), v=cells(), k_scale=torch.ones(2), v_scale=torch.ones(2))
+        return {
+            "moe_attn_prefill": (lambda t: m.attn_prefill(dims, t["q"], t["k"], t["v"], t["cu_q"], t["cu_k"], t["ws"],
+                                                          o=t["o"], lse=t["lse"]),
+                                 dict(q=rows(4), k=rows(2), v=rows(2), cu_q=cu, cu_k=cu, ws=ws, o=rows(4), lse=lse)),
+            "moe_kv_append": (lambda t: m.kv_append(m.KvCache(dims, *(t["c_" + n] for n in kv)), t["k"], t["v"], t["cu"],
+                                                    t["start"], t["table"], t["ws"]),
+                              dict({"c_" + n: x for n, x in kv.items()}, k=rows(2), v=rows(2), cu=cu,
+                                   start=torch.zeros(1, dtype=i32), table=table, ws=ws)),
+            "moe_attn_decode": (lambda t: m.attn_decode(m.KvCache(dims, *(t["c_" + n] for n in kv)), t["q"], t["lens"],
+                                                        t["table"], t["ws"], o=t["o"], lse=t["lse"]),
+                                dict({"c_" + n: x for n, x in kv.items()}, q=rows(4), lens=torch.ones(3, dtype=i32),
+                                     table=torch.zeros(3, 2, dtype=i32), ws=ws, o=rows(4), lse=lse)),
+        }
+
+    for name, (call, tensors) in calls().items():
+        for current in (0, 1):
+            call({n: place(t, current) for n, t in tensors.items()})
+            assert reached.pop() == name
+            with pytest.raises(ValueError):
+                call({n: place(t, 1 - current) for n, t in tensors.items()})
+            for odd in tensors:
+                with pytest.raises(ValueError):
+                    call({n: place(t, 1 - current if n == odd else current) for n, t in tensors.items()})
+                assert not reached, (name, odd)
