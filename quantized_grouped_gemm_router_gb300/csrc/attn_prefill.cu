@@ -99,6 +99,18 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
+// mbar_wait for what may take as long as an item (2^30 keys: about 3e10 cycles): until one of the others' waits, which
+// all end within a few steps, has given up.
+__device__ __forceinline__ bool mbar_wait_item(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (*abort_flag || clock64() - t0 > 64 * kWaitCycles) {
+      *abort_flag = 1;
+      return false;
+    }
+  return true;
+}
+
 // What a CTA works on.
 struct Item {
   int head;          // key-value head, -1: there is no item
@@ -351,9 +363,11 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
   // (V tiles checked). Step n of an item: key tile n / NQ; global number nb + n. With two row tiles the
   // ring's order is K0 V0 K1 V1 ... (each used by two steps), else K0 K1 V0 K2 V1 ...
   const auto wait = [&](uint32_t bar, int parity) { return __all_sync(~0u, mbar_wait(bar, parity & 1, s_abort)); };
+  // the same for the warp that checks V tiles, which has nothing to do for most of an item
+  const auto wait_item = [&](uint32_t bar, int parity) { return __all_sync(~0u, mbar_wait_item(bar, parity & 1, s_abort)); };
   // the t-th item of this CTA; the slot is handed back
   const auto take_item = [&](int t, Item& it) {
-    if (!wait(item_full(t & 1), t >> 1)) return false;
+    if (!(warp == C::kWarpCheck ? wait_item(item_full(t & 1), t >> 1) : wait(item_full(t & 1), t >> 1))) return false;
     it = s_item[t & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(item_free(t & 1));
@@ -551,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         if (sp.nj) r += C::kQEntries;
         for (int j = sp.masked; j < sp.nj; ++j, ++x) {
           const int s = (r + v_at(j, sp.nj)) % kSlots, b = x & 1;
-          if (!(ok = wait(check(b), x >> 1))) break;
+          if (!(ok = wait_item(check(b), x >> 1))) break;
           // 0 times a NaN or an infinity is a NaN, 0 times all else is 0; 32 keys at a time, from the first that some
           // row does not see
           uint32_t h0 = 0, h1 = 0, h2 = 0, h3 = 0;

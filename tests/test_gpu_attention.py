@@ -657,3 +657,25 @@ def test_token_infinite_values_seen(m, d, lens):
         assert (got[at, :, c] == (math.inf if i % 2 == 0 else -math.inf)).all(), (c, got[at, :, c])
         got[at, :, c] = ref[0][at, :, c]
     C.check(got.to(torch.bfloat16).view(torch.int16), lse, ref, 8, f"{d} {lens}")
+
+
+@pytest.mark.parametrize("less", [0, 1], ids=["whole_tiles", "ragged"])
+def test_prompt_item_longer_than_a_wait(m, less):
+    """A row over 100 million keys of 256 values: its one item takes longer than any single wait may (2e9 cycles;
+    64 keys take 1600). Three keys, the first and the last among them, have all the weight."""
+    d, n, lk = 256, 100_000_000, 100_000_000 - less
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 51 GB of keys")
+    rows = torch.zeros((n, 1, d), dtype=torch.int16, device="cuda")     # keys and values alike
+    q = torch.zeros(1, 1, d, dtype=torch.bfloat16)
+    q[..., :16] = 10.0
+    x = rand(1, 3, 1, d)
+    x[..., :16] = 8.0                                                   # a score of 80, and 0 for every other key
+    for at, row in zip((0, 31_234_567, lk - 1), x):
+        rows[at] = row.view(torch.int16).cuda()
+    k = rows[:lk]
+    o, lse = run_prefill(m, m.AttnDims(1, 1, d), q.view(torch.int16).cuda(), k, k, [(1, lk)], False)
+    del rows, k
+    torch.cuda.empty_cache()
+    C.check(o, lse, [x.double().mean(0)[None], torch.tensor([[80 + math.log(3)]]).double(),
+                     x.double().abs().mean(0)[None]], 8)
