@@ -22,6 +22,8 @@ struct AttnPrefillParams {
   int o_wide;  // o is 32-byte aligned
   float* lse;
   WsHeader* hdr;
+  float* aside;      // [kAttnMaxCtas][2][128 x d] sums put aside during long items, of 128 rows each
+  float2* aside_ml;  // [kAttnMaxCtas][2][128] their (m c, l)
 };
 
 // Division by an invariant: n / d = (t + ((n - t) >> s1)) >> s2 with t = the high half of m n, for every
@@ -83,7 +85,8 @@ struct AttnDecodeParams {
   float* scratch;  // [kAttnMaxCtas * kAttnMaxWarps] partial rows of a warp
 };
 
-// Workspace of the attention calls: status word, then what the decode's two kernels hand over.
+// Workspace of the attention calls: status word, then what the decode's two kernels hand over. The prompt kernel puts
+// sums aside in the place of scratch, and their statistics in that of parts.
 constexpr int kAttnMaxCtas = 256;
 constexpr int kAttnMaxWarps = 16;
 struct AttnWs {
@@ -95,6 +98,7 @@ inline AttnWs attn_ws(const moe_attn_dims& d) {
   w.splits = sizeof(WsHeader);
   w.parts = w.splits + kAttnMaxCtas * sizeof(int4);
   w.scratch = w.parts + (size_t)kAttnMaxCtas * 2 * (rows + 128);
+  static_assert(2 * 128 <= 16 * kAttnMaxWarps && 2 * 128 * sizeof(float2) <= 2 * (16 * 64 * 4 + 128), "a CTA's two row tiles");
   w.total = w.scratch + (size_t)kAttnMaxCtas * kAttnMaxWarps * rows;
   return w;
 }

@@ -93,7 +93,10 @@ int moe_attn_prefill(const moe_attn_dims* dims, moe_heads_view q, moe_heads_view
   p.o = o;
   p.o_wide = aligned(o, 32);
   p.lse = lse;
+  const AttnWs w = attn_ws(*dims);
   p.hdr = static_cast<WsHeader*>(ws);
+  p.aside = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.scratch);
+  p.aside_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + w.parts);
   return launch_attn_prefill(p, dims->head_dim, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

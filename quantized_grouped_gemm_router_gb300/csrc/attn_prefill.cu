@@ -47,6 +47,7 @@ __device__ __forceinline__ void regs_for_issue() { asm volatile("setmaxnreg.dec.
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kPutKeys = 32768;  // keys of a stream that are summed up in tensor memory
 
 // What a CTA's streams of steps are: two row tiles over the same keys, two halves of one row tile's keys
 // (even and odd tiles), or one row tile alone (D = 256: tensor memory holds one O). In kOne both softmax
@@ -208,6 +209,40 @@ __device__ __forceinline__ float max_of(const float* s) {
   return max3(m[0], m[1], fmaxf(m[2], m[3]));
 }
 
+// The N values of O at ot and those put aside, times f (none if first), added: OUT: put aside, O becomes 0; else into O.
+template <int N, bool OUT>
+__device__ __forceinline__ void add_aside(uint32_t ot, float4* at, float f, bool first) {
+#pragma unroll 1
+  for (int i = 0; i < N; i += 16) {
+    uint32_t o[16];
+    tmem_ld16(ot + i, o);
+    tmem_wait_ld16(o);
+#pragma unroll
+    for (int x = 0; x < 16; x += 4) {
+      float4* p = at + (i + x) / 4 * 128;
+      float4 y = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *p;
+      y.x = fmaf(y.x, f, __uint_as_float(o[x]));
+      y.y = fmaf(y.y, f, __uint_as_float(o[x + 1]));
+      y.z = fmaf(y.z, f, __uint_as_float(o[x + 2]));
+      y.w = fmaf(y.w, f, __uint_as_float(o[x + 3]));
+      if (OUT) {
+        *p = y;
+        y = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      o[x] = __float_as_uint(y.x);
+      o[x + 1] = __float_as_uint(y.y);
+      o[x + 2] = __float_as_uint(y.z);
+      o[x + 3] = __float_as_uint(y.w);
+    }
+    tmem_st16(ot + i, o);
+  }
+  tmem_wait_st();
+}
+template <int N, bool OUT>
+__device__ __noinline__ void add_aside_call(uint32_t ot, float4* at, float f, bool first) {
+  add_aside<N, OUT>(ot, at, f, first);
+}
+
 // One row's running softmax. Weights are relative to m, which follows the maximum only when that has
 // grown by more than 2^8.
 struct Softmax {
@@ -258,6 +293,27 @@ struct Softmax {
       tmem_st16(to + i / 2, w);
     }
   }
+  // Long contexts. Each product that the tensor cores add to O takes about 2^-23 of O's size from it, always towards
+  // zero: after 32768 keys with values of one sign O is 0.03% low, after 4 million it was 2.5%. So every kPutKeys keys
+  // of a stream the row's O, l and m are put aside, in memory that only this thread reads, and O starts from 0 again.
+  // to: the row's first four values, 128 float4 further the next four; ml: (m c, l). O is at rest.
+  // CALL: not inlined, for want of registers (1024 tokens on 131072, heads of 256: 2.5% slower inlined).
+  template <int N, bool CALL>
+  __device__ __forceinline__ void put_aside(uint32_t ot, float4* to, float2* ml, bool first) {
+    const float2 before = first ? make_float2(-INFINITY, 0.f) : *ml;
+    const float f = ex2(before.x - mc);
+    *ml = make_float2(m == -INFINITY ? -INFINITY : mc, fmaf(before.y, f, sum()));
+    l[0] = l[1] = 0;
+    CALL ? add_aside_call<N, true>(ot, to, f, first) : add_aside<N, true>(ot, to, f, first);
+  }
+  // Back into O and l for the output.
+  template <int N, bool CALL>
+  __device__ __forceinline__ void take_back(uint32_t ot, float4* from, const float2* ml) {
+    const float2 before = *ml;
+    const float f = ex2(before.x - mc);
+    l[0] = add2(l[0], pack2(before.y * f, 0.f));
+    CALL ? add_aside_call<N, false>(ot, from, f, false) : add_aside<N, false>(ot, from, f, false);
+  }
   __device__ __forceinline__ float sum() const {
     float x[4];
     unpack2(l[0], x[0], x[1]);
@@ -266,7 +322,7 @@ struct Softmax {
   }
 };
 
-template <int D, Mode M>
+template <int D, Mode M, bool LONG>
 __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
     attn_prefill_kernel(const __grid_constant__ AttnPrefillParams p, const __grid_constant__ Maps maps) {
   using C = Cfg<D, M>;
@@ -600,6 +656,11 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
     const int col0 = M == kRows ? 0 : wg * kCols;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
     const uint32_t ot = lanes + C::kOCol + a * D;
+    constexpr int kPut = kPutKeys / BN;  // steps of a stream between two times that it puts its sums aside
+    constexpr int kPutCols = M == kOne ? kCols : D;
+    const uint32_t put_ot = ot + (M == kOne ? col0 : 0);
+    const auto put_o = [&] { return reinterpret_cast<float4*>(p.aside + (int64_t)(blockIdx.x * 2 + wg) * (128 * D)) + row; };
+    const auto put_ml = [&] { return p.aside_ml + (blockIdx.x * 2 + wg) * 128 + row; };
     int r = 0, nb = 0, x0 = 0, used = 0;
     int exchanged = 0;  // kOne
     // kOne: this thread's value and the other half's of the same row
@@ -651,93 +712,105 @@ __global__ void __launch_bounds__(Cfg<D, M>::kThreads, 1)
         r += C::kQEntries;
       }
       int last = -1;  // this stream's last step's number within the stream, over all items
-      for (int n = NT == 2 ? (a - nb) & 1 : 0; n < sp.steps; n += NT) {
-        const int j = n / NQ, g = nb + n, b = g & 1, k = NT == 2 ? g >> 1 : g;
-        const bool first = n < NT;
-        const uint32_t st = lanes + b * BN;
-        last = k;
-        if (!(ok = wait(s_full(b), g >> 1))) break;
-        tc_fence_after();
-        // Two halves (BN = 128): the second one's scores are on their way while the first one's weights are
-        // made, the first one's product is under way while the second one's are.
-        const bool masked = j >= sp.masked;
-        const int lim = seen - j * BN, x = x0 + j - sp.masked;
-        if constexpr (M == kOne) {
-          float s[32], other;
-          tmem_ld32(st + wg * 32, s);
-          tmem_wait_ld32(s);
-          if (masked) unsee<32>(s, lim - wg * 32);
-          const float mine = max_of<32>(s);
-          if (!(ok = exchange(mine, other) && grow(fmaxf(mine, other), first, pv_done(a), k - 1))) break;
-          soft.template weights<32>(s, st + wg * 16);
+      int n = NT == 2 ? (a - nb) & 1 : 0;
+      const int begin = n;
+      for (int end = LONG ? min(NT * kPut, sp.steps) : sp.steps;;) {  // up to where the sums are put aside, or the last step
+        for (; n < end; n += NT) {
+          const int j = n / NQ, g = nb + n, b = g & 1, k = NT == 2 ? g >> 1 : g;
+          const bool first = n < NT;
+          const uint32_t st = lanes + b * BN;
+          last = k;
+          if (!(ok = wait(s_full(b), g >> 1))) break;
+          tc_fence_after();
+          // Two halves (BN = 128): the second one's scores are on their way while the first one's weights are
+          // made, the first one's product is under way while the second one's are.
+          const bool masked = j >= sp.masked;
+          const int lim = seen - j * BN, x = x0 + j - sp.masked;
+          if constexpr (M == kOne) {
+            float s[32], other;
+            tmem_ld32(st + wg * 32, s);
+            tmem_wait_ld32(s);
+            if (masked) unsee<32>(s, lim - wg * 32);
+            const float mine = max_of<32>(s);
+            if (!(ok = exchange(mine, other) && grow(fmaxf(mine, other), first, pv_done(a), k - 1))) break;
+            soft.template weights<32>(s, st + wg * 16);
+            tmem_wait_st();
+            if (masked) {
+              if (!(ok = wait(checked(x & 1), x >> 1))) break;
+              if (s_bad[x & 1]) {
+                // both halves' weights are there, and O is at rest
+                if (!(ok = exchange(0.f, other) && (first ? used == 0 || wait(o_free(a), used - 1) : wait(pv_done(a), k - 1)))) break;
+                tc_fence_after();
+                add_seen<kCols>(ot + col0, st, ring + (r + v_at(j, sp.nj)) % kSlots * C::kSlot + wg * (C::kChunks / 2) * (BN * 128),
+                                BN * 128, lim, first);
+              }
+            }
+            // The end of the item waits for the last product. A wait tells a phase from the next one only, and these
+            // scores came after all products but the last two: the one before the last is waited for here, while
+            // the last one cannot have been made.
+            if (n > 0 && n == end - 1 && !(ok = wait(pv_done(a), k - 1))) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(p_half(b));
+              mbar_arrive(p_ready(b));
+            }
+            continue;
+          }
+          float s0[64], s1[64], mx = -INFINITY;
+          bool bad = false;
+          tmem_ld32(st, s0);
+          tmem_ld32(st + 32, s0 + 32);
+          tmem_wait_ld32(s0);
+          tmem_wait_ld32(s0 + 32);
+          if (BN == 128) {
+            tmem_ld32(st + 64, s1);
+            tmem_ld32(st + 96, s1 + 32);
+          }
+          if (masked) unsee<64>(s0, lim);
+          if (!(ok = grow(max_of<64>(s0), first, pv_done(a), k - 1))) break;
+          soft.template weights<64>(s0, st);
+          if (BN == 128) {
+            tmem_wait_ld32(s1);
+            tmem_wait_ld32(s1 + 32);
+            if (masked) unsee<64>(s1, lim - 64);
+            mx = max_of<64>(s1);
+          }
           tmem_wait_st();
           if (masked) {
             if (!(ok = wait(checked(x & 1), x >> 1))) break;
-            if (s_bad[x & 1]) {
-              // both halves' weights are there, and O is at rest
-              if (!(ok = exchange(0.f, other) && (first ? used == 0 || wait(o_free(a), used - 1) : wait(pv_done(a), k - 1)))) break;
+            bad = s_bad[x & 1];
+            if (bad) {
+              // O at rest: its last product, or (a new item's first) read by every warp
+              if (!(ok = first ? used == 0 || wait(o_free(a), used - 1) : wait(pv_done(a), k - 1))) break;
               tc_fence_after();
-              add_seen<kCols>(ot + col0, st, ring + (r + v_at(j, sp.nj)) % kSlots * C::kSlot + wg * (C::kChunks / 2) * (BN * 128),
-                              BN * 128, lim, first);
+              add_seen<D>(ot, st, ring + (r + v_at(j, sp.nj)) % kSlots * C::kSlot, BN * 128, lim, first);
             }
           }
-          // The end of the item waits for the last product. A wait tells a phase from the next one only, and these
-          // scores came after all products but the last two: the one before the last is waited for here, while
-          // the last one cannot have been made.
-          if (n > 0 && n == sp.steps - 1 && !(ok = wait(pv_done(a), k - 1))) break;
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(p_half(b));
-            mbar_arrive(p_ready(b));
+          if (lane == 0) mbar_arrive(p_half(b));
+          if (BN == 128) {
+            if (!(ok = grow(mx, false, pv_half(a), k))) break;
+            soft.template weights<64>(s1, st + 32);
+            tmem_wait_st();
+            if (bad)
+              add_seen<D>(ot, st + 32, ring + (r + v_at(j, sp.nj)) % kSlots * C::kSlot + 64 * 128, BN * 128, lim - 64, false);
+            tc_fence_before();
+            __syncwarp();
           }
-          continue;
+          if (lane == 0) mbar_arrive(p_ready(b));
         }
-        float s0[64], s1[64], mx = -INFINITY;
-        bool bad = false;
-        tmem_ld32(st, s0);
-        tmem_ld32(st + 32, s0 + 32);
-        tmem_wait_ld32(s0);
-        tmem_wait_ld32(s0 + 32);
-        if (BN == 128) {
-          tmem_ld32(st + 64, s1);
-          tmem_ld32(st + 96, s1 + 32);
-        }
-        if (masked) unsee<64>(s0, lim);
-        if (!(ok = grow(max_of<64>(s0), first, pv_done(a), k - 1))) break;
-        soft.template weights<64>(s0, st);
-        if (BN == 128) {
-          tmem_wait_ld32(s1);
-          tmem_wait_ld32(s1 + 32);
-          if (masked) unsee<64>(s1, lim - 64);
-          mx = max_of<64>(s1);
-        }
-        tmem_wait_st();
-        if (masked) {
-          if (!(ok = wait(checked(x & 1), x >> 1))) break;
-          bad = s_bad[x & 1];
-          if (bad) {
-            // O at rest: its last product, or (a new item's first) read by every warp
-            if (!(ok = first ? used == 0 || wait(o_free(a), used - 1) : wait(pv_done(a), k - 1))) break;
-            tc_fence_after();
-            add_seen<D>(ot, st, ring + (r + v_at(j, sp.nj)) % kSlots * C::kSlot, BN * 128, lim, first);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_half(b));
-        if (BN == 128) {
-          if (!(ok = grow(mx, false, pv_half(a), k))) break;
-          soft.template weights<64>(s1, st + 32);
-          tmem_wait_st();
-          if (bad)
-            add_seen<D>(ot, st + 32, ring + (r + v_at(j, sp.nj)) % kSlots * C::kSlot + 64 * 128, BN * 128, lim - 64, false);
-          tc_fence_before();
-          __syncwarp();
-        }
-        if (lane == 0) mbar_arrive(p_ready(b));
+        if (ok && last >= 0) ok = wait(pv_done(a), last);
+        if (!LONG || !ok || end == sp.steps) break;
+        tc_fence_after();
+        if (n < sp.steps) soft.template put_aside<kPutCols, M == kOne>(put_ot, put_o(), put_ml(), end == NT * kPut);
+        end = min(end + NT * kPut, sp.steps);
       }
-      if (ok && last >= 0) ok = wait(pv_done(a), last);
+      if (LONG && ok && sp.steps > begin + NT * kPut) {
+        tc_fence_after();
+        soft.template take_back<kPutCols, M == kOne>(put_ot, put_o(), put_ml());
+      }
       // the factor of O (kKeys: of the even tiles' O and the odd tiles') in the output, and the row's log sum
       float f = 0.f, f2 = 0.f, lse = -INFINITY;
       float l = soft.sum(), l_other;
@@ -840,7 +913,7 @@ int num_sms() {
     int dev = 0, v = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       v = 1;
-    return v > 0 ? v : 1;
+    return v > kAttnMaxCtas ? kAttnMaxCtas : v > 0 ? v : 1;
   }();
   return n;
 }
@@ -853,16 +926,16 @@ bool make_map(CUtensorMap* m, const moe_heads_view& v, int d, int heads, int tok
   return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v.p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, Mode M>
+template <int D, Mode M, bool LONG = true>
 cudaError_t launch(const AttnPrefillParams& p, cudaStream_t s) {
   using C = Cfg<D, M>;
-  static cudaError_t attr = cudaFuncSetAttribute(attn_prefill_kernel<D, M>,
+  static cudaError_t attr = cudaFuncSetAttribute(attn_prefill_kernel<D, M, LONG>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (attr != cudaSuccess) return attr;
   // the register split waits for ever unless the launch brings what it hands out
   static int regs = [] {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, attn_prefill_kernel<D, M>) == cudaSuccess ? a.numRegs : 0;
+    return cudaFuncGetAttributes(&a, attn_prefill_kernel<D, M, LONG>) == cudaSuccess ? a.numRegs : 0;
   }();
   if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
   const int ppt = 128 / p.group;
@@ -876,7 +949,7 @@ cudaError_t launch(const AttnPrefillParams& p, cudaStream_t s) {
   // every sequence has at most one ragged tile
   const int64_t items = ((int64_t)p.total_q / (C::NQ * ppt) + (p.n_seqs < p.total_q ? p.n_seqs : p.total_q)) * p.hkv;
   if (items > 0x40000000) return cudaErrorInvalidValue;
-  return launch_pdl(attn_prefill_kernel<D, M>, dim3((unsigned)(items < num_sms() ? items : num_sms())), C::kThreads,
+  return launch_pdl(attn_prefill_kernel<D, M, LONG>, dim3((unsigned)(items < num_sms() ? items : num_sms())), C::kThreads,
                     (size_t)C::kSmem, 1, s, p, maps);
 }
 
@@ -897,7 +970,10 @@ cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int d, cudaStream_t 
                    (p.n_seqs > 1 && (!p.causal || rows <= 64) && 4 * ((each + rows - 1) / rows * p.n_seqs * p.hkv) >= 3 * sms);
   if (d == 64) return two ? launch<64, kRows>(p, s) : launch<64, kKeys>(p, s);
   if (d == 128) return two ? launch<128, kRows>(p, s) : launch<128, kKeys>(p, s);
-  return launch<256, kOne>(p, s);
+  // Heads of 256: the code that puts sums aside costs registers that the softmax needs (4096 tokens: 109.9 us without
+  // it, 111.9 with it), so that calls with fewer keys take a form without it.
+  // 1024 tokens on 131072 keys take 1687 us with sums put aside, 1648 without.
+  return p.total_k > kPutKeys ? launch<256, kOne, true>(p, s) : launch<256, kOne, false>(p, s);
 }
 
 }  // namespace moe

@@ -679,3 +679,60 @@ def test_prompt_item_longer_than_a_wait(m, less):
     torch.cuda.empty_cache()
     C.check(o, lse, [x.double().mean(0)[None], torch.tensor([[80 + math.log(3)]]).double(),
                      x.double().abs().mean(0)[None]], 8)
+
+
+def long_context_case(m, heads, d, lens, causal, seed, shape=None, sel=None):
+    """Values of one sign (what the sums lose would show) behind long contexts, made and checked on the GPU: `sel` rows
+    of the first and last head. shape(position / length), 0..1, adds up to 40 to the scores: as one exact product, the last
+    of a score, so that its rounding (2^-22 of at most 640, scaled by 1/16) stays within the scores' tolerance."""
+    (hq, hkv), g = heads, torch.Generator(device="cuda").manual_seed(seed)
+    tq, tk = sum(x for x, _ in lens), sum(x for _, x in lens)
+    q = (torch.randn(tq, hq, d, generator=g, device="cuda") * 0.5).to(torch.bfloat16)
+    if shape is not None:
+        q[:, :, d - 1] = 4.0
+    k = torch.empty((tk, hkv, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    for i in range(0, tk, 1 << 18):
+        n = min(1 << 18, tk - i)
+        k[i:i + n] = torch.randn(n, hkv, d, generator=g, device="cuda")
+        if shape is not None:
+            k[i:i + n, :, d - 1] = torch.round(10 * math.sqrt(d) * shape(torch.arange(i, i + n, device="cuda") / tk))[:, None]
+        v[i:i + n] = torch.rand(n, hkv, d, generator=g, device="cuda") + 0.5
+    o, lse = run_prefill(m, m.AttnDims(hq, hkv, d), *(x.view(torch.int16) for x in (q, k, v)), lens, causal)
+    a = b = 0
+    for lq, lk in lens:
+        rows = torch.tensor(range(lq) if sel is None else [r % lq for r in sel], device="cuda")
+        for h in {0, hq - 1}:
+            qd, top = q[a + rows, h].double(), torch.full((len(rows),), -math.inf, dtype=torch.float64, device="cuda")
+            acc, den = torch.zeros(len(rows), d, dtype=torch.float64, device="cuda"), torch.zeros_like(top)
+            for i in range(0, lk, 1 << 18):  # the definition, a running maximum over long pieces
+                n, kv = min(1 << 18, lk - i), h // (hq // hkv)
+                s = qd @ k[b + i:b + i + n, kv].double().t() / math.sqrt(d)
+                if causal:
+                    s.masked_fill_(torch.arange(i, i + n, device="cuda")[None] > (rows + lk - lq)[:, None], -math.inf)
+                t2 = torch.maximum(top, s.amax(1))
+                p, f = torch.exp(s - t2[:, None]), torch.exp(top - t2)
+                acc, den, top = acc * f[:, None] + p @ v[b + i:b + i + n, kv].double(), den * f + p.sum(1), t2
+            ref = [(acc / den[:, None]).cpu(), (top + den.log()).cpu(), (acc / den[:, None]).cpu()]
+            C.check(o[a + rows, h], lse[a + rows, h], ref, 8, f"{heads} {d} {lq} on {lk}, head {h}")
+        a, b = a + lq, b + lk
+
+
+@pytest.mark.parametrize("heads,d,lens,causal", [
+    ((2, 1), 64, [(3, 4_000_000)], True), ((2, 1), 128, [(3, 4_000_001)], False), ((2, 1), 256, [(3, 4_000_000)], True),
+    ((64, 8), 64, [(1300, 3_000_000)], True), ((64, 8), 128, [(1300, 3_000_001)], False)], ids=str)
+def test_prompt_millions_of_keys(m, heads, d, lens, causal):
+    """The tensor cores' sums lose a little with every product; over millions of keys it may not add up."""
+    long_context_case(m, heads, d, lens, causal, seed=3, sel=(0, 130, 1299))
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("shape", [None, lambda x: x, lambda x: 1 - x, lambda x: 1.0 * (x > 0.5)],
+                         ids=["flat", "rising", "falling", "step"])
+@pytest.mark.parametrize("heads,causal", [((16, 2), True), ((7, 1), False), ((2, 2), True)], ids=str)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_long_contexts(m, d, heads, causal, shape):
+    """Around the lengths at which sums are put aside (32768 keys of a stream of key tiles), with maxima that move."""
+    long_context_case(m, heads, d, [(3, 32768), (20, 65536), (1, 65700), (33, 131073), (5, 40)], causal, 5, shape)
+    many = (48 * heads[0] // heads[1], 48)                       # two row tiles to an item
+    long_context_case(m, many, d, [(300, 32900), (301, 70001)], causal, 6, shape, sel=(0, 150, 299))
