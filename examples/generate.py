@@ -93,6 +93,8 @@ class Decoder:
     def prefill(self, prompts: list[list[int]]) -> torch.Tensor:
         """Logits of each prompt's last token; the caches hold the prompts afterwards."""
         lens = [len(p) for p in prompts]
+        if not all(lens):
+            raise ValueError("a prompt has at least one token")
         cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
         start = torch.zeros(len(lens), dtype=torch.int32, device="cuda")
         x = self.embed[torch.tensor([t for p in prompts for t in p], device="cuda")]

@@ -65,3 +65,13 @@ def test_refuses_what_does_not_fit(ex):
         model.generate(ex.some_prompts()[:2], 3)
     with pytest.raises(ValueError):
         model.generate([[1] * 255, [1], [2]], 3)
+
+
+def test_refuses_empty_prompts(ex):
+    """A prompt without a token has no last token whose logits could be taken."""
+    model = ex.small()
+    for prompts in ([[1, 2], [], [3]], [[], [1], [2]], [[1], [2], []]):
+        with pytest.raises(ValueError):
+            model.generate(prompts, 3)
+        with pytest.raises(ValueError):
+            model.prefill(prompts)
