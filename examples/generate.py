@@ -118,6 +118,8 @@ class Decoder:
         longest = max(len(p) for p in prompts) + steps
         if len(prompts) != self.batch or longest > self.longest:
             raise ValueError(f"{self.batch} prompts that end within {self.longest} tokens are wanted")
+        if steps < 1:
+            raise ValueError("at least one token follows a prompt")
         logits = self.prefill(prompts)
         ws = moe.workspace(self.blocks[0].experts.dims, self.batch)
         tokens = logits.argmax(-1)

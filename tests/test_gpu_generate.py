@@ -75,3 +75,12 @@ def test_refuses_empty_prompts(ex):
             model.generate(prompts, 3)
         with pytest.raises(ValueError):
             model.prefill(prompts)
+
+
+def test_refuses_no_steps(ex):
+    """Fewer than one token cannot be returned; one is the prompts' own."""
+    model = ex.small()
+    for steps in (0, -3):
+        with pytest.raises(ValueError):
+            model.generate(ex.some_prompts(), steps)
+    assert model.generate(ex.some_prompts(), 1)[0].shape == (3, 1)
