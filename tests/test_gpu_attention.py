@@ -736,3 +736,229 @@ def test_prompt_long_contexts(m, d, heads, causal, shape):
     long_context_case(m, heads, d, [(3, 32768), (20, 65536), (1, 65700), (33, 131073), (5, 40)], causal, 5, shape)
     many = (48 * heads[0] // heads[1], 48)                       # two row tiles to an item
     long_context_case(m, many, d, [(300, 32900), (301, 70001)], causal, 6, shape, sel=(0, 150, 299))
+
+
+# ------------------------------------------------------------------------------------ forms chosen by size
+RAGGED = [(0, 0), (1, 1), (37, 37), (5, 133), (40, 7), (33, 161), (3, 0), (64, 64), (130, 129), (0, 3), (17, 90)]
+
+
+def two_row_tiles(m, heads, lens):
+    """Enough rows for two row tiles to a CTA: at least two such items per SM."""
+    hq, hkv = heads
+    rows = 2 * (128 // (hq // hkv))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return sum(x for x, _ in lens) // rows * hkv >= 2 * sms
+
+
+def some_heads_case(m, heads, d, lens, causal, seed, gain=2.0):
+    """The first and last head of the first and last group against 64 bits; all rows, all columns."""
+    hq, hkv = heads
+    g, tq, tk = hq // hkv, sum(x for x, _ in lens), sum(x for _, x in lens)
+    q, k, v = rand(seed, tq, hq, d, gain=gain), rand(seed + 1, tk, hkv, d), rand(seed + 2, tk, hkv, d)
+    o, lse = run_prefill(m, m.AttnDims(hq, hkv, d), *(x.view(torch.int16).cuda() for x in (q, k, v)), lens, causal)
+    assert torch.isfinite(o.view(torch.bfloat16)).all()
+    for h in (0, hkv - 1):
+        sel = sorted({h * g, h * g + g - 1})
+        ref = C.prefill(q[:, sel].double(), k[:, h:h + 1].double(), v[:, h:h + 1].double(), lens, 1 / math.sqrt(d), causal)
+        C.check(o[:, sel], lse[:, sel], ref, 8, f"{heads} {d} causal={causal} heads {sel}")
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "both"])
+@pytest.mark.parametrize("heads,times", [((64, 8), 4), ((56, 8), 5), ((48, 16), 5)], ids=["8", "7", "3"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_two_row_tiles_ragged(m, d, heads, times, causal):
+    """Many short sequences with two row tiles to an item: rows that see nothing, tiles without a position,
+    groups that do not divide 128."""
+    lens = RAGGED * times
+    assert two_row_tiles(m, heads, lens)
+    some_heads_case(m, heads, d, lens, causal, seed=60)
+
+
+@pytest.mark.parametrize("heads,lens,causal", [
+    ((64, 8), [(1300, 1300)], True), ((64, 8), [(1251, 1400)], False), ((56, 8), [(1411, 1500)], True),
+    ((48, 16), [(1601, 1500)], True), ((48, 16), [(1650, 70)], False), ((64, 8), [(1300, 128), (33, 256)], False)],
+    ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_two_row_tiles_long(m, d, heads, lens, causal):
+    assert two_row_tiles(m, heads, lens)
+    some_heads_case(m, heads, d, lens, causal, seed=70, gain=4.0)
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "both"])
+@pytest.mark.parametrize("d", [64, 256])
+def test_prompt_thousands_of_sequences(m, d, causal):
+    prompt_case(m, (2, 1), d, [((i * 5) % 4, (i * 7) % 9) for i in range(4096)], causal, seed=80)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_token_thousands_of_sequences(m, fp8):
+    """All 128 groups of 32 sequences, some of them empty, long sequences among the short ones."""
+    lens = [0 if 640 <= i < 704 or i % 7 == 3 else 3000 if i % 1500 == 9 else i % 23 for i in range(4096)]
+    decode_case(m, (2, 1), 64, lens, 16, fp8, seed=90)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("heads", [(64, 1), (12, 1), (40, 2)], ids=str)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_token_many_heads_long(m, d, heads, fp8):
+    """More than 8 and more than 16 query heads to a cache head, cut over warps and SMs."""
+    decode_case(m, heads, d, [1501, 3, 260], 16, fp8, seed=95)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_odd_strides(m, d):
+    """A token stride that is no multiple of the head stride."""
+    hq, hkv, n = 4, 2, 130
+    q, k, v = rand(1, n, hq, d), rand(2, n, hkv, d), rand(3, n, hkv, d)
+    dev = []
+    for x in (q, k, v):
+        h = x.shape[1]
+        buf = torch.full((n * (h * (d + 8) + 40),), 0x7FC0, dtype=torch.int16, device="cuda")
+        dev.append(buf.as_strided((n, h, d), (h * (d + 8) + 40, d + 8, 1)))
+        dev[-1].copy_(x.view(torch.int16).cuda())
+    o, lse = run_prefill(m, m.AttnDims(hq, hkv, d), *dev, [(n, n)], True)
+    C.check(o, lse, C.prefill(q.double(), k.double(), v.double(), [(n, n)], 1 / math.sqrt(d), True), 8)
+
+
+# ------------------------------------------------------------------------------------ bad device data
+def guarded(shape, dtype, fill):
+    """A tensor of `fill` inside a buffer of the same value, 4096 elements on either side; and a check of these."""
+    n = math.prod(shape)
+    buf = torch.full((n + 8192,), fill, dtype=dtype, device="cuda")
+
+    def untouched():
+        return bool((buf[:4096] == fill).all() and (buf[-4096:] == fill).all())
+    return buf[4096:-4096].view(shape), untouched
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cq,ck,good", [
+    ([0, 30, 20, 40], [0, 30, 30, 40], []), ([0, 10, 20, 400], [0, 10, 20, 40], [0, 1]),
+    ([0, 10, 20, 40], [0, 10, 20, 1000000], [0, 1]), ([0, 10, 20, 40], [0, 10, 1 << 30, 40], [0]),
+    ([0, 10, 20, 1 << 30], [0, 10, 20, 40], [0, 1]), ([0, 10, 20, 40], [0, -1000000, 20, 40], [2])])
+def test_prompt_bad_offsets_margins(m, d, cq, ck, good):
+    """Bad offsets write nothing outside o and lse, and leave the sequences beside them right."""
+    dims = m.AttnDims(4, 2, d)
+    x = rand(1, 40, 8, d)
+    dev, ws = x.view(torch.int16).cuda(), m.attn_workspace(dims)
+    o, o_ok = guarded((40, 4, d), torch.int16, 0x1234)
+    lse, lse_ok = guarded((40, 4), torch.float32, 7.25)
+    m.attn_prefill(dims, dev[:, :4], dev[:, 4:6], dev[:, 6:], ints(cq), ints(ck), ws, o=o, lse=lse)
+    assert status(m, ws) == 9
+    assert o_ok() and lse_ok()
+    for b in good:
+        (a, z), (s, e) = cq[b:b + 2], ck[b:b + 2]
+        z = min(z, 40)
+        ref = C.prefill(x[a:z, :4].double(), x[s:e, 4:6].double(), x[s:e, 6:].double(), [(z - a, e - s)], 1 / math.sqrt(d), True)
+        C.check(o[a:z], lse[a:z], ref, 8, f"sequence {b}")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_token_bad_pages_and_lengths_margins(m, fp8):
+    """Bad pages and lengths write nothing outside o and lse, and leave the other sequences right."""
+    dims, lens = m.AttnDims(4, 2, 64), [100, 90, 1000]
+    cache, table, vals = make_cache(m, dims, lens, 16, fp8)
+    q = rand(1, 3, 4, 64)
+    ref = decode_ref(q, vals, 1 / 8)
+    for page, n in ((-1, 90), (1 << 30, 90), (cache.k.shape[0], 90), (None, -1), (None, 1 << 30), (None, 63 * 16 + 1)):
+        t, ws = table.clone(), m.attn_workspace(dims)
+        if page is not None:
+            t[1, 3] = page
+        o, o_ok = guarded((3, 4, 64), torch.int16, 0x1234)
+        lse, lse_ok = guarded((3, 4), torch.float32, 7.25)
+        m.attn_decode(cache, q.view(torch.int16).cuda(), ints([100, n, 1000]), t, ws, o=o, lse=lse)
+        assert status(m, ws) == 9, (page, n)
+        assert o_ok() and lse_ok()
+        C.check(o[::2], lse[::2], [x[::2] for x in ref], 11 if fp8 else 8, f"{page} {n}")
+
+
+# ------------------------------------------------------------------------------------ seen infinities, ends of ranges
+@pytest.mark.parametrize("heads,n", [((4, 2), 700), ((64, 8), 1300)], ids=str)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_infinite_values_seen(m, d, heads, n):
+    """Rows that see an infinite value have it in their output, in that column only."""
+    hq, hkv = heads
+    q, k, v = rand(1, n, hq, d, gain=0.5), rand(2, n, hkv, d), rand(3, n, hkv, d)
+    where = {0: n - 3, 5: 0, 6: n // 2, d - 1: n - 140}                # column -> key
+    vb = v.clone()
+    for i, (c, key) in enumerate(where.items()):
+        vb[key, :, c], v[key, :, c] = math.inf if i % 2 == 0 else -math.inf, 0.0
+    o, lse = run_prefill(m, m.AttnDims(hq, hkv, d), *(x.view(torch.int16).cuda() for x in (q, k, vb)), [(n, n)], True)
+    sel, g = [0, hq - 1], hq // hkv
+    for h in sel:
+        ref = C.prefill(q[:, h:h + 1].double(), k[:, h // g:h // g + 1].double(), v[:, h // g:h // g + 1].double(), [(n, n)],
+                        1 / math.sqrt(d), True)
+        got = C.values(o[:, h:h + 1])
+        for i, (c, key) in enumerate(where.items()):
+            assert (got[key:, :, c] == (math.inf if i % 2 == 0 else -math.inf)).all(), (h, c)
+            got[key:, :, c] = ref[0][key:, :, c]
+        C.check(got.to(torch.bfloat16).view(torch.int16), lse[:, h:h + 1], ref, 8, f"{heads} {d} head {h}")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_infinite_keys_seen(m, d):
+    """A key whose score is minus infinity has no weight, in a prompt and in the cache."""
+    n, at = 300, [0, 17, 255, 299]
+    q, k, v = rand(1, n, 2, d, gain=0.5), rand(2, n, 1, d), rand(3, n, 1, d)
+    q[:, :, 3] = -1.0
+    rest = torch.tensor([i for i in range(n) if i not in at])
+    k[at, 0, 3] = math.inf
+    o, lse = run_prefill(m, m.AttnDims(2, 1, d), *(x.view(torch.int16).cuda() for x in (q, k, v)), [(n, n)], False)
+    ref = C.prefill(q.double(), k[rest].double(), v[rest].double(), [(n, len(rest))], 1 / math.sqrt(d), False)
+    C.check(o, lse, ref, 8)
+    cache, ws = m.KvCache.empty(m.AttnDims(2, 1, d), 20, 16), m.attn_workspace(m.AttnDims(2, 1, d))
+    table = torch.arange(19, dtype=torch.int32, device="cuda")[None].contiguous()
+    m.kv_append(cache, k.view(torch.int16).cuda(), v.view(torch.int16).cuda(), cu([n]), ints([0]), table, ws)
+    o, lse = run_decode(m, cache, q[:1].view(torch.int16).cuda(), [n], table, ws)
+    C.check(o, lse, [x[:1] for x in ref], 8)
+
+
+@pytest.mark.parametrize("heads", [(1024, 16), (1024, 1024), (1023, 1023)], ids=str)
+@pytest.mark.parametrize("d", [64, 256])
+def test_most_heads(m, d, heads):
+    """As many heads as are accepted: a prompt, its append, and one token; the first, a middle and the last group."""
+    (hq, hkv), n, page = heads, 35, 16
+    g, dims = hq // hkv, m.AttnDims(hq, hkv, d)
+    q, k, v = rand(1, n, hq, d), rand(2, n, hkv, d), rand(3, n, hkv, d)
+    dev = [x.view(torch.int16).cuda() for x in (q, k, v)]
+    o, lse = run_prefill(m, dims, *dev, [(n, n)], True)
+    cache, ws, table = m.KvCache.empty(dims, 4, page), m.attn_workspace(dims), ints([[2, 0, 3]])
+    m.kv_append(cache, dev[1], dev[2], cu([n]), ints([0]), table, ws)
+    o1, lse1 = run_decode(m, cache, dev[0][-1:].contiguous(), [n], table, ws)
+    for h in (0, hkv // 2, hkv - 1):
+        sel = sorted({h * g, h * g + g - 1})
+        ref = C.prefill(q[:, sel].double(), k[:, h:h + 1].double(), v[:, h:h + 1].double(), [(n, n)], 1 / math.sqrt(d), True)
+        C.check(o[:, sel], lse[:, sel], ref, 8, f"prompt {h}")
+        C.check(o1[:, sel], lse1[:, sel], [x[-1:] for x in ref], 8, f"token {h}")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_largest_pages(m, fp8):
+    """Pages of 65536 rows, a length that fills the table."""
+    dims, page, n = m.AttnDims(2, 1, 64), 65536, 131072
+    s = torch.tensor([0.02], device="cuda") if fp8 else None
+    cache, ws = m.KvCache.empty(dims, 3, page, s, s), m.attn_workspace(dims)
+    k, v, q = rand(1, n, 1, 64), rand(2, n, 1, 64), rand(3, 1, 2, 64)
+    table = ints([[2, 0]])
+    m.kv_append(cache, k.view(torch.int16).cuda(), v.view(torch.int16).cuda(), cu([n]), ints([0]), table, ws)
+    o, lse = run_decode(m, cache, q.view(torch.int16).cuda(), [n], table, ws)
+    if fp8:
+        k, v = (e4m3(x, 0.02).float().double() * float(s[0]) for x in (k, v))
+    C.check(o, lse, decode_ref(q, [[k.double().transpose(0, 1), v.double().transpose(0, 1)]], 1 / 8), 11 if fp8 else 8)
+
+
+@pytest.mark.parametrize("heads,tokens,d", [((16, 2), 20, 64), ((16, 2), 20, 128), ((16, 2), 20, 256), ((64, 8), 1300, 128)],
+                         ids=str)
+def test_prompt_long_same_bits(m, heads, tokens, d):
+    """Sums put aside along a long context: the same bits from call to call."""
+    (hq, hkv), n = heads, 140_000
+    g = torch.Generator(device="cuda").manual_seed(7)
+    q, k, v = ((torch.randn(r, h, d, generator=g, device="cuda")).to(torch.bfloat16).view(torch.int16)
+               for r, h in ((tokens + 3, hq), (n + 90, hkv), (n + 90, hkv)))
+    dims, cq, ck = m.AttnDims(hq, hkv, d), cu([tokens, 3]), cu([n, 90])
+    ws, first = m.attn_workspace(dims), None
+    for _ in range(5):
+        lse = torch.empty(tokens + 3, hq, device="cuda")
+        got = m.attn_prefill(dims, q, k, v, cq, ck, ws, lse=lse), lse
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
