@@ -409,6 +409,9 @@ MOE_API int moe_selftest_wait_timeout(void* ws, size_t ws_bytes, moe_stream_t st
  *   - Activations are bf16. Scores, softmax statistics and the accumulated output are fp32. The
  *     softmax weights are rounded once, to the other operand's 16-bit type (bf16; fp16 when the
  *     cache is e4m3), for the product with v; o is rounded once to bf16. lse is natural-log, fp32.
+ *     The tensor cores round their fp32 sums towards zero, so that sums of one sign lose about 2^-23
+ *     per 16 keys; the prompt call sums at most 32768 keys so (0.03%), the one-token call the rows
+ *     of one run (0.4% at 441505 rows, a cache of 137 GB; none seen at 110000).
  *   - Supported: head_dim 64, 128 or 256; n_kv_heads divides n_q_heads; at most 64 query heads per
  *     key-value head and 1024 query heads; 1 <= n_seqs <= 4096; page_size 1..65536
  *     (MOE_ERR_UNSUPPORTED_SHAPE otherwise).
@@ -489,6 +492,7 @@ MOE_API int moe_kv_append(const moe_kv_cache* cache, moe_heads_view k, moe_heads
  * lens counts it; 0 gives an empty row). The work of all sequences is cut into equal runs of cache
  * rows, one per SM, so that a batch of uneven lengths and one long sequence alike fill the GPU;
  * cut sequences are joined in a fixed order (the result of a call does not vary from run to run).
+ * Each cache row is read once per 16 query heads of its key-value head.
  * o: bf16 [n_seqs, n_q_heads, head_dim], not overlapping q; lse: fp32 [n_seqs, n_q_heads] or NULL.
  * n_seqs * n_kv_heads * ceil(heads per key-value head / 16) * (table_width * page_size / 16 + 8) must
  * be below 2^31 (MOE_ERR_UNSUPPORTED_SHAPE).

@@ -1,7 +1,8 @@
 // moe_attn_decode: attention of one new token per sequence over the paged cache.
 //
-// Every cache row is read once and used by the G query heads of its key-value head: G flops per byte
-// in bf16, so HBM bounds it. Two things make it run at that rate:
+// Every cache row is read once per 16 query heads of its key-value head (once for groups of up to 16, four times for
+// 64) and used by all of these: up to 16 flops per byte in bf16, so HBM bounds it for groups of up to 8. Two things
+// make it run at that rate:
 //
 //  * Equal work. All sequences' caches are cut into tiles of TR rows (of one head each), and the
 //    tiles, in the order (sequence, head, position), into equal runs, one per warp of a grid of one CTA
@@ -18,14 +19,17 @@
 // The products run on mma.sync with the cache as the 16-row operand and the heads as the 8 columns: S^T =
 // K Q^T (16 keys x 8 heads), O^T = V^T P^T (16 values x 8 heads), P^T turned by movmatrix. A group of up
 // to 8 heads thus wastes no rows; up to 16 heads take two column blocks over the same fragments of K
-// and V. In e4m3 the codes become fp16 (exactly), the query row fp16 times a power of two, and the
+// and V, with twice the registers for q and O (heads of 256: four warps, spills of 58 bytes in bf16, 300 in
+// e4m3). In e4m3 the codes become fp16 (exactly), the query row fp16 times a power of two, and the
 // softmax weights fp16; in bf16 all operands are bf16.
 //
 // Measured (GB300): long batches add cache rows at the copy rate of HBM (75 sequences of 8300 rows, 2 heads of
 // 128, bf16: 102 us, 6.2 TB/s, 92% of it); a call has 14 us beside that (18 in e4m3 at heads of 256): launch, three
 // dependent loads before the first rows, SMs that end up to 5 us apart, the two joins. So 64 sequences of up to
-// 16384 rows take 66 us (5.6 TB/s), one of 131071 rows 31 us (4.4 TB/s), 129 e4m3 sequences of up to 8191 rows of
-// 256 75 us (4.6 TB/s), one of 511 rows 8.4 us.
+// 16384 rows take 66 us (5.6 TB/s), one of 131071 rows 30 us (4.4 TB/s), 129 e4m3 sequences of up to 8191 rows of
+// 256 75 us (4.6 TB/s), one of 511 rows 8.6 us. 32 sequences of up to 16384 rows of one head of 128 for 8, 16 and 64
+// query heads: bf16 24, 29 and 74 us (floor 13.5), e4m3 19, 26 and 59 us (6.8); of 256: bf16 41, 72 and 224 us (27),
+// e4m3 29, 52 and 134 us (13.5).
 #include <cuda_fp8.h>
 
 #include "attn_device.cuh"

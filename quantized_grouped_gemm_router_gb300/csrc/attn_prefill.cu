@@ -26,13 +26,17 @@
 //    some row does not see whole, and a tile with such a value is multiplied by the softmax warps,
 //    seen keys only (rare, and bounded by one tile's work).
 //  * K and V tiles are one ring, filled by TMA in the order in which the MMA warps free them.
+//  * Long contexts. Every 32768 keys of a stream O, l and m are put aside (Softmax::put_aside), so that what the
+//    tensor cores' sums lose does not add up.
 //
 // Bound by the chain S -> softmax -> P V of the two streams: at D = 128 a step takes about 1500 cycles, 1170 of
-// them the tensor cores' own. Measured (GB300): 16384 tokens, 16/2 heads of 128, causal: 0.73 ms, 1.50 PFLOP/s (79%
-// of a cuBLAS bf16 GEMM's burst rate); 1021 tokens on 8192, heads of 256: 0.123 ms, 1.18 PFLOP/s (62%),
+// them the tensor cores' own. Measured (GB300): 16384 tokens, 16/2 heads of 128, causal: 0.73 to 0.75 ms, 1.47 to 1.51
+// PFLOP/s (77 to 80% of a cuBLAS bf16 GEMM's burst rate); 1021 tokens on 8192, heads of 256: 0.123 ms, 1.18 PFLOP/s (62%),
 // bound by the MMAs of 64-key tiles: one of 64 columns takes 67 cycles, as one of 128 does (one of 256 takes 129),
 // so that 64 keys take 1600. Short sequences: an item costs 3 to 4 us beside its steps (start,
-// check, the last product, the output): 24 texts of 250 tokens, 8 heads of 64, both ways: 27 us.
+// check, the last product, the output): 24 texts of 250 tokens, 8 heads of 64, both ways: 27 us. Many
+// sequences: an item is found by a search over the sequences from the first on, 32 at a step: 1024 sequences of 16
+// tokens take 142 us, 4096 of 2 tokens 1.41 ms.
 #include "attn_device.cuh"
 #include "attn_ptx.cuh"
 

@@ -5,7 +5,7 @@
 // rows of a decode step. A thread moves one or two 8-value pieces of a token's k and the same pieces of
 // its v: their loads are in flight while it looks the token's sequence and page up, with 32-bit divisions
 // by multiplication (64-bit ones took two thirds of the issue slots: 13.9 us for 8192 tokens of 8 heads
-// of 128, against 12.2 now, 5.5 TB/s).
+// of 128, against 12.2 now, 5.5 TB/s; as e4m3, with an IEEE division per value, 14.4 us, 3.5 TB/s).
 #include <cuda_fp8.h>
 
 #include "attn_device.cuh"
