@@ -408,7 +408,8 @@ MOE_API int moe_selftest_wait_timeout(void* ws, size_t ws_bytes, moe_stream_t st
  * The conventions at the top of this file hold, with these additions:
  *   - Activations are bf16. Scores, softmax statistics and the accumulated output are fp32. The
  *     softmax weights are rounded once, to the other operand's 16-bit type (bf16; fp16 when the
- *     cache is e4m3), for the product with v; o is rounded once to bf16. lse is natural-log, fp32.
+ *     cache is e4m3: 11 bits down to 2^-21 of the row's largest weight, within 2^-32 of it below),
+ *     for the product with v; o is rounded once to bf16. lse is natural-log, fp32.
  *     The tensor cores round their fp32 sums towards zero, so that sums of one sign lose about 2^-23
  *     per 16 keys; the prompt call sums at most 32768 keys so (0.03%), the one-token call the rows
  *     of one run (0.4% at 441505 rows, a cache of 137 GB; none seen at 110000).
