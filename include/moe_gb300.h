@@ -85,7 +85,8 @@ enum moe_status {
                                      2^-14 in magnitude or with 15*|scale| + |bias| > 65504  */
   MOE_ERR_BAD_INDEX = 9           /* device (attention calls): offsets that do not ascend from 0 to
                                      the row count, a length or position outside the page table,
-                                     or a page number outside the cache                       */
+                                     or a page number outside the cache; (8-bit expert calls) an
+                                     expert id, an offset, a place or a row count out of range */
 };
 
 /* Layer dimensions. `group` is the quantization group along the input dimension (64). */
@@ -501,6 +502,139 @@ MOE_API int moe_kv_append(const moe_kv_cache* cache, moe_heads_view k, moe_heads
 MOE_API int moe_attn_decode(const moe_kv_cache* cache, moe_heads_view q, const int32_t* lens,
                             const int32_t* page_table, int32_t table_width, int32_t n_seqs, float scale, uint16_t* o,
                             float* lse, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Experts in 8 bits, in single steps: tokens sorted by expert and brought back, the grouped matrix
+ * product between, and the activation, each with its gradient. They stand beside the fused Q4 calls
+ * above for experts kept as e4m3 with a scale for each block of 128, for routers of one's own, and
+ * for training a router or the layers below through experts that are not trained themselves.
+ *
+ * A layer of them, and its gradients (K = top_k; x, y, dy: T rows; the rest: T K sorted rows):
+ *   moe_sort_tokens(ids) -> offsets, inv            (or moe_route's offsets and inv_perm)
+ *   xs  = moe_dispatch(x)                           e4m3
+ *   gu  = moe_gemm_e4m3(xs, w_gate_up)              bf16 [.., 2 I], gate then up
+ *   h   = moe_swiglu(gu)                            e4m3 [.., I]
+ *   ys  = moe_gemm_e4m3(h, w_down)                  bf16
+ *   y   = moe_combine(ys, weights)
+ *   dys, dweights = moe_combine_grad(dy, ys)        dys e4m3
+ *   dh  = moe_gemm_e4m3(dys, w_down, transposed)    bf16
+ *   dgu = moe_swiglu_grad(gu, dh)                   e4m3
+ *   dxs = moe_gemm_e4m3(dgu, w_gate_up, transposed) bf16
+ *   dx  = moe_combine(dxs) without weights: the gradient of moe_dispatch
+ *
+ * The conventions at the top of this file hold, with these additions:
+ *   - e4m3 rows carry one fp32 scale per 128 columns (the last block of a row may be shorter): a code
+ *     c stands for scale * c. Quantising a block takes a = its largest finite magnitude, at least
+ *     2^-100; scale = a / 448, code = x * (448 / a) rounded to nearest even; a value that is not
+ *     finite becomes NaN (0x7F) and leaves the others of its block as they are.
+ *   - Sums are fp32. Outputs are rounded once, to bf16 or, from the fp32 values, to e4m3.
+ *   - Rows that no assignment names, and rows from offsets[n_experts] (or `total`) on, are left as
+ *     they were.
+ *   - Supported: 1 <= n_experts <= 1024, 1 <= top_k <= 16, columns (d, n, k, inter) multiples of 16,
+ *     16 to 65536; fewer than 2^26 rows, tokens and assignments (MOE_ERR_UNSUPPORTED_SHAPE). No rows
+ *     are no work.
+ *   - int32 and float arrays need 4-byte alignment, rows 16 bytes, `ws` 128. Outputs do not overlap
+ *     inputs.
+ *   - Ids, offsets and places are device data. A kernel never follows a bad one out of the buffers it
+ *     was given: it skips or clamps it and raises MOE_ERR_BAD_INDEX in `ws`; the rows concerned are
+ *     undefined.
+ *   - `ws`: moe_expert_workspace_bytes(n_experts) bytes, zero-filled once before the first call; the
+ *     rules of moe_workspace_bytes hold. It does not grow with the number of rows. Results do not
+ *     vary from run to run.
+ */
+
+/* Rows of a matrix inside any buffer: value (r, c) at p[r * stride + c] (strides in values). bf16:
+ * stride a multiple of 8. e4m3: stride a multiple of 16, the scale of columns 128 b .. 128 b + 127
+ * of row r at scale[r * scale_stride + b]. Strides hold a row and are below 2^38
+ * (MOE_ERR_INVALID_ARG otherwise). */
+#define MOE_ROWS_BF16 0
+#define MOE_ROWS_E4M3 1
+typedef struct moe_rows {
+  int32_t format;
+  void* p;
+  int64_t stride;
+  float* scale;
+  int64_t scale_stride;
+} moe_rows;
+
+/* 0 for an unsupported number of experts. */
+MOE_API size_t moe_expert_workspace_bytes(int32_t n_experts);
+
+/*
+ * Sorts assignments by expert, stably: ids int32[n] (a token's top_k entries one after the other) in
+ * 0 .. n_experts - 1, or negative for none. offsets int32[n_experts + 1]: where each expert's rows
+ * begin, then their number; inv int32[n]: assignment -> place, -1 for none; perm int32[n]: place ->
+ * assignment, -1 from offsets[n_experts] on. An id of n_experts or more counts as none
+ * (MOE_ERR_BAD_INDEX).
+ */
+MOE_API int moe_sort_tokens(const int32_t* ids, int32_t n, int32_t n_experts, int32_t* offsets, int32_t* perm,
+                            int32_t* inv, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Lays token rows out by place: out[inv[t * top_k + j]] = x[t] for every j with a place (inv >= 0).
+ * x: bf16, T rows of d; out: bf16 or e4m3, out_rows rows. inv == NULL (top_k 1): row t goes to row t,
+ * which is how rows are quantised. Each x row is read, and quantised, once. Its gradient is
+ * moe_combine without weights.
+ */
+MOE_API int moe_dispatch(const moe_rows* x, const int32_t* inv, int32_t T, int32_t top_k, int32_t d,
+                         const moe_rows* out, int32_t out_rows, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * y[t] = add[t] + sum_j w[t * top_k + j] * ys[inv[t * top_k + j]], over the j with a place, in the order of j.
+ * ys: bf16, ys_rows rows of d; w: fp32, NULL for ones; add: bf16 or NULL (the shared expert's rows,
+ * or the residual); y: bf16, T rows; y may be add itself. A token without places gives add[t], or 0.
+ */
+MOE_API int moe_combine(const moe_rows* ys, int32_t ys_rows, const int32_t* inv, const float* w, int32_t T,
+                        int32_t top_k, int32_t d, const moe_rows* add, const moe_rows* y, void* ws, size_t ws_bytes,
+                        moe_stream_t stream);
+
+/*
+ * Gradients of moe_combine (that of add is dy): for p = inv[t * top_k + j] with a place,
+ * dys[p] = w[t * top_k + j] * dy[t] and dw[t * top_k + j] = dy[t] . ys[p]; dw is 0 without one.
+ * dy, ys: bf16; dys: bf16 or e4m3, ys_rows rows; w, dw: fp32 [T, top_k].
+ */
+MOE_API int moe_combine_grad(const moe_rows* dy, const moe_rows* ys, int32_t ys_rows, const int32_t* inv,
+                             const float* w, int32_t T, int32_t top_k, int32_t d, const moe_rows* dys, float* dw,
+                             void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Expert matrices W[e] of n rows (outputs) and k columns (inputs) in e4m3: codes [n_experts, n, k],
+ * contiguous, 16-byte aligned; fp32 scales [n_experts, ceil(n / 128), ceil(k / 128)], contiguous:
+ * a code c at (i, j) stands for scale[e, i / 128, j / 128] * c. */
+typedef struct moe_e4m3_weights {
+  const uint8_t* q;
+  const float* scale;
+  int32_t n_experts, n, k;
+} moe_e4m3_weights;
+
+/* Quantises bf16 matrices [n_experts, n, k], contiguous, into codes and scales of that layout, by
+ * blocks of 128 x 128 with the rule above. */
+MOE_API int moe_quant_weights(const uint16_t* w, int32_t n_experts, int32_t n, int32_t k, uint8_t* q, float* scale,
+                              moe_stream_t stream);
+
+/*
+ * Products of e4m3 rows with their experts' matrices. Rows offsets[e] .. offsets[e + 1] - 1 of a
+ * belong to expert e (device int32[n_experts + 1], ascending, at most `rows`; NULL: all rows belong to
+ * the one expert, n_experts == 1). transposed == 0: out[p] = W[e] a[p] (a: k columns, out: n);
+ * transposed != 0: out[p] = W[e]^T a[p] (a: n columns, out: k), the gradient of the former's
+ * inputs on the same codes. out: bf16.
+ * The codes' products are summed in fp32 within a block of 128; each block's sum is multiplied by its
+ * two scales and added in fp32.
+ */
+MOE_API int moe_gemm_e4m3(const moe_rows* a, int32_t rows, const moe_e4m3_weights* w, const int32_t* offsets,
+                          int32_t transposed, const moe_rows* out, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * h = silu(g) * u for rows gu = g | u of 2 * inter columns (bf16): h of inter columns, bf16 or e4m3.
+ * total: device int32, the number of rows that count (offsets + n_experts, say), NULL for all `rows`.
+ */
+MOE_API int moe_swiglu(const moe_rows* gu, int32_t rows, int32_t inter, const int32_t* total, const moe_rows* h,
+                       void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Its gradient: with s = 1 / (1 + exp(-g)), dgu = (dh u s (1 + g (1 - s))) | (dh g s), 2 * inter
+ * columns, bf16 or e4m3, from gu and dh (bf16, inter columns). */
+MOE_API int moe_swiglu_grad(const moe_rows* gu, const moe_rows* dh, int32_t rows, int32_t inter,
+                            const int32_t* total, const moe_rows* dgu, void* ws, size_t ws_bytes,
+                            moe_stream_t stream);
 
 /* Synchronises `stream`, returns the sticky device status of `ws` (MOE_OK or a device error
  * code) and clears it. */

@@ -659,7 +659,7 @@ const char* moe_status_string(int status) {
     case MOE_ERR_NONFINITE: return "non-finite router logit";
     case MOE_ERR_DEVICE_TIMEOUT: return "bounded device wait gave up";
     case MOE_ERR_OUT_OF_RANGE: return "activation outside the fp16 operand range";
-    case MOE_ERR_BAD_INDEX: return "offset, length or page number outside its range";
+    case MOE_ERR_BAD_INDEX: return "index, offset, length or page number outside its range";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,344 @@
+// The row-wise 8-bit expert calls: moe_dispatch, moe_combine, moe_combine_grad, moe_swiglu and its
+// gradient, moe_quant_weights. Each reads its rows once and writes its rows once: all are bound by HBM
+// where there are many rows, by launch and one load's latency where there are few.
+//
+// A warp takes pieces of 512 columns, 16 to a lane (two 16-byte loads; 16 codes are one 16-byte store),
+// so that 8 neighbouring lanes hold a block of 128 and find its largest magnitude by three shuffles.
+#include "expert_device.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kPiece = 512;   // columns of a warp's step, 16 per lane
+
+// kWarps warps of a CTA as rows x warps per row; each warp takes every warps-th piece of its row.
+struct Split {
+  int warps, rows;
+};
+inline Split split_of(int pieces) {
+  int w = 1;
+  while (w < kWarps && 2 * w <= pieces) w *= 2;
+  return {w, kWarps / w};
+}
+
+// ------------------------------------------------------------------------------------ dispatch
+template <bool E4M3>
+__global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constant__ DispatchParams p, int warps) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * (kWarps / warps) + warp / warps;
+  if (t >= p.T) return;  // the whole warp
+  int place = -1;
+  if (lane < p.k) place = p.inv ? __ldg(p.inv + t * p.k + lane) : (int)t;
+  if (place >= p.out_rows) {
+    raise_index(p.hdr);
+    place = -1;
+  }
+  if (!__any_sync(~0u, place >= 0)) return;
+  for (int piece = warp % warps; piece < p.segments; piece += warps) {
+    const int c = piece * kPiece + lane * 16;
+    const bool mine = c < p.d;
+    uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (mine) load16(p.x, t, c, v);
+    uint4 codes;
+    float scale;
+    if (E4M3) {
+      float x[16];
+      bf16x8_to_float(v[0], x);
+      bf16x8_to_float(v[1], x + 8);
+      codes = quantise16(x, &scale);
+    }
+    for (int j = 0; j < p.k; ++j) {
+      const int row = __shfl_sync(~0u, place, j);
+      if (row >= 0 && mine) {
+        if (E4M3)
+          store_codes(p.out, row, c, codes, scale);
+        else
+          store_bf16(p.out, row, c, v[0], v[1]);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------ combine
+constexpr int kCombinePiece = 256;  // 8 columns per lane: one 16-byte load of each row
+constexpr int kTogether = 8;        // rows whose loads are in flight together
+
+__global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ CombineParams p, int warps) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * (kWarps / warps) + warp / warps;
+  if (t >= p.T) return;
+  int place = lane < p.k ? __ldg(p.inv + t * p.k + lane) : -1;
+  if (place >= p.ys_rows) {
+    raise_index(p.hdr);
+    place = -1;
+  }
+  const float weight = place < 0 ? 0.f : p.w ? __ldg(p.w + t * p.k + lane) : 1.f;
+  for (int piece = warp % warps; piece < p.segments; piece += warps) {
+    const int c = piece * kCombinePiece + lane * 8;
+    const bool mine = c < p.d;
+    float acc[8] = {};
+    if (mine && p.add.p) bf16x8_to_float(*bf16_at(p.add, t, c), acc);
+    for (int j0 = 0; j0 < p.k; j0 += kTogether) {
+      uint4 v[kTogether];
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) {
+        const int row = __shfl_sync(~0u, place, j0 + i);  // lanes from top_k on hold -1
+        v[i] = row >= 0 && mine ? __ldg(bf16_at(p.ys, row, c)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) {
+        const float w = __shfl_sync(~0u, weight, j0 + i);
+        float x[8];
+        bf16x8_to_float(v[i], x);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) acc[u] = fmaf(w, x[u], acc[u]);
+      }
+    }
+    if (mine)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y.p) + t * p.y.stride + c) = float_to_bf16x8(acc);
+  }
+}
+
+// One warp per assignment: dy's row is read by the token's top_k warps out of L1.
+template <bool E4M3>
+__global__ void __launch_bounds__(512) combine_grad_kernel(const __grid_constant__ CombineGradParams p, int tokens) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * tokens + warp / p.k;
+  if (t >= p.T) return;
+  const int64_t a = t * p.k + warp % p.k;
+  const int place = __ldg(p.inv + a);
+  if (place >= p.ys_rows && lane == 0) raise_index(p.hdr);
+  if (place < 0 || place >= p.ys_rows) {
+    if (lane == 0) p.dw[a] = 0.f;
+    return;
+  }
+  const float w = __ldg(p.w + a);
+  float dot = 0.f;
+#pragma unroll 2
+  for (int c0 = 0; c0 < p.d; c0 += kPiece) {
+    const int c = c0 + lane * 16;
+    const bool mine = c < p.d;
+    uint4 g[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, y[2] = {g[0], g[0]};
+    if (mine) {
+      load16(p.dy, t, c, g);
+      load16(p.ys, place, c, y);
+    }
+    float x[16], z[16];
+    bf16x8_to_float(g[0], x);
+    bf16x8_to_float(g[1], x + 8);
+    bf16x8_to_float(y[0], z);
+    bf16x8_to_float(y[1], z + 8);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      dot = fmaf(x[i], z[i], dot);
+      x[i] *= w;
+    }
+    if (!mine) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = 0.f;  // not 0 * w: w may be infinite
+    }
+    store16<E4M3>(p.dys, place, c, x, mine);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
+  if (lane == 0) p.dw[a] = dot;
+}
+
+// ------------------------------------------------------------------------------------ SwiGLU
+// s = 1 / (1 + e^-g): e^-g to a few units of the last place (its argument's rounding: 2^-17 at |g| of 88);
+// above 2^128 it is infinite and s is 0, as in fp32 arithmetic.
+__device__ __forceinline__ float sigmoid(float g) {
+  float e, s;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
+
+__device__ __forceinline__ int rows_that_count(const SwigluParams& p) {
+  if (!p.total) return p.rows;
+  const int n = __ldg(p.total);
+  if (n < 0 || n > p.rows) {
+    if (threadIdx.x == 0) raise_index(p.hdr);
+    return n < 0 ? 0 : p.rows;
+  }
+  return n;
+}
+
+template <bool E4M3>
+__global__ void __launch_bounds__(kThreads) swiglu_kernel(const __grid_constant__ SwigluParams p, int warps) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * (kWarps / warps) + warp / warps;
+  if (t >= rows_that_count(p)) return;
+  for (int piece = warp % warps; piece < p.segments; piece += warps) {
+    const int c = piece * kPiece + lane * 16;
+    const bool mine = c < p.inter;
+    uint4 gv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, uv[2] = {gv[0], gv[0]};
+    if (mine) {
+      load16(p.gu, t, c, gv);
+      load16(p.gu, t, p.inter + c, uv);
+    }
+    float g[16], u[16];
+    bf16x8_to_float(gv[0], g);
+    bf16x8_to_float(gv[1], g + 8);
+    bf16x8_to_float(uv[0], u);
+    bf16x8_to_float(uv[1], u + 8);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = g[i] * sigmoid(g[i]) * u[i];
+    store16<E4M3>(p.out, t, c, g, mine);
+  }
+}
+
+// dg and du of 16 columns; either may be left out.
+__device__ __forceinline__ void swiglu_grad16(const uint4 (&gv)[2], const uint4 (&uv)[2], const uint4 (&hv)[2],
+                                              float (&dg)[16], float (&du)[16]) {
+  float g[16], u[16], h[16];
+  bf16x8_to_float(gv[0], g);
+  bf16x8_to_float(gv[1], g + 8);
+  bf16x8_to_float(uv[0], u);
+  bf16x8_to_float(uv[1], u + 8);
+  bf16x8_to_float(hv[0], h);
+  bf16x8_to_float(hv[1], h + 8);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float s = sigmoid(g[i]), hs = h[i] * s;
+    dg[i] = hs * u[i] * fmaf(g[i], 1.f - s, 1.f);
+    du[i] = hs * g[i];
+  }
+}
+
+// WHOLE: inter is a multiple of 128, so that the blocks of dg and of du begin at the same columns and a
+// warp makes both from one reading. Otherwise the blocks of du straddle the two halves: the pieces run
+// over the 2 inter output columns, and what du needs of g and dh is read again (out of L2).
+template <bool E4M3, bool WHOLE>
+__global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(const __grid_constant__ SwigluParams p, int warps) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * (kWarps / warps) + warp / warps;
+  if (t >= rows_that_count(p)) return;
+  for (int piece = warp % warps; piece < p.segments; piece += warps) {
+    const int at = piece * kPiece + lane * 16;               // output column
+    const bool second = !WHOLE && at >= p.inter;             // one of du
+    const int c = second ? at - p.inter : at;
+    const bool mine = c < p.inter;
+    uint4 gv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, uv[2] = {gv[0], gv[0]}, hv[2] = {gv[0], gv[0]};
+    if (mine) {
+      load16(p.gu, t, c, gv);
+      load16(p.dh, t, c, hv);
+      if (!second) load16(p.gu, t, p.inter + c, uv);
+    }
+    float dg[16], du[16];
+    swiglu_grad16(gv, uv, hv, dg, du);
+    if (WHOLE) {
+      store16<E4M3>(p.out, t, c, dg, mine);
+      store16<E4M3>(p.out, t, p.inter + c, du, mine);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dg[i] = second ? du[i] : dg[i];
+      store16<E4M3>(p.out, t, at, dg, mine);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------ weights
+// One CTA per block of 128 x 128: 16 threads to a row, 16 rows to a pass.
+__global__ void __launch_bounds__(kThreads) quant_weights_kernel(const QuantWeightsParams p) {
+  __shared__ float s_max[kWarps];
+  const int r0 = blockIdx.y * kScaleBlock + threadIdx.x / 16, c = blockIdx.x * kScaleBlock + threadIdx.x % 16 * 8;
+  const int64_t e = blockIdx.z;
+  const uint16_t* w = p.w + (e * p.n) * p.k + c;
+  uint4 v[8];
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i;
+    v[i] = r < p.n && c < p.k ? __ldg(reinterpret_cast<const uint4*>(w + (int64_t)r * p.k)) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float x[8];
+    bf16x8_to_float(v[i], x);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float m = fabsf(x[u]);
+      a = fmaxf(a, m < INFINITY ? m : 0.f);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+  if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = a;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) a = fmaxf(a, s_max[i]);
+  const BlockScale b = block_scale(a);
+  if (threadIdx.x == 0) p.scale[(e * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = b.scale;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i;
+    if (r >= p.n || c >= p.k) continue;
+    float x[8];
+    bf16x8_to_float(v[i], x);
+    uint2 o;
+    o.x = to_e4m3x2(coded(x[0], b.inv), coded(x[1], b.inv)) | to_e4m3x2(coded(x[2], b.inv), coded(x[3], b.inv)) << 16;
+    o.y = to_e4m3x2(coded(x[4], b.inv), coded(x[5], b.inv)) | to_e4m3x2(coded(x[6], b.inv), coded(x[7], b.inv)) << 16;
+    *reinterpret_cast<uint2*>(p.q + (e * p.n + r) * p.k + c) = o;
+  }
+}
+
+unsigned grid_of(int rows, int per) { return (unsigned)((rows + per - 1) / per); }
+
+}  // namespace
+
+cudaError_t launch_dispatch(DispatchParams p, cudaStream_t s) {
+  p.segments = (p.d + kPiece - 1) / kPiece;
+  const Split sp = split_of(p.segments);
+  const dim3 grid(grid_of(p.T, sp.rows));
+  return p.out.format == MOE_ROWS_E4M3 ? launch_pdl(dispatch_kernel<true>, grid, kThreads, 0, 1, s, p, sp.warps)
+                                       : launch_pdl(dispatch_kernel<false>, grid, kThreads, 0, 1, s, p, sp.warps);
+}
+
+cudaError_t launch_combine(CombineParams p, cudaStream_t s) {
+  p.segments = (p.d + kCombinePiece - 1) / kCombinePiece;
+  const Split sp = split_of(p.segments);
+  return launch_pdl(combine_kernel, dim3(grid_of(p.T, sp.rows)), kThreads, 0, 1, s, p, sp.warps);
+}
+
+cudaError_t launch_combine_grad(const CombineGradParams& p, cudaStream_t s) {
+  const int tokens = p.k < kWarps ? kWarps / p.k : 1;
+  const dim3 grid(grid_of(p.T, tokens));
+  return p.dys.format == MOE_ROWS_E4M3
+             ? launch_pdl(combine_grad_kernel<true>, grid, 32 * p.k * tokens, 0, 1, s, p, tokens)
+             : launch_pdl(combine_grad_kernel<false>, grid, 32 * p.k * tokens, 0, 1, s, p, tokens);
+}
+
+cudaError_t launch_swiglu(SwigluParams p, bool grad, cudaStream_t s) {
+  const bool e4m3 = p.out.format == MOE_ROWS_E4M3, whole = p.inter % kScaleBlock == 0;
+  p.segments = ((grad && !whole ? 2 * p.inter : p.inter) + kPiece - 1) / kPiece;
+  const Split sp = split_of(p.segments);
+  const dim3 grid(grid_of(p.rows, sp.rows));
+  if (!grad)
+    return e4m3 ? launch_pdl(swiglu_kernel<true>, grid, kThreads, 0, 1, s, p, sp.warps)
+                : launch_pdl(swiglu_kernel<false>, grid, kThreads, 0, 1, s, p, sp.warps);
+  if (whole)
+    return e4m3 ? launch_pdl(swiglu_grad_kernel<true, true>, grid, kThreads, 0, 1, s, p, sp.warps)
+                : launch_pdl(swiglu_grad_kernel<false, true>, grid, kThreads, 0, 1, s, p, sp.warps);
+  return e4m3 ? launch_pdl(swiglu_grad_kernel<true, false>, grid, kThreads, 0, 1, s, p, sp.warps)
+              : launch_pdl(swiglu_grad_kernel<false, false>, grid, kThreads, 0, 1, s, p, sp.warps);
+}
+
+cudaError_t launch_quant_weights(const QuantWeightsParams& p, int n_experts, cudaStream_t s) {
+  const dim3 grid((p.k + kScaleBlock - 1) / kScaleBlock, (p.n + kScaleBlock - 1) / kScaleBlock, n_experts);
+  quant_weights_kernel<<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace moe
