@@ -1,104 +1,360 @@
-// moe_gemm_e4m3: products of e4m3 rows with their experts' e4m3 matrices, a scale for each block of 128.
+// moe_gemm_e4m3 on the 5th-generation tensor cores: e4m3 rows times their experts' e4m3 matrices, a scale
+// for each block of 128.
 //
-// The simplest form: a CTA makes 64 rows x 64 columns of one expert's output; 32 inputs at a time go
-// through shared memory as floats, each thread sums 4 x 4 values, and every 128 inputs the block's sums
-// are multiplied by their scales and added up.
-#include <cuda_fp8.h>
-
+// out[p, c] = sum_b s_a[p, b] s_w[e, c / 128, b] (sum of the 128 code products of block b). The tensor cores
+// sum a block's codes into a fresh accumulator in tensor memory; 16 warps then read it, multiply by the two
+// scales (one factor per row and warp: a row's scale times the block's) and add to fp32 sums in registers,
+// while the other accumulator takes the next block. So scales of any fp32 value cost no accuracy.
+//
+// A CTA makes 128 rows of one expert x BN columns, rows as the MMA's M: a thread owns a row, so that its
+// factor is one register. Persistent CTAs, one per SM, walk the items (expert, row tile, column tile):
+//   warp 0       copies: per block of 128 inputs the rows (32, 64 or 128 of them) and BN weight columns
+//   warp 1       MMA issue: per block four MMAs of K = 32
+//   warps 2-17   scaling and adding, then the output; warp w reads lane quadrant w % 4 and a quarter of
+//                the columns
+// Transposed weights are read as they lie: their tile has its column axis contiguous (the other "major"
+// of the MMA's B operand), so no second copy of the weights is kept.
 #include "expert_device.cuh"
+#include "attn_ptx.cuh"
 
 namespace moe {
+bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, const void* ptr, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz);
+
 namespace {
 
-constexpr int kTile = 64, kStep = 32, kThreads = 256;
+constexpr int kTileM = 128;
+constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpSum0 = 2, kSumWarps = 16;
+constexpr int kThreads = (kWarpSum0 + kSumWarps) * 32;  // 576: 112 registers a thread
+constexpr int kGroupTiles = 16;  // row tiles of an expert whose column tiles run together
 
-__device__ __forceinline__ float e4m3_float(uint8_t c) {
-  __nv_fp8_e4m3 v;
-  v.__x = c;
-  return static_cast<float>(v);
+struct ProductMaps {
+  CUtensorMap rows[3];  // boxes of 32, 64, 128 rows x 128 inputs
+  CUtensorMap w;
+};
+
+template <int BN>
+struct Layout {
+  static constexpr int kABytes = kTileM * 128, kBBytes = BN * 128, kStage = kABytes + kBBytes;
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int bar_off = kStages * kStage;
+  static constexpr int n_bars = 2 * kStages + 4;
+  static constexpr int misc_off = bar_off + n_bars * 8;
+  static constexpr int table_off = misc_off + 16;   // lo[E], hi[E], first item[E + 1]
+  static constexpr int fixed = table_off + 1024;    // and slack to align the base
+  static constexpr int most = fixed + (3 * kMaxExperts + 1) * 4;
+  static_assert(most <= 232448, "shared memory");
+};
+
+// Four MMAs of K = 32 on a block of 128 inputs under one elected lane; B_STEP: descriptor units (16 bytes)
+// from one K step of B to the next.
+template <int B_STEP>
+__device__ __forceinline__ void mma_block(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred f, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+      "add.s64 b1, %2, %4;\n\tadd.s64 b2, %2, %5;\n\tadd.s64 b3, %2, %6;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)
+      : "memory");
+}
+// kind::f8f6f4: fp32 accumulator, A and B e4m3; trans_b: B has its N axis contiguous.
+__device__ __forceinline__ uint32_t idesc_e4m3(int M, int N, bool trans_b) {
+  return (1u << 4) | (trans_b ? kIdescBMn : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads) product_kernel(const __grid_constant__ ProductParams p) {
-  __shared__ float sa[kStep][kTile + 1], sw[kStep][kTile + 1];
-  __shared__ int s_expert, s_first, s_rows;
+struct Item {
+  int expert, row0, rows, col0;
+};
+
+// The work list: per expert its rows and the number of its first item, in shared memory.
+struct Table {
+  int *lo, *hi, *first;
+  int n_experts, col_tiles, items;
+  // Row tiles of an expert in groups of kGroupTiles; in a group the column tiles one after the other, each
+  // with all row tiles, so that the CTAs at work share both the rows' and the weights' tiles in L2.
+  template <int BN>
+  __device__ __forceinline__ Item item(int i) const {
+    int a = 0, b = n_experts;  // first[a] <= i < first[b]
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if (first[mid] <= i)
+        a = mid;
+      else
+        b = mid;
+    }
+    const int rows = hi[a] - lo[a], tiles = (rows + kTileM - 1) / kTileM;
+    const int r = i - first[a], per = kGroupTiles * col_tiles, group = r / per, in = r - group * per;
+    const int n = min(kGroupTiles, tiles - group * kGroupTiles), ct = in / n, rt = group * kGroupTiles + in - ct * n;
+    return {a, lo[a] + rt * kTileM, min(kTileM, rows - rt * kTileM), ct * BN};
+  }
+};
+
+template <int BN, bool TRANS>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ ProductParams p, const __grid_constant__ ProductMaps maps) {
+  using L = Layout<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_sum[kThreads / 32];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const uint32_t bars = base + L::bar_off;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (L::kStages + s); };
+  auto acc_full = [&](int b) { return bars + 8u * (2 * L::kStages + b); };
+  auto acc_empty = [&](int b) { return bars + 8u * (2 * L::kStages + 2 + b); };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::misc_off);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::misc_off + 4);
+
+  if (tid == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), kSumWarps);
+    }
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(s_tmem), 2 * BN);
+    tmem_relinquish();
+  }
+  if (warp == kWarpCopy && lane < 4) prefetch_tmap(lane < 3 ? &maps.rows[lane] : &maps.w);
+  // Everything above touched shared and tensor memory alone; the offsets and rows are read after the
+  // predecessor has completed.
   pdl_wait();
   pdl_launch_dependents();
-  if (threadIdx.x == 0) {
-    s_rows = 0;
-    if (!p.offsets) {
-      s_expert = 0;
-      s_first = blockIdx.x * kTile;
-      s_rows = min(kTile, p.rows - s_first);
-    } else {
-      int tile = blockIdx.x, end = 0;
-      for (int e = 0; e < p.n_experts; ++e) {
-        const int lo = __ldg(p.offsets + e), hi = __ldg(p.offsets + e + 1);
-        const int b = min(max(lo, end), p.rows), n = min(max(hi, b), p.rows) - b, tiles = (n + kTile - 1) / kTile;
-        if (blockIdx.x == 0 && blockIdx.y == 0 && (lo != b || hi != b + n || (e == 0 && lo != 0))) raise_index(p.hdr);
-        end = b + n;
-        if (tile >= 0 && tile < tiles) {
-          s_expert = e;
-          s_first = b + tile * kTile;
-          s_rows = min(kTile, n - tile * kTile);
+
+  // ---------------------------------------------------------------- work list
+  Table tab;
+  tab.lo = reinterpret_cast<int*>(smem + L::table_off);
+  tab.hi = tab.lo + p.n_experts;
+  tab.first = tab.hi + p.n_experts;
+  tab.n_experts = p.n_experts;
+  tab.col_tiles = (p.outc + BN - 1) / BN;
+  {
+    constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
+    int items[kPer], sum = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid * kPer + i;
+      items[i] = 0;
+      if (e < p.n_experts) {
+        int lo = 0, hi = p.rows;
+        if (p.offsets) {
+          const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+          lo = min(max(a, 0), p.rows);
+          hi = min(max(b, lo), p.rows);
+          bad |= a != lo || b != hi;
         }
-        tile -= tiles;
-        if (tile < 0 && (blockIdx.x || blockIdx.y)) break;
+        tab.lo[e] = lo;
+        tab.hi[e] = hi;
+        items[i] = (hi - lo + kTileM - 1) / kTileM * tab.col_tiles;
+      }
+      sum += items[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    if (blockIdx.x == 0 && bad) raise_index(p.hdr);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int at = incl - sum, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += s_sum[w];
+      all += s_sum[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (tid * kPer + i < p.n_experts) tab.first[tid * kPer + i] = at;
+      at += items[i];
+    }
+    if (tid == 0) tab.first[p.n_experts] = all;
+    tab.items = all;
+    __syncthreads();
+  }
+  const uint32_t tmem = *s_tmem;
+  const int kb_n = p.in_blocks;
+
+  if (warp == kWarpCopy) {
+    // ------------------------------------------------------------ copies
+    if (lane == 0) {
+      uint32_t g = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < tab.items && ok; i += gridDim.x) {
+        const Item it = tab.item<BN>(i);
+        const int box = it.rows > 64 ? 2 : it.rows > 32 ? 1 : 0;
+        const uint32_t bytes = (32u << box) * 128u + L::kBBytes;
+        for (int kb = 0; kb < kb_n; ++kb, ++g) {
+          const int s = g % L::kStages;
+          if (!(ok = mbar_wait(empty(s), ((g / L::kStages) & 1) ^ 1, s_abort))) break;
+          const uint32_t a = base + s * L::kStage, b = a + L::kABytes;
+          mbar_arrive_expect_tx(full(s), bytes);
+          tma_load_2d(a, &maps.rows[box], kb * 128, it.row0, full(s));
+          if (TRANS) {
+#pragma unroll
+            for (int c = 0; c < BN / 128; ++c)
+              tma_load_3d(b + c * 16384, &maps.w, it.col0 + c * 128, kb * 128, it.expert, full(s));
+          } else {
+            tma_load_3d(b, &maps.w, kb * 128, it.col0, it.expert, full(s));
+          }
+        }
+      }
+      if (!ok)  // a wait gave up: the copies in flight land before the CTA ends
+        for (int s = 0; s < L::kStages && (int)g - 1 - s >= 0; ++s) {
+          const uint32_t h = g - 1 - s;
+          const long long t0 = clock64();
+          while (!mbar_try_wait(full(h % L::kStages), (h / L::kStages) & 1) && clock64() - t0 < kWaitCycles) {
+          }
+        }
+    }
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------ MMA issue
+    const uint32_t idesc = idesc_e4m3(kTileM, BN, TRANS);
+    uint32_t g = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < tab.items && ok; i += gridDim.x)
+      for (int kb = 0; kb < kb_n; ++kb, ++g) {
+        const int s = g % L::kStages, buf = g & 1;
+        // one lane waits for the copies, the others for the accumulator
+        ok = __all_sync(~0u, lane == 0 ? mbar_wait(full(s), (g / L::kStages) & 1, s_abort)
+                                       : mbar_wait(acc_empty(buf), ((g >> 1) & 1) ^ 1, s_abort));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = base + s * L::kStage, b = a + L::kABytes;
+        if (TRANS)
+          mma_block<32 * 128 / 16>(tmem + buf * BN, sw128_desc(a), sw128_mn_desc(b, 16384), idesc);
+        else
+          mma_block<2>(tmem + buf * BN, sw128_desc(a), sw128_desc(b), idesc);
+        umma_commit_elect(empty(s));
+        umma_commit_elect(acc_full(buf));
+      }
+    if (!ok && g) {  // a wait gave up: the MMAs in flight end before tensor memory is freed
+      const long long t0 = clock64();
+      while (!mbar_try_wait(empty((g - 1) % L::kStages), ((g - 1) / L::kStages) & 1) && clock64() - t0 < kWaitCycles) {
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ scaling, adding, output
+    constexpr int kCols = BN / 4;  // columns of a warp
+    const int quad = warp & 3, part = (warp - kWarpSum0) >> 2;
+    const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
+    const int w_stride = TRANS ? p.out_blocks : 1;  // from one block of inputs to the next
+    uint32_t g = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < tab.items && ok; i += gridDim.x) {
+      const Item it = tab.item<BN>(i);
+      const int r = quad * 32 + lane, col0 = it.col0 + part * kCols;
+      // rows past the tile and columns past the matrix are computed on what lies there and not stored
+      const float* sa = p.a.scale + (it.row0 + min(r, it.rows - 1)) * p.a.scale_stride;
+      const int cb = min(col0 / kScaleBlock, p.out_blocks - 1);
+      const float* sw = p.wscale + (int64_t)it.expert * p.in_blocks * p.out_blocks + (TRANS ? cb : (int64_t)cb * p.in_blocks);
+      uint64_t acc[kCols / 2];
+#pragma unroll
+      for (int c = 0; c < kCols / 2; ++c) acc[c] = 0;
+      float fa = __ldg(sa), fw = __ldg(sw);
+      for (int kb = 0; kb < kb_n; ++kb, ++g) {
+        const int buf = g & 1;
+        const float f = fa * fw;
+        if (kb + 1 < kb_n) {
+          fa = __ldg(sa + kb + 1);
+          fw = __ldg(sw + (int64_t)(kb + 1) * w_stride);
+        }
+        if (!(ok = __all_sync(~0u, mbar_wait(acc_full(buf), (g >> 1) & 1, s_abort)))) break;
+        tc_fence_after();
+        const uint64_t f2 = pack2(f, f);
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          float v[32];
+          tmem_ld32(taddr + buf * BN + c, v);
+          tmem_wait_ld32(v);
+          if (c + 32 == kCols) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty(buf));
+          }
+#pragma unroll
+          for (int x = 0; x < 16; ++x) acc[c / 2 + x] = fma2(f2, pack2(v[2 * x], v[2 * x + 1]), acc[c / 2 + x]);
+        }
+      }
+      if (ok && r < it.rows) {
+        uint16_t* o = static_cast<uint16_t*>(p.out.p) + (int64_t)(it.row0 + r) * p.out.stride + col0;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 8)
+          if (col0 + c < p.outc) {  // the columns are a multiple of 16
+            float x[8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) unpack2(acc[c / 2 + u], x[2 * u], x[2 * u + 1]);
+            *reinterpret_cast<uint4*>(o + c) = float_to_bf16x8(x);
+          }
       }
     }
   }
+
+  // ---------------------------------------------------------------- tear-down
+  tc_fence_before();
   __syncthreads();
-  if (s_rows <= 0) return;
-  const int e = s_expert, first = s_first, rows = s_rows, c0 = blockIdx.y * kTile;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const uint8_t* aq = static_cast<const uint8_t*>(p.a.p);
-  const uint8_t* wq = p.wq + (int64_t)e * p.n * p.k;
-  const int kb = (p.k + kScaleBlock - 1) / kScaleBlock;
-  const float* ws = p.wscale + (int64_t)e * p.in_blocks * p.out_blocks;
-  float acc[4][4] = {};
-  for (int b = 0; b < p.in_blocks; ++b) {
-    float part[4][4] = {};
-    for (int i0 = b * kScaleBlock; i0 < min(p.in, (b + 1) * kScaleBlock); i0 += kStep) {
-      __syncthreads();
-      for (int x = threadIdx.x; x < kTile * kStep; x += kThreads) {
-        const int r = x / kStep, i = i0 + x % kStep;
-        sa[x % kStep][r] = r < rows && i < p.in ? e4m3_float(aq[(int64_t)(first + r) * p.a.stride + i]) : 0.f;
-        const int c = p.transposed ? x % kTile : x / kStep, j = p.transposed ? x / kTile : x % kStep;
-        const bool there = c0 + c < p.outc && i0 + j < p.in;
-        sw[j][c] = !there         ? 0.f
-                   : p.transposed ? e4m3_float(wq[(int64_t)(i0 + j) * p.k + c0 + c])
-                                  : e4m3_float(wq[(int64_t)(c0 + c) * p.k + i0 + j]);
-      }
-      __syncthreads();
-      for (int j = 0; j < kStep; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) part[r][c] = fmaf(sa[j][ty * 4 + r], sw[j][tx * 4 + c], part[r][c]);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int row = ty * 4 + r, ob = (c0 + tx * 4 + c) / kScaleBlock;
-        if (row < rows && c0 + tx * 4 + c < p.outc)
-          acc[r][c] = fmaf(p.a.scale[(first + row) * p.a.scale_stride + b] * (p.transposed ? ws[b * kb + ob] : ws[ob * kb + b]),
-                           part[r][c], acc[r][c]);
-      }
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * BN);
   }
-  uint16_t* o = static_cast<uint16_t*>(p.out.p);
-  for (int r = 0; r < 4; ++r)
-    for (int c = 0; c < 4; c += 2)  // the number of columns is even
-      if (ty * 4 + r < rows && c0 + tx * 4 + c < p.outc)
-        *reinterpret_cast<uint32_t*>(o + (int64_t)(first + ty * 4 + r) * p.out.stride + c0 + tx * 4 + c) =
-            to_bf16x2(acc[r][c], acc[r][c + 1]);
+  if (tid == 0 && *s_abort) set_device_status(p.hdr, MOE_ERR_DEVICE_TIMEOUT);
+}
+
+template <int BN, bool TRANS>
+cudaError_t launch(const ProductParams& p, cudaStream_t s) {
+  using L = Layout<BN>;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(product_kernel<BN, TRANS>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::most);
+  if (attr != cudaSuccess) return attr;
+  ProductMaps maps;
+  const cuuint64_t adims[2] = {(cuuint64_t)p.in, (cuuint64_t)p.rows}, astr[1] = {(cuuint64_t)p.a.stride};
+  for (int i = 0; i < 3; ++i) {
+    const cuuint32_t box[2] = {128, 32u << i};
+    if (!encode_tiled(&maps.rows[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.a.p, adims, astr, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  const cuuint64_t wdims[3] = {(cuuint64_t)p.k, (cuuint64_t)p.n, (cuuint64_t)p.n_experts};
+  const cuuint64_t wstr[2] = {(cuuint64_t)p.k, (cuuint64_t)p.n * p.k};
+  const cuuint32_t wbox[3] = {128, TRANS ? 128u : (cuuint32_t)BN, 1};
+  if (!encode_tiled(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.wq, wdims, wstr, wbox, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = (p.rows + kTileM - 1) / kTileM + (p.n_experts < p.rows ? p.n_experts : p.rows) - 1;
+  const int64_t items = tiles * ((p.outc + BN - 1) / BN);
+  const int grid = items < sm_count() ? (int)items : sm_count();
+  return launch_pdl(product_kernel<BN, TRANS>, grid, kThreads, (size_t)(L::fixed + (3 * p.n_experts + 1) * 4), 1, s, p, maps);
 }
 
 }  // namespace
 
 cudaError_t launch_product(const ProductParams& p, cudaStream_t s) {
-  const int tiles = (p.rows + kTile - 1) / kTile;
-  const dim3 grid(p.offsets ? tiles + p.n_experts : tiles, (p.outc + kTile - 1) / kTile);
-  return launch_pdl(product_kernel, grid, kThreads, 0, 1, s, p);
+  const int64_t tiles = (p.rows + kTileM - 1) / kTileM + (p.n_experts < p.rows ? p.n_experts : p.rows) - 1;
+  const bool narrow = tiles * ((p.outc + 255) / 256) < sm_count();
+  if (narrow) return p.transposed ? launch<128, true>(p, s) : launch<128, false>(p, s);
+  return p.transposed ? launch<256, true>(p, s) : launch<256, false>(p, s);
 }
 
 }  // namespace moe
