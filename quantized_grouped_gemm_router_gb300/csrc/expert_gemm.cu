@@ -2,7 +2,7 @@
 // for each block of 128.
 //
 // out[p, c] = sum_b s_a[p, b] s_w[e, c / 128, b] (sum of the 128 code products of block b). The tensor cores
-// sum a block's codes into a fresh accumulator in tensor memory; 16 warps then read it, multiply by the two
+// sum a block's codes into a fresh accumulator in tensor memory; 8 warps then read it, multiply by the two
 // scales (one factor per row and warp: a row's scale times the block's) and add to fp32 sums in registers,
 // while the other accumulator takes the next block. So scales of any fp32 value cost no accuracy.
 //
@@ -10,8 +10,8 @@
 // factor is one register. Persistent CTAs, one per SM, walk the items (expert, row tile, column tile):
 //   warp 0       copies: per block of 128 inputs the rows (32, 64 or 128 of them) and BN weight columns
 //   warp 1       MMA issue: per block four MMAs of K = 32
-//   warps 2-17   scaling and adding, then the output; warp w reads lane quadrant w % 4 and a quarter of
-//                the columns
+//   warps 4-11   scaling and adding, then the output; warp w reads lane quadrant w % 4 and half of the
+//                columns
 // Transposed weights are read as they lie: their tile has its column axis contiguous (the other "major"
 // of the MMA's B operand), so no second copy of the weights is kept.
 #include "expert_device.cuh"
@@ -24,8 +24,11 @@ bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, con
 namespace {
 
 constexpr int kTileM = 128;
-constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpSum0 = 2, kSumWarps = 16;
-constexpr int kThreads = (kWarpSum0 + kSumWarps) * 32;  // 576: 112 registers a thread
+constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpSum0 = 4, kSumWarps = 8;
+constexpr int kThreads = (kWarpSum0 + kSumWarps) * 32;  // 384
+// Registers: 168 a thread at launch; the first four warps give up 96 each, the summing ones take 48 more:
+// 128 * 72 + 256 * 216 = 384 * 168.
+constexpr int kFewRegs = 72, kManyRegs = 216;
 constexpr int kGroupTiles = 16;  // row tiles of an expert whose column tiles run together
 
 struct ProductMaps {
@@ -75,6 +78,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
+// Four values of a run of n (zeros behind it), from the i-th on; vec: they are one aligned 16-byte load.
+__device__ __forceinline__ void load4(const float* p, int i, int n, int64_t stride, bool vec, float (&v)[4]) {
+  if (vec) {
+    const float4 x = i < n ? __ldg(reinterpret_cast<const float4*>(p + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = i + u < n ? __ldg(p + (i + u) * stride) : 0.f;
+  }
+}
+
 struct Item {
   int expert, row0, rows, col0;
 };
@@ -108,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Layout<BN>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_sum[kThreads / 32];
+  __shared__ float s_factors[kSumWarps][4][32];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -198,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *s_tmem;
   const int kb_n = p.in_blocks;
 
+  if (warp < kWarpSum0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
   if (warp == kWarpCopy) {
     // ------------------------------------------------------------ copies
     if (lane == 0) {
@@ -256,12 +272,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (!mbar_try_wait(empty((g - 1) % L::kStages), ((g - 1) / L::kStages) & 1) && clock64() - t0 < kWaitCycles) {
       }
     }
-  } else {
+  } else if (warp >= kWarpSum0) {
     // ------------------------------------------------------------ scaling, adding, output
-    constexpr int kCols = BN / 4;  // columns of a warp
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+    constexpr int kCols = BN / 2;  // columns of a warp
     const int quad = warp & 3, part = (warp - kWarpSum0) >> 2;
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
     const int w_stride = TRANS ? p.out_blocks : 1;  // from one block of inputs to the next
+    const bool vec = kb_n % 4 == 0, vec_a = vec && p.a.scale_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.a.scale) & 15) == 0;
+    const bool vec_w = !TRANS && vec && (reinterpret_cast<uintptr_t>(p.wscale) & 15) == 0;
+    float* factors = &s_factors[warp - kWarpSum0][0][lane];
     uint32_t g = 0;
     bool ok = true;
     for (int i = blockIdx.x; i < tab.items && ok; i += gridDim.x) {
@@ -274,16 +294,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t acc[kCols / 2];
 #pragma unroll
       for (int c = 0; c < kCols / 2; ++c) acc[c] = 0;
-      float fa = __ldg(sa), fw = __ldg(sw);
+      float fa[4], fw[4];
+      load4(sa, 0, kb_n, 1, vec_a, fa);
+      load4(sw, 0, kb_n, w_stride, vec_w, fw);
       for (int kb = 0; kb < kb_n; ++kb, ++g) {
-        const int buf = g & 1;
-        const float f = fa * fw;
-        if (kb + 1 < kb_n) {
-          fa = __ldg(sa + kb + 1);
-          fw = __ldg(sw + (int64_t)(kb + 1) * w_stride);
+        if ((kb & 3) == 0) {  // the factors of four blocks: each thread's own, so that no barrier is needed
+#pragma unroll
+          for (int u = 0; u < 4; ++u) factors[u * 32] = fa[u] * fw[u];
+          load4(sa, kb + 4, kb_n, 1, vec_a, fa);
+          load4(sw, kb + 4, kb_n, w_stride, vec_w, fw);
         }
+        const int buf = g & 1;
         if (!(ok = __all_sync(~0u, mbar_wait(acc_full(buf), (g >> 1) & 1, s_abort)))) break;
         tc_fence_after();
+        const float f = factors[(kb & 3) * 32];
         const uint64_t f2 = pack2(f, f);
 #pragma unroll
         for (int c = 0; c < kCols; c += 32) {
