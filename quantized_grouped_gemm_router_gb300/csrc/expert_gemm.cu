@@ -43,9 +43,13 @@ struct Layout {
   static constexpr int bar_off = kStages * kStage;
   static constexpr int n_bars = 2 * kStages + 4;
   static constexpr int misc_off = bar_off + n_bars * 8;
-  static constexpr int table_off = misc_off + 16;   // lo[E], hi[E], first item[E + 1]
-  static constexpr int fixed = table_off + 1024;    // and slack to align the base
-  static constexpr int most = fixed + (3 * kMaxExperts + 1) * 4;
+  static constexpr int out_off = (misc_off + 16 + 127) / 128 * 128;  // per summing warp: 32 rows x 32 columns of bf16
+  static constexpr int sa_off = out_off + kSumWarps * 2048;          // per summing warp: two slots of 4 scales x 32 rows
+  static constexpr int sw_off = sa_off + kSumWarps * 1024;           // and of 4 of the weights
+  static constexpr int sum_off = sw_off + kSumWarps * 32;            // the work list's partial sums
+  static constexpr int table_off = sum_off + 64;                     // first item of every expert, and their number
+  static constexpr int fixed = table_off + 1024;                     // and slack to align the base
+  static constexpr int most = fixed + (kMaxExperts + 1) * 4;
   static_assert(most <= 232448, "shared memory");
 };
 
@@ -78,51 +82,76 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// Four values of a run of n (zeros behind it), from the i-th on; vec: they are one aligned 16-byte load.
-__device__ __forceinline__ void load4(const float* p, int i, int n, int64_t stride, bool vec, float (&v)[4]) {
-  if (vec) {
-    const float4 x = i < n ? __ldg(reinterpret_cast<const float4*>(p + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-  } else {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = i + u < n ? __ldg(p + (i + u) * stride) : 0.f;
-  }
+__device__ __forceinline__ void mbar_arrive_elect(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b64 st;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+// Asynchronous copies of 4 or 16 bytes; nothing is read and zeros are written where !there.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const float* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ float4 lds128(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 struct Item {
   int expert, row0, rows, col0;
 };
 
-// The work list: per expert its rows and the number of its first item, in shared memory.
-struct Table {
-  int *lo, *hi, *first;
-  int n_experts, col_tiles, items;
-  // Row tiles of an expert in groups of kGroupTiles; in a group the column tiles one after the other, each
-  // with all row tiles, so that the CTAs at work share both the rows' and the weights' tiles in L2.
-  template <int BN>
-  __device__ __forceinline__ Item item(int i) const {
-    int a = 0, b = n_experts;  // first[a] <= i < first[b]
-    while (b - a > 1) {
-      const int mid = (a + b) >> 1;
-      if (first[mid] <= i)
-        a = mid;
-      else
-        b = mid;
-    }
-    const int rows = hi[a] - lo[a], tiles = (rows + kTileM - 1) / kTileM;
-    const int r = i - first[a], per = kGroupTiles * col_tiles, group = r / per, in = r - group * per;
-    const int n = min(kGroupTiles, tiles - group * kGroupTiles), ct = in / n, rt = group * kGroupTiles + in - ct * n;
-    return {a, lo[a] + rt * kTileM, min(kTileM, rows - rt * kTileM), ct * BN};
-  }
+// An expert's rows, offsets out of range or descending cut to what lies inside.
+struct Range {
+  int lo, hi;
+  bool bad;
 };
+__device__ __forceinline__ Range expert_rows(const ProductParams& p, int e) {
+  if (!p.offsets) return {0, p.rows, false};
+  const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+  const int lo = min(max(a, 0), p.rows), hi = min(max(b, lo), p.rows);
+  return {lo, hi, a != lo || b != hi};
+}
+
+// The i-th item of the work list; first[e]: the first one of expert e, in shared memory. A whole warp calls it.
+// Row tiles of an expert go in groups of kGroupTiles; in a group the column tiles one after the other, each
+// with all row tiles, so that the CTAs at work share both the rows' and the weights' tiles in L2.
+template <int BN>
+__device__ __forceinline__ Item find_item(const ProductParams& p, const int* first, int col_tiles, int i) {
+  const int lane = threadIdx.x & 31;
+  int a = 0, b = p.n_experts;  // first[a] <= i < first[b]
+  while (b - a > 1) {          // 32 pieces at a time
+    const int step = (b - a + 31) / 32, at = a + lane * step;
+    const unsigned m = __ballot_sync(~0u, at < b && first[at] <= i);  // a run of ones from lane 0 on
+    a += (31 - __clz(m)) * step;
+    b = min(a + step, b);
+  }
+  const Range x = expert_rows(p, a);
+  const int rows = x.hi - x.lo, tiles = (rows + kTileM - 1) / kTileM;
+  int in = i - first[a], base = 0;
+  if (tiles > kGroupTiles) {
+    const int per = kGroupTiles * col_tiles, group = in / per;
+    in -= group * per;
+    base = group * kGroupTiles;
+  }
+  const int n = min(kGroupTiles, tiles - base);
+  const int ct = (int)__fdividef((float)in + 0.5f, (float)n);  // in < 2^13 and n <= 16: never near an integer
+  const int rt = base + in - ct * n;
+  return {a, x.lo + rt * kTileM, min(kTileM, rows - rt * kTileM), ct * BN};
+}
 
 template <int BN, bool TRANS>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ ProductParams p, const __grid_constant__ ProductMaps maps) {
   using L = Layout<BN>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_sum[kThreads / 32];
-  __shared__ float s_factors[kSumWarps][4][32];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -157,12 +186,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   // ---------------------------------------------------------------- work list
-  Table tab;
-  tab.lo = reinterpret_cast<int*>(smem + L::table_off);
-  tab.hi = tab.lo + p.n_experts;
-  tab.first = tab.hi + p.n_experts;
-  tab.n_experts = p.n_experts;
-  tab.col_tiles = (p.outc + BN - 1) / BN;
+  int* first = reinterpret_cast<int*>(smem + L::table_off);
+  int* s_sum = reinterpret_cast<int*>(smem + L::sum_off);
+  const int col_tiles = (p.outc + BN - 1) / BN;
+  int n_items = 0;
   {
     constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
     int items[kPer], sum = 0;
@@ -172,16 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e = tid * kPer + i;
       items[i] = 0;
       if (e < p.n_experts) {
-        int lo = 0, hi = p.rows;
-        if (p.offsets) {
-          const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
-          lo = min(max(a, 0), p.rows);
-          hi = min(max(b, lo), p.rows);
-          bad |= a != lo || b != hi;
-        }
-        tab.lo[e] = lo;
-        tab.hi[e] = hi;
-        items[i] = (hi - lo + kTileM - 1) / kTileM * tab.col_tiles;
+        const Range r = expert_rows(p, e);
+        bad |= r.bad;
+        items[i] = (r.hi - r.lo + kTileM - 1) / kTileM * col_tiles;
       }
       sum += items[i];
     }
@@ -196,18 +216,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int at = incl - sum, all = 0;
+    int at = incl - sum;
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) at += s_sum[w];
-      all += s_sum[w];
+      n_items += s_sum[w];
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      if (tid * kPer + i < p.n_experts) tab.first[tid * kPer + i] = at;
+      if (tid * kPer + i < p.n_experts) first[tid * kPer + i] = at;
       at += items[i];
     }
-    if (tid == 0) tab.first[p.n_experts] = all;
-    tab.items = all;
     __syncthreads();
   }
   const uint32_t tmem = *s_tmem;
@@ -216,13 +234,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kWarpSum0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
   if (warp == kWarpCopy) {
     // ------------------------------------------------------------ copies
-    if (lane == 0) {
-      uint32_t g = 0;
-      bool ok = true;
-      for (int i = blockIdx.x; i < tab.items && ok; i += gridDim.x) {
-        const Item it = tab.item<BN>(i);
-        const int box = it.rows > 64 ? 2 : it.rows > 32 ? 1 : 0;
-        const uint32_t bytes = (32u << box) * 128u + L::kBBytes;
+    uint32_t g = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+      const Item it = find_item<BN>(p, first, col_tiles, i);
+      const int box = it.rows > 64 ? 2 : it.rows > 32 ? 1 : 0;
+      const uint32_t bytes = (32u << box) * 128u + L::kBBytes;
+      if (lane == 0)
         for (int kb = 0; kb < kb_n; ++kb, ++g) {
           const int s = g % L::kStages;
           if (!(ok = mbar_wait(empty(s), ((g / L::kStages) & 1) ^ 1, s_abort))) break;
@@ -237,21 +255,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(b, &maps.w, kb * 128, it.col0, it.expert, full(s));
           }
         }
-      }
-      if (!ok)  // a wait gave up: the copies in flight land before the CTA ends
-        for (int s = 0; s < L::kStages && (int)g - 1 - s >= 0; ++s) {
-          const uint32_t h = g - 1 - s;
-          const long long t0 = clock64();
-          while (!mbar_try_wait(full(h % L::kStages), (h / L::kStages) & 1) && clock64() - t0 < kWaitCycles) {
-          }
-        }
+      ok = __shfl_sync(~0u, ok, 0);
     }
+    if (!ok && lane == 0)  // a wait gave up: the copies in flight land before the CTA ends
+      for (int s = 0; s < L::kStages && (int)g - 1 - s >= 0; ++s) {
+        const uint32_t h = g - 1 - s;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(full(h % L::kStages), (h / L::kStages) & 1) && clock64() - t0 < kWaitCycles) {
+        }
+      }
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issue
     const uint32_t idesc = idesc_e4m3(kTileM, BN, TRANS);
     uint32_t g = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < tab.items && ok; i += gridDim.x)
+    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x)
       for (int kb = 0; kb < kb_n; ++kb, ++g) {
         const int s = g % L::kStages, buf = g & 1;
         // one lane waits for the copies, the others for the accumulator
@@ -276,63 +294,103 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ scaling, adding, output
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     constexpr int kCols = BN / 2;  // columns of a warp
-    const int quad = warp & 3, part = (warp - kWarpSum0) >> 2;
+    const int quad = warp & 3, part = (warp - kWarpSum0) >> 2, r = quad * 32 + lane;
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
-    const int w_stride = TRANS ? p.out_blocks : 1;  // from one block of inputs to the next
-    const bool vec = kb_n % 4 == 0, vec_a = vec && p.a.scale_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.a.scale) & 15) == 0;
-    const bool vec_w = !TRANS && vec && (reinterpret_cast<uintptr_t>(p.wscale) & 15) == 0;
-    float* factors = &s_factors[warp - kWarpSum0][0][lane];
+    const uint32_t s_a = base + L::sa_off + (warp - kWarpSum0) * 1024 + lane * 16;
+    const uint32_t s_w = base + L::sw_off + (warp - kWarpSum0) * 32;
+    const uint32_t s_out = base + L::out_off + (warp - kWarpSum0) * 2048;
+    const bool vec = kb_n % 4 == 0 && p.a.scale_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.a.scale) & 15) == 0;
+    const float *sa = nullptr, *sw = nullptr;  // scales of the item whose copies are issued next
+    // Rows past the tile and columns past the matrix are computed on what lies there and not stored.
+    auto scales_of = [&](const Item& it) {
+      sa = p.a.scale + (it.row0 + min(r, it.rows - 1)) * p.a.scale_stride;
+      const int cb = min((it.col0 + part * kCols) / kScaleBlock, p.out_blocks - 1);
+      sw = p.wscale + (int64_t)it.expert * p.in_blocks * p.out_blocks + (TRANS ? cb : (int64_t)cb * p.in_blocks);
+    };
+    // The factors of blocks kb .. kb + 3, asynchronously, into a slot of the warp's own: a row's scales into its
+    // thread's, the weights' by the first four lanes. (Loads into registers would be waited for where the loop
+    // closes: 177 cycles a block.)
+    auto copy_scales = [&](int kb, int slot) {
+      if (vec)
+        copy16(s_a + slot * 512, sa + kb, true);
+      else
+#pragma unroll
+        for (int u = 0; u < 4; ++u) copy4(s_a + slot * 512 + u * 4, kb + u < kb_n ? sa + kb + u : sa, kb + u < kb_n);
+      if (lane < 4) {
+        const bool there = kb + lane < kb_n;
+        copy4(s_w + slot * 16 + lane * 4, there ? sw + (int64_t)(kb + lane) * (TRANS ? p.out_blocks : 1) : sw, there);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     uint32_t g = 0;
-    bool ok = true;
-    for (int i = blockIdx.x; i < tab.items && ok; i += gridDim.x) {
-      const Item it = tab.item<BN>(i);
-      const int r = quad * 32 + lane, col0 = it.col0 + part * kCols;
-      // rows past the tile and columns past the matrix are computed on what lies there and not stored
-      const float* sa = p.a.scale + (it.row0 + min(r, it.rows - 1)) * p.a.scale_stride;
-      const int cb = min(col0 / kScaleBlock, p.out_blocks - 1);
-      const float* sw = p.wscale + (int64_t)it.expert * p.in_blocks * p.out_blocks + (TRANS ? cb : (int64_t)cb * p.in_blocks);
-      uint64_t acc[kCols / 2];
+    int slot = 0;
+    Item nx = {0, 0, 1, 0};
+    if (blockIdx.x < n_items) {
+      nx = find_item<BN>(p, first, col_tiles, blockIdx.x);
+      scales_of(nx);
+      copy_scales(0, 0);
+    }
+    for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
+      const Item it = nx;
+      const bool more = i + (int)gridDim.x < n_items;
+      if (more) nx = find_item<BN>(p, first, col_tiles, i + gridDim.x);
+      float acc[kCols];
 #pragma unroll
-      for (int c = 0; c < kCols / 2; ++c) acc[c] = 0;
-      float fa[4], fw[4];
-      load4(sa, 0, kb_n, 1, vec_a, fa);
-      load4(sw, 0, kb_n, w_stride, vec_w, fw);
-      for (int kb = 0; kb < kb_n; ++kb, ++g) {
-        if ((kb & 3) == 0) {  // the factors of four blocks: each thread's own, so that no barrier is needed
-#pragma unroll
-          for (int u = 0; u < 4; ++u) factors[u * 32] = fa[u] * fw[u];
-          load4(sa, kb + 4, kb_n, 1, vec_a, fa);
-          load4(sw, kb + 4, kb_n, w_stride, vec_w, fw);
+      for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+      for (int kb0 = 0; kb0 < kb_n; kb0 += 4) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();  // the other lanes' copies too; and nobody reads the other slot any more
+        const float4 fa = lds128(s_a + slot * 512), fw = lds128(s_w + slot * 16);
+        const float f4[4] = {fa.x * fw.x, fa.y * fw.y, fa.z * fw.z, fa.w * fw.w};
+        slot ^= 1;
+        if (kb0 + 4 < kb_n) {
+          copy_scales(kb0 + 4, slot);
+        } else if (more) {
+          scales_of(nx);
+          copy_scales(0, slot);
         }
-        const int buf = g & 1;
-        if (!(ok = __all_sync(~0u, mbar_wait(acc_full(buf), (g >> 1) & 1, s_abort)))) break;
-        tc_fence_after();
-        const float f = factors[(kb & 3) * 32];
-        const uint64_t f2 = pack2(f, f);
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          float v[32];
-          tmem_ld32(taddr + buf * BN + c, v);
-          tmem_wait_ld32(v);
-          if (c + 32 == kCols) {
-            tc_fence_before();
+        for (int u = 0; u < 4; ++u) {
+          if (kb0 + u < kb_n) {
+            const int buf = g & 1;
+            // after a wait that gave up, all later ones return at once, and what is computed is not stored
+            if (!mbar_try_wait(acc_full(buf), (g >> 1) & 1)) mbar_wait(acc_full(buf), (g >> 1) & 1, s_abort);
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty(buf));
-          }
+            tc_fence_after();
+            ++g;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) acc[c / 2 + x] = fma2(f2, pack2(v[2 * x], v[2 * x + 1]), acc[c / 2 + x]);
+            for (int c = 0; c < kCols; c += 32) {
+              float v[32];
+              tmem_ld32(taddr + buf * BN + c, v);
+              tmem_wait_ld32(v);
+              if (c + 32 == kCols) {
+                tc_fence_before();
+                mbar_arrive_elect(acc_empty(buf));
+              }
+#pragma unroll
+              for (int x = 0; x < 32; ++x) acc[c + x] = fmaf(f4[u], v[x], acc[c + x]);
+            }
+          }
         }
       }
-      if (ok && r < it.rows) {
-        uint16_t* o = static_cast<uint16_t*>(p.out.p) + (int64_t)(it.row0 + r) * p.out.stride + col0;
+      if (*s_abort) continue;
+      // 32 rows x 32 columns at a time through shared memory, so that four lanes store 64 bytes of a row
+      // (a thread's own row in 16-byte stores costs a tag lookup each: 4000 cycles an item)
+      const int col0 = it.col0 + part * kCols, sub = lane & 3;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 8)
-          if (col0 + c < p.outc) {  // the columns are a multiple of 16
-            float x[8];
+      for (int c = 0; c < kCols; c += 32) {
+        __syncwarp();
 #pragma unroll
-            for (int u = 0; u < 4; ++u) unpack2(acc[c / 2 + u], x[2 * u], x[2 * u + 1]);
-            *reinterpret_cast<uint4*>(o + c) = float_to_bf16x8(x);
-          }
+        for (int x = 0; x < 4; ++x) sts128(s_out + lane * 64 + ((x ^ (lane >> 1)) & 3) * 16, float_to_bf16x8(acc + c + 8 * x));
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int row = y * 8 + (lane >> 2);
+          const float4 v = lds128(s_out + row * 64 + ((sub ^ (row >> 1)) & 3) * 16);
+          if (quad * 32 + row < it.rows && col0 + c + sub * 8 < p.outc)
+            *reinterpret_cast<float4*>(static_cast<uint16_t*>(p.out.p) + (int64_t)(it.row0 + quad * 32 + row) * p.out.stride +
+                                       col0 + c + sub * 8) = v;
+        }
       }
     }
   }
@@ -369,7 +427,7 @@ cudaError_t launch(const ProductParams& p, cudaStream_t s) {
   const int64_t tiles = (p.rows + kTileM - 1) / kTileM + (p.n_experts < p.rows ? p.n_experts : p.rows) - 1;
   const int64_t items = tiles * ((p.outc + BN - 1) / BN);
   const int grid = items < sm_count() ? (int)items : sm_count();
-  return launch_pdl(product_kernel<BN, TRANS>, grid, kThreads, (size_t)(L::fixed + (3 * p.n_experts + 1) * 4), 1, s, p, maps);
+  return launch_pdl(product_kernel<BN, TRANS>, grid, kThreads, (size_t)(L::fixed + (p.n_experts + 1) * 4), 1, s, p, maps);
 }
 
 }  // namespace
