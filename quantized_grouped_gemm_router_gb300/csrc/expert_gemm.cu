@@ -10,6 +10,7 @@
 // factor is one register. Persistent CTAs, one per SM, walk the items (expert, row tile, column tile):
 //   warp 0       copies: per block of 128 inputs the rows (32, 64 or 128 of them) and BN weight columns
 //   warp 1       MMA issue: per block four MMAs of K = 32
+//   warps 2-3    the factors of four blocks ahead, into shared memory
 //   warps 4-11   scaling and adding, then the output; warp w reads lane quadrant w % 4 and half of the
 //                columns
 // Transposed weights are read as they lie: their tile has its column axis contiguous (the other "major"
@@ -24,11 +25,12 @@ bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, con
 namespace {
 
 constexpr int kTileM = 128;
-constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpSum0 = 4, kSumWarps = 8;
+constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpScale0 = 2, kScaleWarps = 2, kWarpSum0 = 4, kSumWarps = 8;
 constexpr int kThreads = (kWarpSum0 + kSumWarps) * 32;  // 384
 // Registers: 168 a thread at launch; the first four warps give up 96 each, the summing ones take 48 more:
 // 128 * 72 + 256 * 216 = 384 * 168.
 constexpr int kFewRegs = 72, kManyRegs = 216;
+constexpr int kSlots = 3, kSlotBytes = 4 * 2 * kTileM * 4;
 constexpr int kGroupTiles = 16;  // row tiles of an expert whose column tiles run together
 
 struct ProductMaps {
@@ -41,13 +43,13 @@ struct Layout {
   static constexpr int kABytes = kTileM * 128, kBBytes = BN * 128, kStage = kABytes + kBBytes;
   static constexpr int kStages = BN == 256 ? 4 : 6;
   static constexpr int bar_off = kStages * kStage;
-  static constexpr int n_bars = 2 * kStages + 4;
+  static constexpr int n_bars = 2 * kStages + 4 + 2 * kSlots;
   static constexpr int misc_off = bar_off + n_bars * 8;
   static constexpr int out_off = (misc_off + 16 + 127) / 128 * 128;  // per summing warp: 32 rows x 32 columns of bf16
-  static constexpr int sa_off = out_off + kSumWarps * 2048;          // per summing warp: two slots of 4 scales x 32 rows
-  static constexpr int sw_off = sa_off + kSumWarps * 1024;           // and of 4 of the weights
-  static constexpr int sum_off = sw_off + kSumWarps * 32;            // the work list's partial sums
-  static constexpr int table_off = sum_off + 64;                     // first item of every expert, and their number
+  static constexpr int f_off = out_off + kSumWarps * 2048;           // factors: slots of 4 blocks x 2 column halves x 128 rows
+  static constexpr int item_off = f_off + kSlots * kSlotBytes;       // and the item that a slot belongs to
+  static constexpr int sum_off = item_off + kSlots * 16;             // the work list's partial sums
+  static constexpr int table_off = sum_off + 64;                     // first item of every expert
   static constexpr int fixed = table_off + 1024;                     // and slack to align the base
   static constexpr int most = fixed + (kMaxExperts + 1) * 4;
   static_assert(most <= 232448, "shared memory");
@@ -88,13 +90,20 @@ __device__ __forceinline__ void mbar_arrive_elect(uint32_t bar) {
       "@e mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
-// Asynchronous copies of 4 or 16 bytes; nothing is read and zeros are written where !there.
-__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+// Four values of a run of n (zeros behind it), from the i-th on; vec: they are one aligned 16-byte load.
+__device__ __forceinline__ float4 load4(const float* p, int i, int n, int64_t stride, bool vec) {
+  if (vec) return __ldg(reinterpret_cast<const float4*>(p + i));
+  float v[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) v[u] = i + u < n ? __ldg(p + (i + u) * stride) : 0.f;
+  return make_float4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const float* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+__device__ __forceinline__ float lds32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
 }
+__device__ __forceinline__ void sts32(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 __device__ __forceinline__ float4 lds128(uint32_t a) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
@@ -160,6 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto empty = [&](int s) { return bars + 8u * (L::kStages + s); };
   auto acc_full = [&](int b) { return bars + 8u * (2 * L::kStages + b); };
   auto acc_empty = [&](int b) { return bars + 8u * (2 * L::kStages + 2 + b); };
+  auto f_full = [&](int s) { return bars + 8u * (2 * L::kStages + 4 + s); };
+  auto f_empty = [&](int s) { return bars + 8u * (2 * L::kStages + 4 + kSlots + s); };
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::misc_off);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::misc_off + 4);
 
@@ -171,6 +182,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
       mbar_init(acc_empty(b), kSumWarps);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(f_full(s), kScaleWarps);
+      mbar_init(f_empty(s), kSumWarps);
     }
     *s_abort = 0;
     fence_barrier_init();
@@ -272,10 +287,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x)
       for (int kb = 0; kb < kb_n; ++kb, ++g) {
         const int s = g % L::kStages, buf = g & 1;
-        // one lane waits for the copies, the others for the accumulator
-        ok = __all_sync(~0u, lane == 0 ? mbar_wait(full(s), (g / L::kStages) & 1, s_abort)
-                                       : mbar_wait(acc_empty(buf), ((g >> 1) & 1) ^ 1, s_abort));
-        if (!ok) break;
+        const bool ready = mbar_try_wait(full(s), (g / L::kStages) & 1) & mbar_try_wait(acc_empty(buf), ((g >> 1) & 1) ^ 1);
+        if (!__all_sync(~0u, ready)) {
+          ok = __all_sync(~0u, mbar_wait(full(s), (g / L::kStages) & 1, s_abort)) &&
+               __all_sync(~0u, mbar_wait(acc_empty(buf), ((g >> 1) & 1) ^ 1, s_abort));
+          if (!ok) break;
+        }
         tc_fence_after();
         const uint32_t a = base + s * L::kStage, b = a + L::kABytes;
         if (TRANS)
@@ -290,85 +307,101 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (!mbar_try_wait(empty((g - 1) % L::kStages), ((g - 1) / L::kStages) & 1) && clock64() - t0 < kWaitCycles) {
       }
     }
-  } else if (warp >= kWarpSum0) {
+  } else if (warp < kWarpSum0) {
+    // ------------------------------------------------------------ factors
+    // Of four blocks at a time: each row's scale times that of the weights, for either half of the columns.
+    // Rows past the tile and columns past the matrix get those of the last ones; their sums are not stored.
+    const bool vec = kb_n % 4 == 0, vec_a = vec && p.a.scale_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.a.scale) & 15) == 0;
+    const bool vec_w = !TRANS && vec && (reinterpret_cast<uintptr_t>(p.wscale) & 15) == 0;
+    const int r0 = (warp - kWarpScale0) * 64 + lane, w_stride = TRANS ? p.out_blocks : 1;
+    uint32_t g = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+      const Item it = find_item<BN>(p, first, col_tiles, i);
+      const float *sa[2], *sw[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sa[h] = p.a.scale + (it.row0 + min(r0 + 32 * h, it.rows - 1)) * p.a.scale_stride;
+        const int cb = min((it.col0 + h * (BN / 2)) / kScaleBlock, p.out_blocks - 1);
+        sw[h] = p.wscale + (int64_t)it.expert * p.in_blocks * p.out_blocks + (TRANS ? cb : (int64_t)cb * p.in_blocks);
+      }
+      for (int kb = 0; kb < kb_n; kb += 4, ++g) {
+        const int s = g % kSlots;
+        float4 a[2], w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          a[h] = load4(sa[h], kb, kb_n, 1, vec_a);
+          w[h] = load4(sw[h], kb, kb_n, w_stride, vec_w);
+        }
+        if (!(ok = __all_sync(~0u, mbar_wait(f_empty(s), ((g / kSlots) & 1) ^ 1, s_abort)))) break;
+        const uint32_t f = base + L::f_off + s * kSlotBytes + r0 * 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            sts32(f + h * 512 + x * 128, a[x].x * w[h].x);
+            sts32(f + 1024 + h * 512 + x * 128, a[x].y * w[h].y);
+            sts32(f + 2048 + h * 512 + x * 128, a[x].z * w[h].z);
+            sts32(f + 3072 + h * 512 + x * 128, a[x].w * w[h].w);
+          }
+        if (threadIdx.x == kWarpScale0 * 32)
+          sts128(base + L::item_off + s * 16, make_uint4(it.row0, it.rows, it.col0, 0));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(f_full(s));
+      }
+    }
+  } else {
     // ------------------------------------------------------------ scaling, adding, output
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     constexpr int kCols = BN / 2;  // columns of a warp
-    const int quad = warp & 3, part = (warp - kWarpSum0) >> 2, r = quad * 32 + lane;
+    const int quad = warp & 3, part = (warp - kWarpSum0) >> 2;
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
-    const uint32_t s_a = base + L::sa_off + (warp - kWarpSum0) * 1024 + lane * 16;
-    const uint32_t s_w = base + L::sw_off + (warp - kWarpSum0) * 32;
+    const uint32_t s_f = base + L::f_off + part * 512 + (quad * 32 + lane) * 4;
     const uint32_t s_out = base + L::out_off + (warp - kWarpSum0) * 2048;
-    const bool vec = kb_n % 4 == 0 && p.a.scale_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.a.scale) & 15) == 0;
-    const float *sa = nullptr, *sw = nullptr;  // scales of the item whose copies are issued next
-    // Rows past the tile and columns past the matrix are computed on what lies there and not stored.
-    auto scales_of = [&](const Item& it) {
-      sa = p.a.scale + (it.row0 + min(r, it.rows - 1)) * p.a.scale_stride;
-      const int cb = min((it.col0 + part * kCols) / kScaleBlock, p.out_blocks - 1);
-      sw = p.wscale + (int64_t)it.expert * p.in_blocks * p.out_blocks + (TRANS ? cb : (int64_t)cb * p.in_blocks);
+    // After a wait that gave up, all later ones return at once, and what is computed is not stored.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (!mbar_try_wait(bar, parity)) mbar_wait(bar, parity, s_abort);
+      __syncwarp();
     };
-    // The factors of blocks kb .. kb + 3, asynchronously, into a slot of the warp's own: a row's scales into its
-    // thread's, the weights' by the first four lanes. (Loads into registers would be waited for where the loop
-    // closes: 177 cycles a block.)
-    auto copy_scales = [&](int kb, int slot) {
-      if (vec)
-        copy16(s_a + slot * 512, sa + kb, true);
-      else
-#pragma unroll
-        for (int u = 0; u < 4; ++u) copy4(s_a + slot * 512 + u * 4, kb + u < kb_n ? sa + kb + u : sa, kb + u < kb_n);
-      if (lane < 4) {
-        const bool there = kb + lane < kb_n;
-        copy4(s_w + slot * 16 + lane * 4, there ? sw + (int64_t)(kb + lane) * (TRANS ? p.out_blocks : 1) : sw, there);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    uint32_t g = 0;
-    int slot = 0;
-    Item nx = {0, 0, 1, 0};
-    if (blockIdx.x < n_items) {
-      nx = find_item<BN>(p, first, col_tiles, blockIdx.x);
-      scales_of(nx);
-      copy_scales(0, 0);
-    }
+    uint32_t g = 0, q = 0;
     for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
-      const Item it = nx;
-      const bool more = i + (int)gridDim.x < n_items;
-      if (more) nx = find_item<BN>(p, first, col_tiles, i + gridDim.x);
+      Item it;
       float acc[kCols];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-      for (int kb0 = 0; kb0 < kb_n; kb0 += 4) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncwarp();  // the other lanes' copies too; and nobody reads the other slot any more
-        const float4 fa = lds128(s_a + slot * 512), fw = lds128(s_w + slot * 16);
-        const float f4[4] = {fa.x * fw.x, fa.y * fw.y, fa.z * fw.z, fa.w * fw.w};
-        slot ^= 1;
-        if (kb0 + 4 < kb_n) {
-          copy_scales(kb0 + 4, slot);
-        } else if (more) {
-          scales_of(nx);
-          copy_scales(0, slot);
+      for (int kb0 = 0; kb0 < kb_n; kb0 += 4, ++q) {
+        const int s = q % kSlots;
+        wait(f_full(s), (q / kSlots) & 1);
+        float f4[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) f4[u] = lds32(s_f + s * kSlotBytes + u * 1024);
+        if (kb0 == 0) {
+          const float4 x = lds128(base + L::item_off + s * 16);
+          it = {0, __float_as_int(x.x), __float_as_int(x.y), __float_as_int(x.z)};
         }
+        __syncwarp();
+        mbar_arrive_elect(f_empty(s));
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           if (kb0 + u < kb_n) {
             const int buf = g & 1;
-            // after a wait that gave up, all later ones return at once, and what is computed is not stored
-            if (!mbar_try_wait(acc_full(buf), (g >> 1) & 1)) mbar_wait(acc_full(buf), (g >> 1) & 1, s_abort);
-            __syncwarp();
+            wait(acc_full(buf), (g >> 1) & 1);
             tc_fence_after();
             ++g;
+            float v[2][32];  // the next 32 columns arrive while these are added
+            tmem_ld32(taddr + buf * BN, v[0]);
 #pragma unroll
             for (int c = 0; c < kCols; c += 32) {
-              float v[32];
-              tmem_ld32(taddr + buf * BN + c, v);
-              tmem_wait_ld32(v);
-              if (c + 32 == kCols) {
+              const int x = c / 32 & 1;
+              tmem_wait_ld32(v[x]);
+              if (c + 32 < kCols) {
+                tmem_ld32(taddr + buf * BN + c + 32, v[x ^ 1]);
+              } else {
                 tc_fence_before();
                 mbar_arrive_elect(acc_empty(buf));
               }
 #pragma unroll
-              for (int x = 0; x < 32; ++x) acc[c + x] = fmaf(f4[u], v[x], acc[c + x]);
+              for (int y = 0; y < 32; ++y) acc[c + y] = fmaf(f4[u], v[x][y], acc[c + y]);
             }
           }
         }
