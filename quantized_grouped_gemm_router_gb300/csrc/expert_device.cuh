@@ -47,12 +47,21 @@ __device__ __forceinline__ BlockScale block_scale(float a) {
 // The code's value before rounding: infinities become NaN (inf * 0), everything else stays x * inv.
 __device__ __forceinline__ float coded(float x, float inv) { return __fmaf_rn(x, 0.f, __fmul_rn(x, inv)); }
 
+__device__ __forceinline__ uint4 codes16(const float (&y)[16]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = to_e4m3x2(y[4 * i], y[4 * i + 1]) | to_e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Quantises 16 consecutive values per lane, 8 lanes to a block of 128; a whole warp calls it.
 __device__ __forceinline__ uint4 quantise16(const float (&x)[16], float* scale) {
-  float a = 0.f;
+  float a = 0.f, y[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x[i]));  // NaN is passed over
-  if (__any_sync(~0u, !(a < INFINITY))) {                  // rare: an infinity does not count either
+  const bool fine = __all_sync(~0u, a < INFINITY);
+  if (!fine) {  // rare: an infinity does not count either
     a = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -64,12 +73,14 @@ __device__ __forceinline__ uint4 quantise16(const float (&x)[16], float* scale) 
   for (int o = 1; o < 8; o <<= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
   const BlockScale b = block_scale(a);
   *scale = b.scale;
-  uint32_t w[4];
+  if (fine) {  // no infinities: the product alone (NaN stays NaN)
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = to_e4m3x2(coded(x[4 * i], b.inv), coded(x[4 * i + 1], b.inv)) |
-           to_e4m3x2(coded(x[4 * i + 2], b.inv), coded(x[4 * i + 3], b.inv)) << 16;
-  return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(x[i], b.inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = coded(x[i], b.inv);
+  }
+  return codes16(y);
 }
 
 __device__ __forceinline__ const uint4* bf16_at(const moe_rows& r, int64_t row, int col) {

@@ -4,6 +4,7 @@
 //
 // A warp takes pieces of 512 columns, 16 to a lane (two 16-byte loads; 16 codes are one 16-byte store),
 // so that 8 neighbouring lanes hold a block of 128 and find its largest magnitude by three shuffles.
+#include "attn_ptx.cuh"
 #include "expert_device.cuh"
 
 namespace moe {
@@ -21,6 +22,8 @@ inline Split split_of(int pieces) {
   while (w < kWarps && 2 * w <= pieces) w *= 2;
   return {w, kWarps / w};
 }
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // ------------------------------------------------------------------------------------ dispatch
 template <bool E4M3>
@@ -120,32 +123,45 @@ __global__ void __launch_bounds__(512) combine_grad_kernel(const __grid_constant
     return;
   }
   const float w = __ldg(p.w + a);
-  float dot = 0.f;
-#pragma unroll 2
-  for (int c0 = 0; c0 < p.d; c0 += kPiece) {
-    const int c = c0 + lane * 16;
-    const bool mine = c < p.d;
-    uint4 g[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, y[2] = {g[0], g[0]};
-    if (mine) {
-      load16(p.dy, t, c, g);
-      load16(p.ys, place, c, y);
-    }
-    float x[16], z[16];
-    bf16x8_to_float(g[0], x);
-    bf16x8_to_float(g[1], x + 8);
-    bf16x8_to_float(y[0], z);
-    bf16x8_to_float(y[1], z + 8);
+  const uint64_t w2 = pack2(w, w);
+  uint64_t dot2[2] = {0, 0};
+  constexpr int kAhead = 2;  // pieces whose loads are in flight together
+  for (int c0 = 0; c0 < p.d; c0 += kAhead * kPiece) {
+    uint4 g[kAhead][2], y[kAhead][2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      dot = fmaf(x[i], z[i], dot);
-      x[i] *= w;
+    for (int h = 0; h < kAhead; ++h) {
+      const int c = c0 + h * kPiece + lane * 16;
+      g[h][0] = g[h][1] = y[h][0] = y[h][1] = make_uint4(0, 0, 0, 0);
+      if (c < p.d) {
+        load16(p.ys, place, c, y[h]);
+        load16(p.dy, t, c, g[h]);
+      }
     }
-    if (!mine) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = 0.f;  // not 0 * w: w may be infinite
+    for (int h = 0; h < kAhead; ++h) {
+      if (c0 + h * kPiece >= p.d) break;
+      const int c = c0 + h * kPiece + lane * 16;
+      const bool mine = c < p.d;
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t gw = word(g[h][i >> 2], i & 3), yw = word(y[h][i >> 2], i & 3);
+        const uint64_t g2 = pack2(__uint_as_float(gw << 16), __uint_as_float(gw & 0xFFFF0000u));
+        const uint64_t y2 = pack2(__uint_as_float(yw << 16), __uint_as_float(yw & 0xFFFF0000u));
+        dot2[i & 1] = fma2(g2, y2, dot2[i & 1]);
+        unpack2(mul2(g2, w2), x[2 * i], x[2 * i + 1]);
+      }
+      if (!mine) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = 0.f;  // not 0 * w: w may be infinite
+      }
+      store16<E4M3>(p.dys, place, c, x, mine);
     }
-    store16<E4M3>(p.dys, place, c, x, mine);
   }
+  float part[4];
+  unpack2(dot2[0], part[0], part[1]);
+  unpack2(dot2[1], part[2], part[3]);
+  float dot = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
   if (lane == 0) p.dw[a] = dot;

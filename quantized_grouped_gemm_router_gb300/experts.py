@@ -130,14 +130,23 @@ class E4m3Weights:
         return cls(q, scale)
 
 
+_I16, _I32, _F32, _U8 = torch.int16, torch.int32, torch.float32, torch.uint8
+
+# The checks below take as few calls into torch as they can: a call on small rows is bound by its host time.
+
+
 def _bf16(t: torch.Tensor, rows: int | None, cols: int | None, name: str, dev: int) -> RowsC:
     """A view of bf16 rows; rows and cols None: any."""
-    if (t.dtype is not torch.int16 or t.get_device() != dev or t.dim() != 2 or rows not in (None, t.shape[0])
-            or cols not in (None, t.shape[1]) or (t.numel() and t.stride(1) != 1)):
-        want = f"[{'rows' if rows is None else rows}, {'columns' if cols is None else cols}]"
-        raise ValueError(f"{name} must be an int16 tensor {want} on the current CUDA device, the values of a row "
-                         "contiguous")
-    return RowsC(ROWS_BF16, t.data_ptr(), t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8, None, 0)
+    shape = t.shape
+    if t.dtype is _I16 and t.get_device() == dev and len(shape) == 2:
+        r, c = shape
+        if (rows is None or r == rows) and (cols is None or c == cols):
+            stride, inner = t.stride()
+            if inner == 1 or r * c == 0:
+                # the stride of an axis of length one is never used, and torch may give any
+                return RowsC(ROWS_BF16, t.data_ptr(), stride if r > 1 else (c + 7) // 8 * 8, None, 0)
+    want = f"[{'rows' if rows is None else rows}, {'columns' if cols is None else cols}]"
+    raise ValueError(f"{name} must be an int16 tensor {want} on the current CUDA device, the values of a row contiguous")
 
 
 def _e4m3(r: E4m3Rows, rows: int | None, cols: int, name: str, dev: int) -> RowsC:
@@ -146,46 +155,48 @@ def _e4m3(r: E4m3Rows, rows: int | None, cols: int, name: str, dev: int) -> Rows
     return r._c
 
 
-def _out(out, e4m3: bool, rows: int | None, cols: int, dev: int):
-    """The output rows (made, if none are given, for `rows` rows) and their description."""
+def _out(out, e4m3: bool, rows: int | None, cols: int, dev: int, like: torch.Tensor):
+    """The output rows and their description; if none are given, `rows` new ones on the device of `like`."""
     if out is None:
-        device = torch.device("cuda", dev)
-        out = (E4m3Rows.empty(rows, cols, device) if e4m3
-               else torch.empty((rows, cols), dtype=torch.int16, device=device))
+        if not e4m3:
+            out = torch.empty((rows, cols), dtype=_I16, device=like.device)
+            return out, RowsC(ROWS_BF16, out.data_ptr(), cols if rows > 1 else (cols + 7) // 8 * 8, None, 0)
+        out = E4m3Rows.empty(rows, cols, like.device)
     if isinstance(out, E4m3Rows):
         return out, _e4m3(out, rows, cols, "out", dev)
     return out, _bf16(out, rows, cols, "out", dev)
 
 
 def _space(ws: torch.Tensor, dev: int) -> int:
-    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+    if ws.dtype is not _U8 or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on the current CUDA device (expert_workspace)")
     return ws.data_ptr()
 
 
 def _floats(t: torch.Tensor, shape, name: str, dev: int) -> int:
-    if t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
+    if t.dtype is not _F32 or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
         raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape)} on the current CUDA device")
     return t.data_ptr()
 
 
 def _places(inv: torch.Tensor, T: int, dev: int) -> tuple[int, int]:
     """The pointer of inv [T, top_k], and top_k."""
-    if inv.dim() != 2 or inv.shape[0] != T:
+    shape = inv.shape
+    if len(shape) != 2 or shape[0] != T:
         raise ValueError(f"inv must be [{T}, top_k]")
-    return _ints(inv, None, "inv", dev), inv.shape[1]
+    return _ints(inv, None, "inv", dev), shape[1]
 
 
 def sort_tokens(ids: torch.Tensor, n_experts: int, ws: torch.Tensor):
     """moe_sort_tokens: ids int32 [T, top_k], negative for none. Returns offsets [n_experts + 1],
     perm [T * top_k] (place -> assignment) and inv [T, top_k] (assignment -> place), int32."""
     dev = _device(ids, "ids")
-    p = _ints(ids, None, "ids", dev)
-    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=ids.device)
-    perm = torch.empty(ids.numel(), dtype=torch.int32, device=ids.device)
-    inv = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
-    _check(_fn("moe_sort_tokens")(p, ids.numel(), n_experts, offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(),
-                                  _space(ws, dev), ws.numel(), _stream(dev)), "moe_sort_tokens")
+    p, n, device = _ints(ids, None, "ids", dev), ids.numel(), ids.device
+    offsets = torch.empty(max(n_experts, 0) + 1, dtype=_I32, device=device)
+    perm = torch.empty(n, dtype=_I32, device=device)
+    inv = torch.empty_like(ids)
+    _check(_fn("moe_sort_tokens")(p, n, n_experts, offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), _space(ws, dev),
+                                  ws.numel(), _stream(dev)), "moe_sort_tokens")
     return offsets, perm, inv
 
 
@@ -197,7 +208,7 @@ def dispatch(x: torch.Tensor, inv: torch.Tensor | None, ws: torch.Tensor, *, e4m
     xv = _bf16(x, None, None, "x", dev)
     T, d = x.shape
     iv, k = (None, 1) if inv is None else _places(inv, T, dev)
-    out, ov = _out(out, e4m3, T * k if out is None else None, d, dev)
+    out, ov = _out(out, e4m3, T * k if out is None else None, d, dev, x)
     _check(_fn("moe_dispatch")(ctypes.byref(xv), iv, T, k, d, ctypes.byref(ov), out.shape[0], _space(ws, dev),
                                ws.numel(), _stream(dev)), "moe_dispatch")
     return out
@@ -213,7 +224,7 @@ def combine(ys: torch.Tensor, inv: torch.Tensor, w: torch.Tensor | None, ws: tor
     T = inv.shape[0]
     iv, k = _places(inv, T, dev)
     av = None if add is None else _bf16(add, T, d, "add", dev)
-    y, ov = _out(y, False, T, d, dev)
+    y, ov = _out(y, False, T, d, dev, ys)
     _check(_fn("moe_combine")(ctypes.byref(yv), rows, iv, None if w is None else _floats(w, (T, k), "w", dev), T, k, d,
                               None if av is None else ctypes.byref(av), ctypes.byref(ov), _space(ws, dev), ws.numel(),
                               _stream(dev)), "moe_combine")
@@ -231,12 +242,13 @@ def combine_grad(dy: torch.Tensor, ys: torch.Tensor, inv: torch.Tensor, w: torch
     """moe_combine_grad: the gradients (dys, dw) of combine's rows and weights; dys int16 or (e4m3=True)
     E4m3Rows, as many as ys; `out` gives them. The gradient of combine's `add` is dy itself."""
     dev = _device(dy, "dy")
-    dv, yv = _bf16(dy, None, None, "dy", dev), _bf16(ys, None, dy.shape[-1], "ys", dev)
+    dv = _bf16(dy, None, None, "dy", dev)
     T, d = dy.shape
+    yv, rows = _bf16(ys, None, d, "ys", dev), ys.shape[0]
     iv, k = _places(inv, T, dev)
-    out, ov = _out(out, e4m3, ys.shape[0], d, dev)
+    out, ov = _out(out, e4m3, rows, d, dev, dy)
     dw = torch.empty((T, k), dtype=torch.float32, device=dy.device) if dw is None else dw
-    _check(_fn("moe_combine_grad")(ctypes.byref(dv), ctypes.byref(yv), ys.shape[0], iv, _floats(w, (T, k), "w", dev), T,
+    _check(_fn("moe_combine_grad")(ctypes.byref(dv), ctypes.byref(yv), rows, iv, _floats(w, (T, k), "w", dev), T,
                                    k, d, ctypes.byref(ov), _floats(dw, (T, k), "dw", dev), _space(ws, dev), ws.numel(),
                                    _stream(dev)), "moe_combine_grad")
     return out, dw
@@ -254,7 +266,7 @@ def gemm_e4m3(a: E4m3Rows, w: E4m3Weights, offsets: torch.Tensor | None, ws: tor
         raise ValueError("w must be on the current CUDA device")
     E, n, k = w.shape
     av = _e4m3(a, None, n if transposed else k, "a", dev)
-    out, ov = _out(out, False, a.shape[0], k if transposed else n, dev)
+    out, ov = _out(out, False, a.shape[0], k if transposed else n, dev, a.q)
     _check(_fn("moe_gemm_e4m3")(ctypes.byref(av), a.shape[0], ctypes.byref(w._c),
                                 None if offsets is None else _ints(offsets, E + 1, "offsets", dev),
                                 1 if transposed else 0, ctypes.byref(ov), _space(ws, dev), ws.numel(), _stream(dev)),
@@ -271,10 +283,11 @@ def swiglu(gu: torch.Tensor, ws: torch.Tensor, *, total: torch.Tensor | None = N
     number of rows that count (offsets[-1:]). Returns int16 or (e4m3=True) E4m3Rows; `out` gives them."""
     dev = _device(gu, "gu")
     gv = _bf16(gu, None, None, "gu", dev)
-    rows, inter = gu.shape[0], gu.shape[1] // 2
-    if gu.shape[1] % 2:
+    rows, cols = gu.shape
+    inter = cols // 2
+    if cols % 2:
         raise ValueError("gu must have an even number of columns")
-    out, ov = _out(out, e4m3, rows, inter, dev)
+    out, ov = _out(out, e4m3, rows, inter, dev, gu)
     _check(_fn("moe_swiglu")(ctypes.byref(gv), rows, inter, _total(total, dev), ctypes.byref(ov), _space(ws, dev),
                              ws.numel(), _stream(dev)), "moe_swiglu")
     return out
@@ -286,11 +299,12 @@ def swiglu_grad(gu: torch.Tensor, dh: torch.Tensor, ws: torch.Tensor, *, total: 
     result, dh [rows, inter]."""
     dev = _device(gu, "gu")
     gv = _bf16(gu, None, None, "gu", dev)
-    rows, inter = gu.shape[0], gu.shape[1] // 2
-    if gu.shape[1] % 2:
+    rows, cols = gu.shape
+    inter = cols // 2
+    if cols % 2:
         raise ValueError("gu must have an even number of columns")
     hv = _bf16(dh, rows, inter, "dh", dev)
-    out, ov = _out(out, e4m3, rows, 2 * inter, dev)
+    out, ov = _out(out, e4m3, rows, 2 * inter, dev, gu)
     _check(_fn("moe_swiglu_grad")(ctypes.byref(gv), ctypes.byref(hv), rows, inter, _total(total, dev), ctypes.byref(ov),
                                   _space(ws, dev), ws.numel(), _stream(dev)), "moe_swiglu_grad")
     return out
