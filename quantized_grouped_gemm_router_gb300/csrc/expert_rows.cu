@@ -2,8 +2,7 @@
 // gradient, moe_quant_weights. Each reads its rows once and writes its rows once: all are bound by HBM
 // where there are many rows, by launch and one load's latency where there are few.
 //
-// A warp takes pieces of 512 columns, 16 to a lane (two 16-byte loads; 16 codes are one 16-byte store),
-// so that 8 neighbouring lanes hold a block of 128 and find its largest magnitude by three shuffles.
+// A warp takes pieces of 512 columns, 16 to a lane; a block's largest magnitude takes four shuffles.
 #include "attn_ptx.cuh"
 #include "expert_device.cuh"
 
@@ -11,7 +10,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPiece = 512;   // columns of a warp's step, 16 per lane
 
 // kWarps warps of a CTA as rows x warps per row; each warp takes every warps-th piece of its row.
 struct Split {
@@ -41,26 +39,21 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
   }
   if (!__any_sync(~0u, place >= 0)) return;
   for (int piece = warp % warps; piece < p.segments; piece += warps) {
-    const int c = piece * kPiece + lane * 16;
-    const bool mine = c < p.d;
-    uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (mine) load16(p.x, t, c, v);
-    uint4 codes;
-    float scale;
+    uint4 v[2];
+    load_piece(p.x, t, piece, p.d, v);
+    PieceCodes codes;
     if (E4M3) {
       float x[16];
-      bf16x8_to_float(v[0], x);
-      bf16x8_to_float(v[1], x + 8);
-      codes = quantise16(x, &scale);
+      piece_to_float(v, x);
+      codes = quantise_piece(x);
     }
     for (int j = 0; j < p.k; ++j) {
       const int row = __shfl_sync(~0u, place, j);
-      if (row >= 0 && mine) {
-        if (E4M3)
-          store_codes(p.out, row, c, codes, scale);
-        else
-          store_bf16(p.out, row, c, v[0], v[1]);
-      }
+      if (row < 0) continue;
+      if (E4M3)
+        store_codes(p.out, row, piece, p.d, codes);
+      else
+        store_bf16(p.out, row, piece, p.d, v);
     }
   }
 }
@@ -125,38 +118,28 @@ __global__ void __launch_bounds__(512) combine_grad_kernel(const __grid_constant
   const float w = __ldg(p.w + a);
   const uint64_t w2 = pack2(w, w);
   uint64_t dot2[2] = {0, 0};
-  constexpr int kAhead = 2;  // pieces whose loads are in flight together
-  for (int c0 = 0; c0 < p.d; c0 += kAhead * kPiece) {
-    uint4 g[kAhead][2], y[kAhead][2];
+  uint4 g[2], y[2];
+  load_piece(p.ys, place, 0, p.d, y);
+  load_piece(p.dy, t, 0, p.d, g);
+  for (int piece = 0; piece * kPiece < p.d; ++piece) {
+    float x[16];
 #pragma unroll
-    for (int h = 0; h < kAhead; ++h) {
-      const int c = c0 + h * kPiece + lane * 16;
-      g[h][0] = g[h][1] = y[h][0] = y[h][1] = make_uint4(0, 0, 0, 0);
-      if (c < p.d) {
-        load16(p.ys, place, c, y[h]);
-        load16(p.dy, t, c, g[h]);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t gw = word(g[i >> 2], i & 3), yw = word(y[i >> 2], i & 3);
+      const uint64_t g2 = pack2(__uint_as_float(gw << 16), __uint_as_float(gw & 0xFFFF0000u));
+      const uint64_t y2 = pack2(__uint_as_float(yw << 16), __uint_as_float(yw & 0xFFFF0000u));
+      dot2[i & 1] = fma2(g2, y2, dot2[i & 1]);
+      unpack2(mul2(g2, w2), x[2 * i], x[2 * i + 1]);
     }
+    load_piece(p.ys, place, piece + 1, p.d, y);  // zeros past the end
+    load_piece(p.dy, t, piece + 1, p.d, g);
 #pragma unroll
-    for (int h = 0; h < kAhead; ++h) {
-      if (c0 + h * kPiece >= p.d) break;
-      const int c = c0 + h * kPiece + lane * 16;
-      const bool mine = c < p.d;
-      float x[16];
+    for (int i = 0; i < 2; ++i)
+      if (piece_col(piece, i) >= p.d) {  // past the row's end: zeros, not 0 * w (w may be infinite)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t gw = word(g[h][i >> 2], i & 3), yw = word(y[h][i >> 2], i & 3);
-        const uint64_t g2 = pack2(__uint_as_float(gw << 16), __uint_as_float(gw & 0xFFFF0000u));
-        const uint64_t y2 = pack2(__uint_as_float(yw << 16), __uint_as_float(yw & 0xFFFF0000u));
-        dot2[i & 1] = fma2(g2, y2, dot2[i & 1]);
-        unpack2(mul2(g2, w2), x[2 * i], x[2 * i + 1]);
+        for (int u = 0; u < 8; ++u) x[8 * i + u] = 0.f;
       }
-      if (!mine) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = 0.f;  // not 0 * w: w may be infinite
-      }
-      store16<E4M3>(p.dys, place, c, x, mine);
-    }
+    store_piece<E4M3>(p.dys, place, piece, p.d, x);
   }
   float part[4];
   unpack2(dot2[0], part[0], part[1]);
@@ -169,11 +152,11 @@ __global__ void __launch_bounds__(512) combine_grad_kernel(const __grid_constant
 
 // ------------------------------------------------------------------------------------ SwiGLU
 // s = 1 / (1 + e^-g): e^-g to a few units of the last place (its argument's rounding: 2^-17 at |g| of 88);
-// above 2^128 it is infinite and s is 0, as in fp32 arithmetic.
+// below 2^-126 (g < -87.3) s is 0.
 __device__ __forceinline__ float sigmoid(float g) {
   float e, s;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
   return s;
 }
 
@@ -187,29 +170,54 @@ __device__ __forceinline__ int rows_that_count(const SwigluParams& p) {
   return n;
 }
 
+// A warp's way over the pieces of its rows, rows a grid's width apart: the next piece's loads are issued
+// before the present one is worked on.
+struct Walk {
+  int64_t row, step;
+  int piece, warps, pieces, rows;
+  Walk() = default;
+  __device__ __forceinline__ Walk(const SwigluParams& p, int w) {
+    const int warp = threadIdx.x >> 5;
+    warps = w, pieces = p.segments, rows = rows_that_count(p), piece = warp % w;
+    row = (int64_t)blockIdx.x * (kWarps / w) + warp / w, step = (int64_t)gridDim.x * (kWarps / w);
+  }
+  __device__ __forceinline__ bool inside() const { return row < rows; }
+  __device__ __forceinline__ Walk next() const {
+    Walk n = *this;
+    if ((n.piece += warps) >= pieces) n.piece = (threadIdx.x >> 5) % warps, n.row += step;
+    return n;
+  }
+};
+
+// Rows of p from column `first` on.
+__device__ __forceinline__ moe_rows from_col(moe_rows r, int first) {
+  r.p = static_cast<uint16_t*>(r.p) + first;
+  return r;
+}
+
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const __grid_constant__ SwigluParams p, int warps) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = (int64_t)blockIdx.x * (kWarps / warps) + warp / warps;
-  if (t >= rows_that_count(p)) return;
-  for (int piece = warp % warps; piece < p.segments; piece += warps) {
-    const int c = piece * kPiece + lane * 16;
-    const bool mine = c < p.inter;
-    uint4 gv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, uv[2] = {gv[0], gv[0]};
-    if (mine) {
-      load16(p.gu, t, c, gv);
-      load16(p.gu, t, p.inter + c, uv);
-    }
+  const moe_rows up = from_col(p.gu, p.inter);
+  Walk at(p, warps), next;
+  uint4 gv[2], uv[2];
+  if (at.inside()) {
+    load_piece(p.gu, at.row, at.piece, p.inter, gv);
+    load_piece(up, at.row, at.piece, p.inter, uv);
+  }
+  for (; at.inside(); at = next) {
+    next = at.next();
     float g[16], u[16];
-    bf16x8_to_float(gv[0], g);
-    bf16x8_to_float(gv[1], g + 8);
-    bf16x8_to_float(uv[0], u);
-    bf16x8_to_float(uv[1], u + 8);
+    piece_to_float(gv, g);
+    piece_to_float(uv, u);
+    if (next.inside()) {
+      load_piece(p.gu, next.row, next.piece, p.inter, gv);
+      load_piece(up, next.row, next.piece, p.inter, uv);
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i) g[i] = g[i] * sigmoid(g[i]) * u[i];
-    store16<E4M3>(p.out, t, c, g, mine);
+    store_piece<E4M3>(p.out, at.row, at.piece, p.inter, g);
   }
 }
 
@@ -217,12 +225,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const __grid_constant_
 __device__ __forceinline__ void swiglu_grad16(const uint4 (&gv)[2], const uint4 (&uv)[2], const uint4 (&hv)[2],
                                               float (&dg)[16], float (&du)[16]) {
   float g[16], u[16], h[16];
-  bf16x8_to_float(gv[0], g);
-  bf16x8_to_float(gv[1], g + 8);
-  bf16x8_to_float(uv[0], u);
-  bf16x8_to_float(uv[1], u + 8);
-  bf16x8_to_float(hv[0], h);
-  bf16x8_to_float(hv[1], h + 8);
+  piece_to_float(gv, g);
+  piece_to_float(uv, u);
+  piece_to_float(hv, h);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float s = sigmoid(g[i]), hs = h[i] * s;
@@ -238,29 +243,43 @@ template <bool E4M3, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(const __grid_constant__ SwigluParams p, int warps) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = (int64_t)blockIdx.x * (kWarps / warps) + warp / warps;
-  if (t >= rows_that_count(p)) return;
-  for (int piece = warp % warps; piece < p.segments; piece += warps) {
-    const int at = piece * kPiece + lane * 16;               // output column
-    const bool second = !WHOLE && at >= p.inter;             // one of du
-    const int c = second ? at - p.inter : at;
-    const bool mine = c < p.inter;
-    uint4 gv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, uv[2] = {gv[0], gv[0]}, hv[2] = {gv[0], gv[0]};
-    if (mine) {
-      load16(p.gu, t, c, gv);
-      load16(p.dh, t, c, hv);
-      if (!second) load16(p.gu, t, p.inter + c, uv);
+  const moe_rows up = from_col(p.gu, p.inter);
+  moe_rows second = p.out;  // WHOLE: du begins with a block of its own
+  second.p = static_cast<uint8_t*>(second.p) + (E4M3 ? 1 : 2) * p.inter;
+  second.scale += E4M3 ? p.inter / kScaleBlock : 0;
+  uint4 gv[2], uv[2], hv[2];
+  auto load = [&](const Walk& at) {
+    if (WHOLE) {
+      load_piece(p.gu, at.row, at.piece, p.inter, gv);
+      load_piece(p.dh, at.row, at.piece, p.inter, hv);
+      load_piece(up, at.row, at.piece, p.inter, uv);
+      return;
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int o = piece_col(at.piece, h), c = o >= p.inter ? o - p.inter : o;  // output column, its g's
+      gv[h] = uv[h] = hv[h] = make_uint4(0, 0, 0, 0);
+      if (o < 2 * p.inter) {
+        gv[h] = __ldg(bf16_at(p.gu, at.row, c));
+        hv[h] = __ldg(bf16_at(p.dh, at.row, c));
+        if (o < p.inter) uv[h] = __ldg(bf16_at(up, at.row, c));
+      }
+    }
+  };
+  Walk at(p, warps), next;
+  if (at.inside()) load(at);
+  for (; at.inside(); at = next) {
+    next = at.next();
     float dg[16], du[16];
     swiglu_grad16(gv, uv, hv, dg, du);
+    if (next.inside()) load(next);
     if (WHOLE) {
-      store16<E4M3>(p.out, t, c, dg, mine);
-      store16<E4M3>(p.out, t, p.inter + c, du, mine);
+      store_piece<E4M3>(p.out, at.row, at.piece, p.inter, dg);
+      store_piece<E4M3>(second, at.row, at.piece, p.inter, du);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) dg[i] = second ? du[i] : dg[i];
-      store16<E4M3>(p.out, t, at, dg, mine);
+      for (int i = 0; i < 16; ++i) dg[i] = piece_col(at.piece, i >> 3) >= p.inter ? du[i] : dg[i];
+      store_piece<E4M3>(p.out, at.row, at.piece, 2 * p.inter, dg);
     }
   }
 }
@@ -340,7 +359,9 @@ cudaError_t launch_swiglu(SwigluParams p, bool grad, cudaStream_t s) {
   const bool e4m3 = p.out.format == MOE_ROWS_E4M3, whole = p.inter % kScaleBlock == 0;
   p.segments = ((grad && !whole ? 2 * p.inter : p.inter) + kPiece - 1) / kPiece;
   const Split sp = split_of(p.segments);
-  const dim3 grid(grid_of(p.rows, sp.rows));
+  // as many CTAs as the SMs hold at once (by registers), or fewer
+  const int most = sm_count() * (grad ? 3 : 4), need = (int)grid_of(p.rows, sp.rows);
+  const dim3 grid(need < most ? need : most);
   if (!grad)
     return e4m3 ? launch_pdl(swiglu_kernel<true>, grid, kThreads, 0, 1, s, p, sp.warps)
                 : launch_pdl(swiglu_kernel<false>, grid, kThreads, 0, 1, s, p, sp.warps);
