@@ -466,6 +466,7 @@ cudaError_t launch(const ProductParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_product(const ProductParams& p, cudaStream_t s) {
+  if (product_is_small(p)) return launch_product_small(p, s);
   const int64_t tiles = (p.rows + kTileM - 1) / kTileM + (p.n_experts < p.rows ? p.n_experts : p.rows) - 1;
   const bool narrow = tiles * ((p.outc + 255) / 256) < sm_count();
   if (narrow) return p.transposed ? launch<128, true>(p, s) : launch<128, false>(p, s);

@@ -65,38 +65,50 @@ constexpr int kTogether = 8;        // rows whose loads are in flight together
 __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ CombineParams p, int warps) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = (int64_t)blockIdx.x * (kWarps / warps) + warp / warps;
-  if (t >= p.T) return;
-  int place = lane < p.k ? __ldg(p.inv + t * p.k + lane) : -1;
-  if (place >= p.ys_rows) {
-    raise_index(p.hdr);
-    place = -1;
-  }
-  const float weight = place < 0 ? 0.f : p.w ? __ldg(p.w + t * p.k + lane) : 1.f;
-  for (int piece = warp % warps; piece < p.segments; piece += warps) {
-    const int c = piece * kCombinePiece + lane * 8;
-    const bool mine = c < p.d;
-    float acc[8] = {};
-    if (mine && p.add.p) bf16x8_to_float(*bf16_at(p.add, t, c), acc);
-    for (int j0 = 0; j0 < p.k; j0 += kTogether) {
-      uint4 v[kTogether];
-#pragma unroll
-      for (int i = 0; i < kTogether; ++i) {
-        const int row = __shfl_sync(~0u, place, j0 + i);  // lanes from top_k on hold -1
-        v[i] = row >= 0 && mine ? __ldg(bf16_at(p.ys, row, c)) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < kTogether; ++i) {
-        const float w = __shfl_sync(~0u, weight, j0 + i);
-        float x[8];
-        bf16x8_to_float(v[i], x);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) acc[u] = fmaf(w, x[u], acc[u]);
-      }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = gridDim.x * (kWarps / warps);
+  int t = blockIdx.x * (kWarps / warps) + warp / warps;
+  // the places and weights of a token, loaded while the one before is worked on
+  int place = -1;
+  float weight = 1.f;
+  auto load = [&](int t) {
+    if (lane < p.k && t < p.T) {
+      place = __ldg(p.inv + (int64_t)t * p.k + lane);
+      if (p.w) weight = __ldg(p.w + (int64_t)t * p.k + lane);
     }
-    if (mine)
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y.p) + t * p.y.stride + c) = float_to_bf16x8(acc);
+  };
+  load(t);
+  for (; t < p.T; t += step) {
+    if (place >= p.ys_rows) {
+      raise_index(p.hdr);
+      place = -1;
+    }
+    const int now = place;
+    const float w_now = now < 0 ? 0.f : weight;
+    load(t + step);
+    for (int piece = warp % warps; piece < p.segments; piece += warps) {
+      const int c = piece * kCombinePiece + lane * 8;
+      const bool mine = c < p.d;
+      float acc[8] = {};
+      if (mine && p.add.p) bf16x8_to_float(*bf16_at(p.add, t, c), acc);
+      for (int j0 = 0; j0 < p.k; j0 += kTogether) {
+        uint4 v[kTogether];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+          const int row = __shfl_sync(~0u, now, j0 + i);  // lanes from top_k on hold -1
+          v[i] = row >= 0 && mine ? __ldg(bf16_at(p.ys, row, c)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+          const float w = __shfl_sync(~0u, w_now, j0 + i);
+          float x[8];
+          bf16x8_to_float(v[i], x);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) acc[u] = fmaf(w, x[u], acc[u]);
+        }
+      }
+      if (mine)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y.p) + t * p.y.stride + c) = float_to_bf16x8(acc);
+    }
   }
 }
 
@@ -105,49 +117,60 @@ template <bool E4M3>
 __global__ void __launch_bounds__(512) combine_grad_kernel(const __grid_constant__ CombineGradParams p, int tokens) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = (int64_t)blockIdx.x * tokens + warp / p.k;
-  if (t >= p.T) return;
-  const int64_t a = t * p.k + warp % p.k;
-  const int place = __ldg(p.inv + a);
-  if (place >= p.ys_rows && lane == 0) raise_index(p.hdr);
-  if (place < 0 || place >= p.ys_rows) {
-    if (lane == 0) p.dw[a] = 0.f;
-    return;
-  }
-  const float w = __ldg(p.w + a);
-  const uint64_t w2 = pack2(w, w);
-  uint64_t dot2[2] = {0, 0};
-  uint4 g[2], y[2];
-  load_piece(p.ys, place, 0, p.d, y);
-  load_piece(p.dy, t, 0, p.d, g);
-  for (int piece = 0; piece * kPiece < p.d; ++piece) {
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t gw = word(g[i >> 2], i & 3), yw = word(y[i >> 2], i & 3);
-      const uint64_t g2 = pack2(__uint_as_float(gw << 16), __uint_as_float(gw & 0xFFFF0000u));
-      const uint64_t y2 = pack2(__uint_as_float(yw << 16), __uint_as_float(yw & 0xFFFF0000u));
-      dot2[i & 1] = fma2(g2, y2, dot2[i & 1]);
-      unpack2(mul2(g2, w2), x[2 * i], x[2 * i + 1]);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = warp % p.k, step = gridDim.x * tokens;
+  int t = blockIdx.x * tokens + warp / p.k, place = -1;
+  float w = 0.f;
+  auto load = [&](int t) {  // a token's place and weight, loaded while the one before is worked on
+    if (t < p.T) {
+      place = __ldg(p.inv + (int64_t)t * p.k + j);
+      w = __ldg(p.w + (int64_t)t * p.k + j);
     }
-    load_piece(p.ys, place, piece + 1, p.d, y);  // zeros past the end
-    load_piece(p.dy, t, piece + 1, p.d, g);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (piece_col(piece, i) >= p.d) {  // past the row's end: zeros, not 0 * w (w may be infinite)
-#pragma unroll
-        for (int u = 0; u < 8; ++u) x[8 * i + u] = 0.f;
+  };
+  load(t);
+  for (; t < p.T; t += step) {
+    const int now = place;
+    const uint64_t w2 = pack2(w, w);
+    float* dw = p.dw + (int64_t)t * p.k + j;
+    load(t + step);
+    if (now < 0 || now >= p.ys_rows) {
+      if (lane == 0) {
+        if (now >= 0) raise_index(p.hdr);
+        *dw = 0.f;
       }
-    store_piece<E4M3>(p.dys, place, piece, p.d, x);
-  }
-  float part[4];
-  unpack2(dot2[0], part[0], part[1]);
-  unpack2(dot2[1], part[2], part[3]);
-  float dot = (part[0] + part[1]) + (part[2] + part[3]);
+      continue;
+    }
+    uint64_t dot2[2] = {0, 0};
+    uint4 g[2], y[2];
+    load_piece(p.ys, now, 0, p.d, y);
+    load_piece(p.dy, t, 0, p.d, g);
+    for (int piece = 0; piece * kPiece < p.d; ++piece) {
+      float x[16];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
-  if (lane == 0) p.dw[a] = dot;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t gw = word(g[i >> 2], i & 3), yw = word(y[i >> 2], i & 3);
+        const uint64_t g2 = pack2(__uint_as_float(gw << 16), __uint_as_float(gw & 0xFFFF0000u));
+        const uint64_t y2 = pack2(__uint_as_float(yw << 16), __uint_as_float(yw & 0xFFFF0000u));
+        dot2[i & 1] = fma2(g2, y2, dot2[i & 1]);
+        unpack2(mul2(g2, w2), x[2 * i], x[2 * i + 1]);
+      }
+      load_piece(p.ys, now, piece + 1, p.d, y);  // zeros past the end
+      load_piece(p.dy, t, piece + 1, p.d, g);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (piece_col(piece, i) >= p.d) {  // past the row's end: zeros, not 0 * w (w may be infinite)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) x[8 * i + u] = 0.f;
+        }
+      store_piece<E4M3>(p.dys, now, piece, p.d, x);
+    }
+    float part[4];
+    unpack2(dot2[0], part[0], part[1]);
+    unpack2(dot2[1], part[2], part[3]);
+    float dot = (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
+    if (lane == 0) *dw = dot;
+  }
 }
 
 // ------------------------------------------------------------------------------------ SwiGLU
@@ -249,20 +272,20 @@ __global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(const __grid_cons
   second.scale += E4M3 ? p.inter / kScaleBlock : 0;
   uint4 gv[2], uv[2], hv[2];
   auto load = [&](const Walk& at) {
-    if (WHOLE) {
+    if constexpr (WHOLE) {
       load_piece(p.gu, at.row, at.piece, p.inter, gv);
       load_piece(p.dh, at.row, at.piece, p.inter, hv);
       load_piece(up, at.row, at.piece, p.inter, uv);
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int o = piece_col(at.piece, h), c = o >= p.inter ? o - p.inter : o;  // output column, its g's
-      gv[h] = uv[h] = hv[h] = make_uint4(0, 0, 0, 0);
-      if (o < 2 * p.inter) {
-        gv[h] = __ldg(bf16_at(p.gu, at.row, c));
-        hv[h] = __ldg(bf16_at(p.dh, at.row, c));
-        if (o < p.inter) uv[h] = __ldg(bf16_at(up, at.row, c));
+      for (int h = 0; h < 2; ++h) {
+        const int o = piece_col(at.piece, h), c = o >= p.inter ? o - p.inter : o;  // output column, its g's
+        gv[h] = uv[h] = hv[h] = make_uint4(0, 0, 0, 0);
+        if (o < 2 * p.inter) {
+          gv[h] = __ldg(bf16_at(p.gu, at.row, c));
+          hv[h] = __ldg(bf16_at(p.dh, at.row, c));
+          if (o < p.inter) uv[h] = __ldg(bf16_at(up, at.row, c));
+        }
       }
     }
   };
@@ -330,6 +353,11 @@ __global__ void __launch_bounds__(kThreads) quant_weights_kernel(const QuantWeig
 }
 
 unsigned grid_of(int rows, int per) { return (unsigned)((rows + per - 1) / per); }
+// At most as many CTAs as the SMs hold at once, `each` to an SM (by registers).
+dim3 grid_within(int rows, int per, int each) {
+  const unsigned need = grid_of(rows, per), most = (unsigned)(sm_count() * each);
+  return dim3(need < most ? need : most);
+}
 
 }  // namespace
 
@@ -344,12 +372,12 @@ cudaError_t launch_dispatch(DispatchParams p, cudaStream_t s) {
 cudaError_t launch_combine(CombineParams p, cudaStream_t s) {
   p.segments = (p.d + kCombinePiece - 1) / kCombinePiece;
   const Split sp = split_of(p.segments);
-  return launch_pdl(combine_kernel, dim3(grid_of(p.T, sp.rows)), kThreads, 0, 1, s, p, sp.warps);
+  return launch_pdl(combine_kernel, grid_within(p.T, sp.rows, 4), kThreads, 0, 1, s, p, sp.warps);
 }
 
 cudaError_t launch_combine_grad(const CombineGradParams& p, cudaStream_t s) {
   const int tokens = p.k < kWarps ? kWarps / p.k : 1;
-  const dim3 grid(grid_of(p.T, tokens));
+  const dim3 grid = grid_within(p.T, tokens, 1024 / (32 * p.k * tokens));
   return p.dys.format == MOE_ROWS_E4M3
              ? launch_pdl(combine_grad_kernel<true>, grid, 32 * p.k * tokens, 0, 1, s, p, tokens)
              : launch_pdl(combine_grad_kernel<false>, grid, 32 * p.k * tokens, 0, 1, s, p, tokens);
@@ -359,9 +387,7 @@ cudaError_t launch_swiglu(SwigluParams p, bool grad, cudaStream_t s) {
   const bool e4m3 = p.out.format == MOE_ROWS_E4M3, whole = p.inter % kScaleBlock == 0;
   p.segments = ((grad && !whole ? 2 * p.inter : p.inter) + kPiece - 1) / kPiece;
   const Split sp = split_of(p.segments);
-  // as many CTAs as the SMs hold at once (by registers), or fewer
-  const int most = sm_count() * (grad ? 3 : 4), need = (int)grid_of(p.rows, sp.rows);
-  const dim3 grid(need < most ? need : most);
+  const dim3 grid = grid_within(p.rows, sp.rows, grad ? 3 : 4);
   if (!grad)
     return e4m3 ? launch_pdl(swiglu_kernel<true>, grid, kThreads, 0, 1, s, p, sp.warps)
                 : launch_pdl(swiglu_kernel<false>, grid, kThreads, 0, 1, s, p, sp.warps);
