@@ -86,7 +86,7 @@ int moe_dispatch(const moe_rows* x, const int32_t* inv, int32_t T, int32_t top_k
                  int32_t out_rows, void* ws, size_t ws_bytes, moe_stream_t stream) {
   int st = check_assignments(T, top_k, d);
   if (st || (st = check_counts(out_rows))) return st;
-  if (!inv && (top_k != 1 || out_rows < T)) return MOE_ERR_INVALID_ARG;
+  if (T && !inv && (top_k != 1 || out_rows < T)) return MOE_ERR_INVALID_ARG;
   if (!aligned(inv, 4)) return MOE_ERR_MISALIGNED;
   if ((st = check_space(ws, ws_bytes, 1))) return st;
   if (T == 0) return MOE_OK;

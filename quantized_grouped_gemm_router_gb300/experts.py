@@ -79,6 +79,8 @@ class E4m3Rows:
         if q.dtype is not torch.uint8 or q.dim() != 2 or not q.is_cuda or (q.numel() and q.stride(1) != 1):
             raise ValueError("q must be a CUDA tensor of uint8 [rows, columns], the values of a row contiguous")
         rows, cols = q.shape
+        if rows >= _MANY or cols >= _MANY:
+            raise ValueError("rows and columns must be fewer than 2^31")
         if (scale.dtype is not torch.float32 or scale.shape != (rows, _blocks(cols)) or not scale.is_cuda
                 or scale.get_device() != q.get_device() or (scale.shape[1] > 1 and rows and scale.stride(1) != 1)):
             raise ValueError(f"scale must be a float32 tensor [{rows}, {_blocks(cols)}] on q's device, the values of "
@@ -109,7 +111,7 @@ class E4m3Weights:
     def __init__(self, q: torch.Tensor, scale: torch.Tensor):
         _check_dev(q, torch.uint8, "q")
         _check_dev(scale, torch.float32, "scale")
-        if q.dim() != 3 or scale.shape != (q.shape[0], _blocks(q.shape[1]), _blocks(q.shape[2])):
+        if q.dim() != 3 or max(q.shape) >= _MANY or scale.shape != (q.shape[0], _blocks(q.shape[1]), _blocks(q.shape[2])):
             raise ValueError("q must be [n_experts, n, k] and scale [n_experts, ceil(n / 128), ceil(k / 128)]")
         if q.get_device() != scale.get_device():
             raise ValueError("the weights' tensors must be on one device")
@@ -120,7 +122,7 @@ class E4m3Weights:
     def quantise(cls, w: torch.Tensor) -> "E4m3Weights":
         """moe_quant_weights: bf16 matrices int16 [n_experts, n, k] in blocks of 128 x 128."""
         dev = _device(w, "w")
-        if w.dtype is not torch.int16 or w.dim() != 3 or not w.is_contiguous():
+        if w.dtype is not torch.int16 or w.dim() != 3 or not w.is_contiguous() or max(w.shape) >= _MANY:
             raise ValueError("w must be a contiguous int16 tensor [n_experts, n, k]")
         E, n, k = w.shape
         q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
@@ -131,6 +133,7 @@ class E4m3Weights:
 
 
 _I16, _I32, _F32, _U8 = torch.int16, torch.int32, torch.float32, torch.uint8
+_MANY = 1 << 31  # sizes from here on do not fit the library's integers; it refuses smaller ones itself
 
 # The checks below take as few calls into torch as they can: a call on small rows is bound by its host time.
 
@@ -140,7 +143,7 @@ def _bf16(t: torch.Tensor, rows: int | None, cols: int | None, name: str, dev: i
     shape = t.shape
     if t.dtype is _I16 and t.get_device() == dev and len(shape) == 2:
         r, c = shape
-        if (rows is None or r == rows) and (cols is None or c == cols):
+        if (rows is None or r == rows) and (cols is None or c == cols) and r < _MANY and c < _MANY:
             stride, inner = t.stride()
             if inner == 1 or r * c == 0:
                 # the stride of an axis of length one is never used, and torch may give any
@@ -182,7 +185,7 @@ def _floats(t: torch.Tensor, shape, name: str, dev: int) -> int:
 def _places(inv: torch.Tensor, T: int, dev: int) -> tuple[int, int]:
     """The pointer of inv [T, top_k], and top_k."""
     shape = inv.shape
-    if len(shape) != 2 or shape[0] != T:
+    if len(shape) != 2 or shape[0] != T or shape[1] >= _MANY:
         raise ValueError(f"inv must be [{T}, top_k]")
     return _ints(inv, None, "inv", dev), shape[1]
 
@@ -192,6 +195,8 @@ def sort_tokens(ids: torch.Tensor, n_experts: int, ws: torch.Tensor):
     perm [T * top_k] (place -> assignment) and inv [T, top_k] (assignment -> place), int32."""
     dev = _device(ids, "ids")
     p, n, device = _ints(ids, None, "ids", dev), ids.numel(), ids.device
+    if n >= _MANY:
+        raise ValueError("ids must have fewer than 2^31 entries")
     offsets = torch.empty(max(n_experts, 0) + 1, dtype=_I32, device=device)
     perm = torch.empty(n, dtype=_I32, device=device)
     inv = torch.empty_like(ids)

@@ -418,3 +418,293 @@ def test_product(m, ws, counts, n, k, transposed):
     if len(counts) == 1:  # one expert needs no offsets
         b = m.E4m3Rows(a.q[:rows], a.scale[:rows])
         assert torch.equal(m.gemm_e4m3(b, w, None, ws, transposed=transposed), out[:rows])
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["plain", "transposed"])
+@pytest.mark.parametrize("counts,n,k", [([2700], 528, 400), ([2200, 0, 1, 2500], 272, 144), ([5] * 60 + [0] * 900 + [3] * 64, 32, 48),
+                                        ([37, 300], 160, 8336), ([130], 4112, 256), ([1, 700], 2064, 1040)])
+def test_product_many_tiles(m, ws, counts, n, k, transposed):
+    """More row tiles than run together, more items than SMs, many experts, many blocks of inputs."""
+    a, w, offsets, (ref, size) = make_product(m, n + 7 * k, counts, n, k, transposed)
+    got = m.gemm_e4m3(a, w, offsets, ws, transposed=transposed)
+    C.check_product(got, ref, size, C.blocks(n if transposed else k))
+
+
+@pytest.mark.parametrize("counts", [[1], [3, 5], [9], [40, 0, 91]], ids=str)
+@pytest.mark.parametrize("n,k,transposed", [(144, 1040, False), (1040, 144, True), (512, 512, False), (512, 512, True)])
+def test_product_strides(m, ws, counts, n, k, transposed):
+    """Rows and scales inside wider buffers, on every alignment that the call takes: the same bits."""
+    a, w, offsets, _ = make_product(m, 5, counts, n, k, transposed)
+    want = m.gemm_e4m3(a, w, offsets, ws, transposed=transposed)
+    rows, cols = a.shape
+    nb = C.blocks(cols)
+    for pad, spad, sat in ((16, 1, 0), (48, 3, 2), (128, 4, 1), (16, 4 - nb % 4, 0)):
+        q = torch.full((rows, cols + pad), 0x7F, dtype=torch.uint8, device="cuda")
+        s = torch.full((rows, nb + spad + sat), float("nan"), device="cuda")
+        q[:, 16:16 + cols], s[:, sat:sat + nb] = a.q, a.scale
+        b = m.E4m3Rows(q[:, 16:16 + cols], s[:, sat:sat + nb])
+        whole, out = guarded(rows, want.shape[1], 0x7FC0)
+        m.gemm_e4m3(b, w, offsets, ws, transposed=transposed, out=out)
+        assert torch.equal(out, want) and untouched(whole, rows, want.shape[1], 0x7FC0)
+    # the weights' scales on a 4-byte boundary
+    flat = torch.full((w.scale.numel() + 1,), float("nan"), device="cuda")
+    flat[1:] = w.scale.reshape(-1)
+    v = m.E4m3Weights(w.q, flat[1:].view(w.scale.shape))
+    assert torch.equal(m.gemm_e4m3(a, v, offsets, ws, transposed=transposed), want)
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["plain", "transposed"])
+@pytest.mark.parametrize("counts", [[2, 3, 1], [70, 129, 40]], ids=str)
+def test_product_not_finite(m, ws, counts, transposed):
+    """A NaN in a row, a weight or a scale spoils what it belongs to and nothing else."""
+    n, k = 272, 400
+    a, w, offsets, _ = make_product(m, 9, counts, n, k, transposed)
+    want = m.gemm_e4m3(a, w, offsets, ws, transposed=transposed).view(torch.bfloat16)
+    first = counts[0]
+    q, s = a.q.clone(), a.scale.clone()
+    q[1, 17] = 0x7F
+    s[first, -1] = float("inf")
+    got = m.gemm_e4m3(m.E4m3Rows(q, s), w, offsets, ws, transposed=transposed).view(torch.bfloat16)
+    fine = torch.ones(sum(counts), dtype=torch.bool, device="cuda")
+    fine[1] = fine[first] = False
+    assert torch.isnan(got[1]).all() and not torch.isfinite(got[first]).any() and torch.equal(got[fine], want[fine])
+    wq, w_s = w.q.clone(), w.scale.clone()
+    wq[1, 33, 44] = 0x7F
+    w_s[0, 1, 0] = float("nan")
+    got = m.gemm_e4m3(a, m.E4m3Weights(wq, w_s), offsets, ws, transposed=transposed).view(torch.bfloat16)
+    bad = torch.isnan(got)
+    expect = torch.zeros_like(bad)
+    expect[first:first + counts[1], 44 if transposed else 33] = True   # the second expert's column
+    expect[:first, slice(0, 128) if transposed else slice(128, 256)] = True  # the first expert's block of columns
+    assert torch.equal(bad, expect) and torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("rows", [7, 300])
+def test_product_bad_offsets(m, ws, rows):
+    """Offsets outside the rows, descending or not reaching them: reported where they are wrong, rows of experts
+    whose offsets are right computed, nothing outside written."""
+    n, k = 144, 256
+    a, w, _, _ = make_product(m, 11, [rows, 0, 0, 0], n, k, False)
+    one = [m.gemm_e4m3(a, m.E4m3Weights(w.q[e:e + 1], w.scale[e:e + 1]), None, ws) for e in range(4)]
+    for offsets, status, right in (([0, 2, 2, rows + 9, rows + 9], 9, [(0, 0, 2)]), ([-5, 3, 4, 4, rows], 9, [(1, 3, 4), (3, 4, rows)]),
+                                   ([0, 4, 2, 5, 6], 9, []), ([2 ** 31 - 1, -2 ** 31, 5, 5, 5], 9, []),
+                                   ([1, 3, 3, 5, 6], 0, [(0, 1, 3), (2, 3, 5), (3, 5, 6)]), ([rows] * 5, 0, [])):
+        whole, out = guarded(rows, n, 0x7FC0)
+        m.gemm_e4m3(a, w, torch.tensor(offsets, dtype=torch.int32, device="cuda"), ws, out=out)
+        assert m.read_device_status(ws) == status, offsets
+        assert untouched(whole, rows, n, 0x7FC0)
+        for e, lo, hi in right:
+            assert torch.equal(out[lo:hi], one[e][lo:hi]), offsets
+        if status == 0:
+            lo, hi = offsets[0], offsets[-1]
+            assert (out[:lo] == 0x7FC0).all() and (out[hi:] == 0x7FC0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 64])
+def test_product_sums_in_32_bits(m, ws, rows):
+    """Large products that cancel leave the small ones, within a block and across blocks, up to fp32's precision: within
+    a block 2^17.6 beside 2^-4, 22 bits; across blocks 2^18 beside 2^-4."""
+    def run(a, w):
+        k = len(a)
+        code = lambda x: torch.tensor(x).to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+        r = m.E4m3Rows(code([a] * rows).cuda(), torch.ones(rows, C.blocks(k), device="cuda"))
+        v = m.E4m3Weights(code([w] * 16)[None].cuda(), torch.ones(1, 1, C.blocks(k), device="cuda"))
+        return m.gemm_e4m3(r, v, None, ws).view(torch.bfloat16)
+    for k, far in ((128, 31), (128, 127), (1152, 128), (1152, 1151)):
+        a, w = [0.0] * k, [0.0] * k
+        a[0] = w[0] = w[far] = 448.0
+        a[far] = -448.0
+        a[5], w[5] = 0.25, 0.25
+        assert (run(a, w) == 0.0625).all(), (k, far)
+
+
+def test_product_directions_agree(m, ws):
+    """The transposed product on W is the plain one on a copy of W^T."""
+    counts, n, k = [40, 0, 200, 3], 384, 256
+    a, w, offsets, _ = make_product(m, 21, counts, n, k, True)
+    t = m.E4m3Weights(w.q.transpose(1, 2).contiguous(), w.scale.transpose(1, 2).contiguous())
+    assert torch.equal(m.gemm_e4m3(a, w, offsets, ws, transposed=True), m.gemm_e4m3(a, t, offsets, ws))
+
+
+def test_product_same_bits(m):
+    """Calls repeat bit for bit, on any stream, two at once with a workspace each, and from a graph."""
+    for counts, n, k in (([700, 0, 333, 1], 784, 1040), ([1, 2, 0, 1], 528, 2064)):
+        a, w, offsets, _ = make_product(m, 3, counts, n, k, False)
+        spaces = [m.expert_workspace(4) for _ in range(2)]
+        want = m.gemm_e4m3(a, w, offsets, spaces[0])
+        for _ in range(10):
+            assert torch.equal(m.gemm_e4m3(a, w, offsets, spaces[0]), want)
+        torch.cuda.synchronize()
+        streams, outs = [torch.cuda.Stream() for _ in range(2)], [[], []]
+        for _ in range(5):
+            for s, sp, o in zip(streams, spaces, outs):
+                with torch.cuda.stream(s):
+                    o.append(m.gemm_e4m3(a, w, offsets, sp))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, want) for o in outs for x in o)
+        assert all(m.read_device_status(sp) == 0 for sp in spaces)
+
+
+# ------------------------------------------------------------------------------------ long strides
+def test_rows_far_apart(m, ws):
+    """Rows whose distance from the first passes 2^31 values and bytes."""
+    rows, d, n, stride = 140, 256, 144, 1 << 24
+    buf16, buf8 = (torch.empty(rows * stride, dtype=t, device="cuda") for t in (torch.int16, torch.uint8))
+    bufs = torch.empty(rows * stride, dtype=torch.float32, device="cuda")
+
+    def far16(cols):
+        return buf16.as_strided((rows, cols), (stride, 1))
+
+    def far8(cols):
+        return m.E4m3Rows(buf8.as_strided((rows, cols), (stride, 1)), bufs.as_strided((rows, C.blocks(cols)), (stride, 1)))
+
+    x = dev(rand(1, rows, d))
+    inv = torch.arange(rows, dtype=torch.int32, device="cuda").flip(0).view(rows, 1).contiguous()
+    near = m.dispatch(x, inv, ws, e4m3=True)
+    far = m.dispatch(x, inv, ws, out=far8(d))
+    assert torch.equal(far.q, near.q) and torch.equal(far.scale, near.scale)
+    w = m.E4m3Weights.quantise(dev(rand(2, 1, n, d, gain=0.1)))
+    y = m.gemm_e4m3(near, w, None, ws)
+    assert torch.equal(m.gemm_e4m3(far, w, None, ws, out=far16(n)), y)
+    one = torch.ones(rows, 1, device="cuda")
+    back = m.combine(y, inv, one, ws)
+    assert torch.equal(m.combine(far16(n), inv, one, ws), back) and torch.equal(back, y.flip(0))
+    dys, dw = m.combine_grad(back, y, inv, one, ws)
+    far_dys, far_dw = m.combine_grad(back, far16(n), inv, one, ws, out=far8(n))
+    assert torch.equal(dw, far_dw) and torch.equal(far_dys.q, m.dispatch(dys, None, ws, e4m3=True).q)
+    far16(d).copy_(x)
+    assert torch.equal(m.swiglu(far16(d), ws), m.swiglu(x, ws))
+    dh = dev(rand(3, rows, d // 2))
+    assert torch.equal(m.swiglu_grad(far16(d), dh, ws), m.swiglu_grad(x, dh, ws))
+    assert torch.equal(m.dispatch(far16(d), inv, ws), m.dispatch(x, inv, ws))
+
+
+# ------------------------------------------------------------------------------------ together
+class Layer:
+    """A layer of e4m3 experts and its gradients, as a program would run them; every intermediate is kept."""
+
+    def __init__(self, m, E, d, inter, seed):
+        self.m, self.E, self.ws = m, E, m.expert_workspace(E)
+        self.gate_up = m.E4m3Weights.quantise(dev(rand(seed, E, 2 * inter, d, gain=d ** -0.5)))
+        self.down = m.E4m3Weights.quantise(dev(rand(seed + 1, E, d, inter, gain=inter ** -0.5)))
+
+    def forward(self, x, ids, w):
+        m, ws, s = self.m, self.ws, {}
+        s["offsets"], s["perm"], s["inv"] = m.sort_tokens(ids, self.E, ws)
+        s["xs"] = m.dispatch(x, s["inv"], ws, e4m3=True)
+        s["gu"] = m.gemm_e4m3(s["xs"], self.gate_up, s["offsets"], ws)
+        s["h"] = m.swiglu(s["gu"], ws, total=s["offsets"][-1:], e4m3=True)
+        s["ys"] = m.gemm_e4m3(s["h"], self.down, s["offsets"], ws)
+        s["y"] = m.combine(s["ys"], s["inv"], w, ws, add=x)
+        return s
+
+    def backward(self, s, dy, w):
+        m, ws = self.m, self.ws
+        s["dys"], s["dw"] = m.combine_grad(dy, s["ys"], s["inv"], w, ws, e4m3=True)
+        s["dh"] = m.gemm_e4m3(s["dys"], self.down, s["offsets"], ws, transposed=True)
+        s["dgu"] = m.swiglu_grad(s["gu"], s["dh"], ws, total=s["offsets"][-1:], e4m3=True)
+        s["dxs"] = m.gemm_e4m3(s["dgu"], self.gate_up, s["offsets"], ws, transposed=True)
+        s["dx"] = m.dispatch_grad(s["dxs"], s["inv"], ws, add=dy)
+        return s
+
+
+def check_layer(layer, s, x, ids, w, dy):
+    """Every step against 64 bits on what the step before made."""
+    E, T, k = layer.E, *ids.shape
+    offsets, perm, inv = C.sort(ids, E)
+    for name, want in (("offsets", offsets), ("perm", perm), ("inv", inv)):
+        assert torch.equal(s[name].cpu(), want), name
+    n = int(offsets[-1])
+    counts = (offsets[1:] - offsets[:-1]).tolist()
+    q, scale = C.quantise(x[(perm[:n] // k).long()].float())
+    assert C.same_codes(s["xs"].q[:n], q) and torch.equal(s["xs"].scale[:n].cpu(), scale)
+    gate_up, down = (C.weight_values(v.q, v.scale) for v in (layer.gate_up, layer.down))
+
+    def rows(r):
+        return C.code_values(r.q[:n], r.scale[:n])
+
+    def product(got, a, v, weights, transposed, nb):
+        ref, size = C.product(rows(a), weights, counts, transposed)
+        C.check_product(got[:n], ref, size, nb, v)
+
+    d, inter = x.shape[1], down.shape[2]
+    product(s["gu"], s["xs"], "gu", gate_up, False, C.blocks(d))
+    gu = C.values(s["gu"])[:n]
+    E4 = type(s["h"])
+    C.check_rows(E4(s["h"].q[:n], s["h"].scale[:n]), *C.swiglu(gu), "h")
+    product(s["ys"], s["h"], "ys", down, False, C.blocks(inter))
+    ys = torch.zeros(T * k, d).double()
+    ys[:n] = C.values(s["ys"])[:n]
+    C.check_combine(s["y"], *C.combine(ys, inv, w.double(), x.double()), k, "y")
+    there = inv >= 0
+    of, place = there.nonzero()[:, 0], inv[there].long()
+    q, scale = C.quantise(dy.float()[of] * w[there][:, None])
+    assert C.same_codes(s["dys"].q[place], q) and torch.equal(s["dys"].scale[place].cpu(), scale)
+    dw, size = torch.zeros(T, k).double(), torch.zeros(T, k).double()
+    dw[there] = (dy.double()[of] * ys[place]).sum(-1)
+    size[there] = (dy.double()[of] * ys[place]).abs().sum(-1)
+    C.close(s["dw"], dw, ((d + 511) // 512 * 16 + 8) * 2.0 ** -24 * size, "dw")
+    product(s["dh"], s["dys"], "dh", down, True, C.blocks(d))
+    C.check_rows(E4(s["dgu"].q[:n], s["dgu"].scale[:n]), *C.swiglu_grad(gu, C.values(s["dh"])[:n]), "dgu")
+    product(s["dxs"], s["dgu"], "dxs", gate_up, True, C.blocks(2 * inter))
+    dxs = torch.zeros(T * k, d).double()
+    dxs[:n] = C.values(s["dxs"])[:n]
+    C.check_combine(s["dx"], *C.combine(dxs, inv, None, dy.double()), k, "dx")
+
+
+def batch(seed, T, k, E, d):
+    x, dy = rand(seed, T, d), rand(seed + 1, T, d, gain=0.01)
+    ids = some_ids(seed + 2, T, k, E)
+    ids[T - T // 8:] = -1  # padding at the end of the batch
+    return x, dy, ids, torch.softmax(torch.randn(T, k, generator=gen(seed + 3)), -1)
+
+
+@pytest.mark.parametrize("T,k,E,d,inter", [(1, 2, 8, 256, 128), (7, 4, 16, 272, 144), (150, 3, 6, 512, 256), (40, 8, 64, 128, 80)])
+def test_layer(m, T, k, E, d, inter):
+    layer = Layer(m, E, d, inter, seed=T)
+    x, dy, ids, w = batch(T, T, k, E, d)
+    s = layer.backward(layer.forward(dev(x), ids.cuda(), w.cuda()), dev(dy), w.cuda())
+    assert m.read_device_status(layer.ws) == 0
+    check_layer(layer, s, x, ids, w, dy)
+
+
+def test_layer_from_a_graph(m):
+    """Forward and backward captured once, replayed on other inputs: other routing, other absent tokens."""
+    T, k, E, d, inter = 60, 3, 12, 256, 144
+    layer = Layer(m, E, d, inter, seed=1)
+    x, dy, ids, w = (t.cuda() for t in batch(1, T, k, E, d))
+    x, dy = x.view(torch.int16), dy.view(torch.int16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer.backward(layer.forward(x, ids, w), dy, w)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s = layer.backward(layer.forward(x, ids, w), dy, w)
+    for seed in (5, 9):
+        new = batch(seed, T, k, E, d)
+        for to, t in zip((x, dy, ids, w), new):
+            to.copy_(dev(t))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert m.read_device_status(layer.ws) == 0
+        check_layer(layer, s, new[0], new[2], new[3], new[1])
+        eager = layer.backward(layer.forward(x, ids, w), dy, w)
+        for name in ("y", "dx", "dw", "inv"):
+            assert torch.equal(eager[name], s[name]), name
+
+
+def test_no_rows(m, ws):
+    """Nothing to do is nothing done."""
+    x, inv = torch.empty(0, 64, dtype=torch.int16, device="cuda"), torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    w = torch.empty(0, 3, device="cuda")
+    assert m.dispatch(x, inv, ws).shape == (0, 64) and m.dispatch(x, inv, ws, e4m3=True).shape == (0, 64)
+    assert m.combine(x, inv, w, ws).shape == (0, 64)
+    assert m.combine_grad(x, x, inv, w, ws)[1].shape == (0, 3)
+    v = m.E4m3Weights.quantise(dev(rand(0, 2, 32, 64)))
+    offsets = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert m.gemm_e4m3(m.E4m3Rows.empty(0, 64), v, offsets, ws).shape == (0, 32)
+    out = torch.full((5, 32), 0x7FC0, dtype=torch.int16, device="cuda")
+    m.gemm_e4m3(m.dispatch(dev(rand(1, 5, 64)), None, ws, e4m3=True), v, offsets, ws, out=out)  # no expert has rows
+    assert (out == 0x7FC0).all()
