@@ -25,6 +25,7 @@ bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, con
 namespace {
 
 constexpr int kTileM = 128;
+constexpr int kPairRows = 256;  // rows of an expert, on average, from which on CTAs work in pairs
 constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpScale0 = 2, kScaleWarps = 2, kWarpSum0 = 4, kSumWarps = 8;
 constexpr int kThreads = (kWarpSum0 + kSumWarps) * 32;  // 384
 // Registers: 168 a thread at launch; the first four warps give up 96 each, the summing ones take 48 more:
@@ -38,10 +39,13 @@ struct ProductMaps {
   CUtensorMap w;
 };
 
-template <int BN>
+// PAIR: two CTAs of a cluster make 256 rows x BN columns with MMAs that span both; each holds its own 128 rows
+// and half of the columns' weights.
+template <int BN, bool PAIR>
 struct Layout {
-  static constexpr int kABytes = kTileM * 128, kBBytes = BN * 128, kStage = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kABytes = kTileM * 128, kBCols = PAIR ? BN / 2 : BN, kBBytes = kBCols * 128, kStage = kABytes + kBBytes;
+  static constexpr int kItemM = PAIR ? 2 * kTileM : kTileM;  // rows of an item
+  static constexpr int kStages = kBCols == 256 ? 4 : 6;
   static constexpr int bar_off = kStages * kStage;
   static constexpr int n_bars = 2 * kStages + 4 + 2 * kSlots;
   static constexpr int misc_off = bar_off + n_bars * 8;
@@ -57,38 +61,131 @@ struct Layout {
 
 // Four MMAs of K = 32 on a block of 128 inputs under one elected lane; B_STEP: descriptor units (16 bytes)
 // from one K step of B to the next.
-template <int B_STEP>
+#define MOE_MMA_BLOCK(GROUP)                                                                     \
+  asm volatile(                                                                                  \
+      "{\n\t.reg .pred f, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"                         \
+      "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"                                         \
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"                       \
+      "add.s64 b1, %2, %4;\n\tadd.s64 b2, %2, %5;\n\tadd.s64 b3, %2, %6;\n\t"                    \
+      "elect.sync _|e, 0xffffffff;\n\t"                                                          \
+      "@e tcgen05.mma.cta_group::" GROUP ".kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"               \
+      "@e tcgen05.mma.cta_group::" GROUP ".kind::f8f6f4 [%0], a1, b1, %3, t;\n\t"               \
+      "@e tcgen05.mma.cta_group::" GROUP ".kind::f8f6f4 [%0], a2, b2, %3, t;\n\t"               \
+      "@e tcgen05.mma.cta_group::" GROUP ".kind::f8f6f4 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem), \
+      "l"(a), "l"(b), "r"(idesc), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)                  \
+      : "memory")
+template <int B_STEP, bool PAIR>
 __device__ __forceinline__ void mma_block(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+  if constexpr (PAIR)
+    MOE_MMA_BLOCK("2");
+  else
+    MOE_MMA_BLOCK("1");
+}
+#undef MOE_MMA_BLOCK
+// Arrives on the barrier once the MMAs issued so far are done; PAIR: on that of both CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  if constexpr (PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar)
+        : "memory");
+  } else {
+    umma_commit_elect(bar);
+  }
+}
+// The address of a shared-memory location of this CTA in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Waits as mbar_wait for a barrier that threads of the other CTA arrive on, too.
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred f, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-      "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
-      "add.s64 b1, %2, %4;\n\tadd.s64 b2, %2, %5;\n\tadd.s64 b3, %2, %6;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, "
+      "p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
       : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const long long t0 = clock64();
+  while (!try_wait_cluster(bar, parity)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
 }
 // kind::f8f6f4: fp32 accumulator, A and B e4m3; trans_b: B has its N axis contiguous.
 __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N, bool trans_b) {
   return (1u << 4) | (trans_b ? kIdescBMn : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, int c0, int c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
+// Tiled copies; PAIR: the barrier may be the other CTA's (an address in the cluster).
+template <bool PAIR>
+__device__ __forceinline__ void copy_2d(uint32_t dst, const CUtensorMap* m, int c0, int c1, uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
 }
-
-__device__ __forceinline__ void mbar_arrive_elect(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t.reg .b64 st;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar)
-      : "memory");
+template <bool PAIR>
+__device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+  else
+    tma_load_3d(dst, m, c0, c1, c2, bar);
+}
+// One arrival of a warp; PAIR: on a barrier of either CTA. It orders tensor-memory loads alone (they are complete, and
+// fenced, before it), so it need not release other memory to the cluster: .release.cluster takes 1300 cycles here.
+template <bool PAIR>
+__device__ __forceinline__ void arrive_elect(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b64 st;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void alloc_tmem(uint32_t dst, uint32_t cols) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, cols);
+    tmem_relinquish();
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void free_tmem(uint32_t taddr, uint32_t cols) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+  else
+    tmem_dealloc(taddr, cols);
 }
 // Four values of a run of n (zeros behind it), from the i-th on; vec: they are one aligned 16-byte load.
 __device__ __forceinline__ float4 load4(const float* p, int i, int n, int64_t stride, bool vec) {
@@ -132,7 +229,7 @@ __device__ __forceinline__ Range expert_rows(const ProductParams& p, int e) {
 // The i-th item of the work list; first[e]: the first one of expert e, in shared memory. A whole warp calls it.
 // Row tiles of an expert go in groups of kGroupTiles; in a group the column tiles one after the other, each
 // with all row tiles, so that the CTAs at work share both the rows' and the weights' tiles in L2.
-template <int BN>
+template <int BN, int ITEM_M>
 __device__ __forceinline__ Item find_item(const ProductParams& p, const int* first, int col_tiles, int i) {
   const int lane = threadIdx.x & 31;
   int a = 0, b = p.n_experts;  // first[a] <= i < first[b]
@@ -143,7 +240,7 @@ __device__ __forceinline__ Item find_item(const ProductParams& p, const int* fir
     b = min(a + step, b);
   }
   const Range x = expert_rows(p, a);
-  const int rows = x.hi - x.lo, tiles = (rows + kTileM - 1) / kTileM;
+  const int rows = x.hi - x.lo, tiles = (rows + ITEM_M - 1) / ITEM_M;
   int in = i - first[a], base = 0;
   if (tiles > kGroupTiles) {
     const int per = kGroupTiles * col_tiles, group = in / per;
@@ -153,17 +250,27 @@ __device__ __forceinline__ Item find_item(const ProductParams& p, const int* fir
   const int n = min(kGroupTiles, tiles - base);
   const int ct = (int)__fdividef((float)in + 0.5f, (float)n);  // in < 2^13 and n <= 16: never near an integer
   const int rt = base + in - ct * n;
-  return {a, x.lo + rt * kTileM, min(kTileM, rows - rt * kTileM), ct * BN};
+  return {a, x.lo + rt * ITEM_M, min(ITEM_M, rows - rt * ITEM_M), ct * BN};
 }
 
-template <int BN, bool TRANS>
+// The part of an item that this CTA makes: 128 rows of it, or fewer, or none.
+__device__ __forceinline__ Item part_of(Item it, int rank) {
+  it.row0 += rank * kTileM;
+  it.rows = max(0, min(kTileM, it.rows - rank * kTileM));
+  return it;
+}
+__device__ __forceinline__ int box_of(int rows) { return rows > 64 ? 2 : rows > 32 ? 1 : 0; }
+
+template <int BN, bool TRANS, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ ProductParams p, const __grid_constant__ ProductMaps maps) {
-  using L = Layout<BN>;
+  using L = Layout<BN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int rank = PAIR ? blockIdx.x & 1 : 0;  // in the pair; 0 issues the MMAs
+  const int item0 = PAIR ? blockIdx.x >> 1 : blockIdx.x, item_step = PAIR ? gridDim.x >> 1 : gridDim.x;
   const uint32_t bars = base + L::bar_off;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (L::kStages + s); };
@@ -181,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), kSumWarps);
+      mbar_init(acc_empty(b), PAIR ? 2 * kSumWarps : kSumWarps);
     }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(f_full(s), kScaleWarps);
@@ -190,10 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     *s_abort = 0;
     fence_barrier_init();
   }
-  if (warp == kWarpMma) {
-    tmem_alloc(smem_u32(s_tmem), 2 * BN);
-    tmem_relinquish();
+  if (PAIR) {
+    __syncthreads();
+    cluster_sync();  // the other CTA's barriers are ready, too
   }
+  if (warp == kWarpMma) alloc_tmem<PAIR>(smem_u32(s_tmem), 2 * BN);
   if (warp == kWarpCopy && lane < 4) prefetch_tmap(lane < 3 ? &maps.rows[lane] : &maps.w);
   // Everything above touched shared and tensor memory alone; the offsets and rows are read after the
   // predecessor has completed.
@@ -216,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (e < p.n_experts) {
         const Range r = expert_rows(p, e);
         bad |= r.bad;
-        items[i] = (r.hi - r.lo + kTileM - 1) / kTileM * col_tiles;
+        items[i] = (r.hi - r.lo + L::kItemM - 1) / L::kItemM * col_tiles;
       }
       sum += items[i];
     }
@@ -251,28 +359,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ copies
     uint32_t g = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-      const Item it = find_item<BN>(p, first, col_tiles, i);
-      const int box = it.rows > 64 ? 2 : it.rows > 32 ? 1 : 0;
-      const uint32_t bytes = (32u << box) * 128u + L::kBBytes;
+    for (int i = item0; i < n_items && ok; i += item_step) {
+      const Item whole = find_item<BN, L::kItemM>(p, first, col_tiles, i), it = part_of(whole, rank);
+      const int box = box_of(it.rows), col0 = it.col0 + rank * L::kBCols;
+      // what lands in this CTA, or, where a pair's first CTA counts for both, in both
+      uint32_t bytes = ((32u << box) * 128u) + L::kBBytes;
+      if (PAIR) {
+        const int other = part_of(whole, 1).rows;
+        bytes += L::kBBytes + (other > 0 ? (32u << box_of(other)) * 128u : 0u);
+      }
       if (lane == 0)
         for (int kb = 0; kb < kb_n; ++kb, ++g) {
           const int s = g % L::kStages;
           if (!(ok = mbar_wait(empty(s), ((g / L::kStages) & 1) ^ 1, s_abort))) break;
-          const uint32_t a = base + s * L::kStage, b = a + L::kABytes;
-          mbar_arrive_expect_tx(full(s), bytes);
-          tma_load_2d(a, &maps.rows[box], kb * 128, it.row0, full(s));
+          const uint32_t a = base + s * L::kStage, b = a + L::kABytes, bar = PAIR ? in_cta(full(s), 0) : full(s);
+          if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
+          if (it.rows > 0) copy_2d<PAIR>(a, &maps.rows[box], kb * 128, it.row0, bar);
           if (TRANS) {
 #pragma unroll
-            for (int c = 0; c < BN / 128; ++c)
-              tma_load_3d(b + c * 16384, &maps.w, it.col0 + c * 128, kb * 128, it.expert, full(s));
+            for (int c = 0; c < L::kBCols / 128; ++c)
+              copy_3d<PAIR>(b + c * 16384, &maps.w, col0 + c * 128, kb * 128, it.expert, bar);
           } else {
-            tma_load_3d(b, &maps.w, kb * 128, it.col0, it.expert, full(s));
+            copy_3d<PAIR>(b, &maps.w, kb * 128, col0, it.expert, bar);
           }
         }
       ok = __shfl_sync(~0u, ok, 0);
     }
-    if (!ok && lane == 0)  // a wait gave up: the copies in flight land before the CTA ends
+    if (!ok && lane == 0 && rank == 0)  // a wait gave up: the copies in flight land before the CTAs end
       for (int s = 0; s < L::kStages && (int)g - 1 - s >= 0; ++s) {
         const uint32_t h = g - 1 - s;
         const long long t0 = clock64();
@@ -281,26 +394,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issue
-    const uint32_t idesc = idesc_e4m3(kTileM, BN, TRANS);
+    const uint32_t idesc = idesc_e4m3(L::kItemM, BN, TRANS);
     uint32_t g = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x)
+    for (int i = item0; i < n_items && ok && rank == 0; i += item_step)
       for (int kb = 0; kb < kb_n; ++kb, ++g) {
         const int s = g % L::kStages, buf = g & 1;
-        const bool ready = mbar_try_wait(full(s), (g / L::kStages) & 1) & mbar_try_wait(acc_empty(buf), ((g >> 1) & 1) ^ 1);
+        const uint32_t par = (g / L::kStages) & 1, acc_par = ((g >> 1) & 1) ^ 1;
+        const bool ready = PAIR ? try_wait_cluster(full(s), par) & try_wait_cluster(acc_empty(buf), acc_par)
+                                : mbar_try_wait(full(s), par) & mbar_try_wait(acc_empty(buf), acc_par);
         if (!__all_sync(~0u, ready)) {
-          ok = __all_sync(~0u, mbar_wait(full(s), (g / L::kStages) & 1, s_abort)) &&
-               __all_sync(~0u, mbar_wait(acc_empty(buf), ((g >> 1) & 1) ^ 1, s_abort));
+          ok = __all_sync(~0u, PAIR ? wait_cluster(full(s), par, s_abort) : mbar_wait(full(s), par, s_abort)) &&
+               __all_sync(~0u, PAIR ? wait_cluster(acc_empty(buf), acc_par, s_abort) : mbar_wait(acc_empty(buf), acc_par, s_abort));
           if (!ok) break;
         }
         tc_fence_after();
         const uint32_t a = base + s * L::kStage, b = a + L::kABytes;
         if (TRANS)
-          mma_block<32 * 128 / 16>(tmem + buf * BN, sw128_desc(a), sw128_mn_desc(b, 16384), idesc);
+          mma_block<32 * 128 / 16, PAIR>(tmem + buf * BN, sw128_desc(a), sw128_mn_desc(b, 16384), idesc);
         else
-          mma_block<2>(tmem + buf * BN, sw128_desc(a), sw128_desc(b), idesc);
-        umma_commit_elect(empty(s));
-        umma_commit_elect(acc_full(buf));
+          mma_block<2, PAIR>(tmem + buf * BN, sw128_desc(a), sw128_desc(b), idesc);
+        mma_commit<PAIR>(empty(s));
+        mma_commit<PAIR>(acc_full(buf));
       }
     if (!ok && g) {  // a wait gave up: the MMAs in flight end before tensor memory is freed
       const long long t0 = clock64();
@@ -316,12 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r0 = (warp - kWarpScale0) * 64 + lane, w_stride = TRANS ? p.out_blocks : 1;
     uint32_t g = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-      const Item it = find_item<BN>(p, first, col_tiles, i);
+    for (int i = item0; i < n_items && ok; i += item_step) {
+      const Item it = part_of(find_item<BN, L::kItemM>(p, first, col_tiles, i), rank);
       const float *sa[2], *sw[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        sa[h] = p.a.scale + (it.row0 + min(r0 + 32 * h, it.rows - 1)) * p.a.scale_stride;
+        sa[h] = p.a.scale + min(it.row0 + min(r0 + 32 * h, max(it.rows - 1, 0)), p.rows - 1) * p.a.scale_stride;
         const int cb = min((it.col0 + h * (BN / 2)) / kScaleBlock, p.out_blocks - 1);
         sw[h] = p.wscale + (int64_t)it.expert * p.in_blocks * p.out_blocks + (TRANS ? cb : (int64_t)cb * p.in_blocks);
       }
@@ -364,7 +479,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     uint32_t g = 0, q = 0;
-    for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
+    uint32_t acc_free[2];
+    for (int b = 0; b < 2; ++b) acc_free[b] = PAIR ? in_cta(acc_empty(b), 0) : acc_empty(b);
+    for (int i = item0; i < n_items; i += item_step) {
       Item it;
       float acc[kCols];
 #pragma unroll
@@ -380,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           it = {0, __float_as_int(x.x), __float_as_int(x.y), __float_as_int(x.z)};
         }
         __syncwarp();
-        mbar_arrive_elect(f_empty(s));
+        arrive_elect<false>(f_empty(s));
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           if (kb0 + u < kb_n) {
@@ -398,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(taddr + buf * BN + c + 32, v[x ^ 1]);
               } else {
                 tc_fence_before();
-                mbar_arrive_elect(acc_empty(buf));
+                arrive_elect<PAIR>(acc_free[buf]);
               }
 #pragma unroll
               for (int y = 0; y < 32; ++y) acc[c + y] = fmaf(f4[u], v[x][y], acc[c + y]);
@@ -431,19 +548,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---------------------------------------------------------------- tear-down
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // the other CTA arrives on no barrier of this one any more
   if (warp == kWarpMma) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * BN);
+    free_tmem<PAIR>(tmem, 2 * BN);
   }
   if (tid == 0 && *s_abort) set_device_status(p.hdr, MOE_ERR_DEVICE_TIMEOUT);
 }
 
-template <int BN, bool TRANS>
+// Row tiles at most: every expert that has rows has one that is not full, the others are full ones.
+int64_t most_tiles(const ProductParams& p, int tile) {
+  const int hit = p.n_experts < p.rows ? p.n_experts : p.rows;
+  return (p.rows - hit) / tile + hit;
+}
+
+template <int BN, bool TRANS, bool PAIR>
 cudaError_t launch(const ProductParams& p, cudaStream_t s) {
-  using L = Layout<BN>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(product_kernel<BN, TRANS>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::most);
+  using L = Layout<BN, PAIR>;
+  auto kernel = product_kernel<BN, TRANS, PAIR>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::most);
   if (attr != cudaSuccess) return attr;
   ProductMaps maps;
   const cuuint64_t adims[2] = {(cuuint64_t)p.in, (cuuint64_t)p.rows}, astr[1] = {(cuuint64_t)p.a.stride};
@@ -454,23 +578,40 @@ cudaError_t launch(const ProductParams& p, cudaStream_t s) {
   }
   const cuuint64_t wdims[3] = {(cuuint64_t)p.k, (cuuint64_t)p.n, (cuuint64_t)p.n_experts};
   const cuuint64_t wstr[2] = {(cuuint64_t)p.k, (cuuint64_t)p.n * p.k};
-  const cuuint32_t wbox[3] = {128, TRANS ? 128u : (cuuint32_t)BN, 1};
+  const cuuint32_t wbox[3] = {128, TRANS ? 128u : (cuuint32_t)L::kBCols, 1};
   if (!encode_tiled(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.wq, wdims, wstr, wbox, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const int64_t tiles = (p.rows + kTileM - 1) / kTileM + (p.n_experts < p.rows ? p.n_experts : p.rows) - 1;
-  const int64_t items = tiles * ((p.outc + BN - 1) / BN);
-  const int grid = items < sm_count() ? (int)items : sm_count();
-  return launch_pdl(product_kernel<BN, TRANS>, grid, kThreads, (size_t)(L::fixed + (p.n_experts + 1) * 4), 1, s, p, maps);
+  const int64_t items = most_tiles(p, L::kItemM) * ((p.outc + BN - 1) / BN);
+  // As many CTAs as run at once: a pair needs two SMs of one group, so that not every SM may find a partner.
+  static const int at_once = [&] {
+    if (!PAIR) return sm_count();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (sm_count() / 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::most;
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = 2;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+  }();
+  if (at_once < 1) return cudaErrorInvalidConfiguration;
+  const int grid = (items < at_once ? (int)items : at_once) * (PAIR ? 2 : 1);
+  return launch_pdl(kernel, grid, kThreads, (size_t)(L::fixed + (p.n_experts + 1) * 4), PAIR ? 2 : 1, s, p, maps);
 }
 
 }  // namespace
 
 cudaError_t launch_product(const ProductParams& p, cudaStream_t s) {
   if (product_is_small(p)) return launch_product_small(p, s);
-  const int64_t tiles = (p.rows + kTileM - 1) / kTileM + (p.n_experts < p.rows ? p.n_experts : p.rows) - 1;
-  const bool narrow = tiles * ((p.outc + 255) / 256) < sm_count();
-  if (narrow) return p.transposed ? launch<128, true>(p, s) : launch<128, false>(p, s);
-  return p.transposed ? launch<256, true>(p, s) : launch<256, false>(p, s);
+  const bool narrow = most_tiles(p, kTileM) * ((p.outc + 255) / 256) < sm_count();
+  if (narrow) return p.transposed ? launch<128, true, false>(p, s) : launch<128, false, false>(p, s);
+  if (p.rows >= kPairRows * (int64_t)p.n_experts)
+    return p.transposed ? launch<256, true, true>(p, s) : launch<256, false, true>(p, s);
+  return p.transposed ? launch<256, true, false>(p, s) : launch<256, false, false>(p, s);
 }
 
 }  // namespace moe

@@ -430,6 +430,23 @@ def test_product_many_tiles(m, ws, counts, n, k, transposed):
     C.check_product(got, ref, size, C.blocks(n if transposed else k))
 
 
+@pytest.mark.parametrize("transposed", [False, True], ids=["plain", "transposed"])
+@pytest.mark.parametrize("counts,out,cols", [
+    ([2700, 0, 3301], 2064, 144), ([5400], 2064, 1296), ([129, 1, 256, 4700, 40], 4112, 80),        # pairs of CTAs
+    ([130] * 30 + [0, 1, 128, 127, 300] * 2, 1040, 144), ([7] * 200, 400, 272), ([64, 32, 65, 33] * 40, 272, 528)])
+def test_product_wide(m, ws, counts, out, cols, transposed):
+    """More items than SMs: columns 256 at a time, by single CTAs or, where experts have many rows, by pairs."""
+    n, k = (cols, out) if transposed else (out, cols)
+    a, w, offsets, (ref, size) = make_product(m, out + 3 * cols, counts, n, k, transposed)
+    rows = sum(counts)
+    whole, got = guarded(rows, out, 0x7FC0)
+    for _ in range(3):
+        m.gemm_e4m3(a, w, offsets, ws, transposed=transposed, out=got)
+    assert m.read_device_status(ws) == 0
+    C.check_product(got, ref, size, C.blocks(cols))
+    assert untouched(whole, rows, out, 0x7FC0)
+
+
 @pytest.mark.parametrize("counts", [[1], [3, 5], [9], [40, 0, 91]], ids=str)
 @pytest.mark.parametrize("n,k,transposed", [(144, 1040, False), (1040, 144, True), (512, 512, False), (512, 512, True)])
 def test_product_strides(m, ws, counts, n, k, transposed):
