@@ -43,9 +43,12 @@ struct ProductMaps {
 // and half of the columns' weights.
 template <int BN, bool PAIR>
 struct Layout {
-  static constexpr int kABytes = kTileM * 128, kBCols = PAIR ? BN / 2 : BN, kBBytes = kBCols * 128, kStage = kABytes + kBBytes;
+  static constexpr int kABytes = kTileM * 128, kBCols = PAIR ? BN / 2 : BN, kBBytes = kBCols * 128;
   static constexpr int kItemM = PAIR ? 2 * kTileM : kTileM;  // rows of an item
-  static constexpr int kStages = kBCols == 256 ? 4 : 6;
+  // Blocks to a step: what is copied, waited for and handed over together. Tensor memory holds two steps' sums.
+  static constexpr int kStep = BN == 128 ? 2 : 1, kTmemCols = 2 * kStep * BN;
+  static constexpr int kBlock = kABytes + kBBytes, kStage = kStep * kBlock;
+  static constexpr int kStages = 196608 / kStage;
   static constexpr int bar_off = kStages * kStage;
   static constexpr int n_bars = 2 * kStages + 4 + 2 * kSlots;
   static constexpr int misc_off = bar_off + n_bars * 8;
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();  // the other CTA's barriers are ready, too
   }
-  if (warp == kWarpMma) alloc_tmem<PAIR>(smem_u32(s_tmem), 2 * BN);
+  if (warp == kWarpMma) alloc_tmem<PAIR>(smem_u32(s_tmem), L::kTmemCols);
   if (warp == kWarpCopy && lane < 4) prefetch_tmap(lane < 3 ? &maps.rows[lane] : &maps.w);
   // Everything above touched shared and tensor memory alone; the offsets and rows are read after the
   // predecessor has completed.
@@ -369,18 +372,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         bytes += L::kBBytes + (other > 0 ? (32u << box_of(other)) * 128u : 0u);
       }
       if (lane == 0)
-        for (int kb = 0; kb < kb_n; ++kb, ++g) {
+        for (int kb0 = 0; kb0 < kb_n; kb0 += L::kStep, ++g) {
           const int s = g % L::kStages;
           if (!(ok = mbar_wait(empty(s), ((g / L::kStages) & 1) ^ 1, s_abort))) break;
-          const uint32_t a = base + s * L::kStage, b = a + L::kABytes, bar = PAIR ? in_cta(full(s), 0) : full(s);
-          if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
-          if (it.rows > 0) copy_2d<PAIR>(a, &maps.rows[box], kb * 128, it.row0, bar);
-          if (TRANS) {
+          const uint32_t bar = PAIR ? in_cta(full(s), 0) : full(s);
+          if (rank == 0) mbar_arrive_expect_tx(full(s), bytes * min(L::kStep, kb_n - kb0));
 #pragma unroll
-            for (int c = 0; c < L::kBCols / 128; ++c)
-              copy_3d<PAIR>(b + c * 16384, &maps.w, col0 + c * 128, kb * 128, it.expert, bar);
-          } else {
-            copy_3d<PAIR>(b, &maps.w, kb * 128, col0, it.expert, bar);
+          for (int u = 0; u < L::kStep; ++u) {
+            const int kb = kb0 + u;
+            if (kb >= kb_n) break;
+            const uint32_t a = base + s * L::kStage + u * L::kBlock, b = a + L::kABytes;
+            if (it.rows > 0) copy_2d<PAIR>(a, &maps.rows[box], kb * 128, it.row0, bar);
+            if (TRANS) {
+#pragma unroll
+              for (int c = 0; c < L::kBCols / 128; ++c)
+                copy_3d<PAIR>(b + c * 16384, &maps.w, col0 + c * 128, kb * 128, it.expert, bar);
+            } else {
+              copy_3d<PAIR>(b, &maps.w, kb * 128, col0, it.expert, bar);
+            }
           }
         }
       ok = __shfl_sync(~0u, ok, 0);
@@ -398,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t g = 0;
     bool ok = true;
     for (int i = item0; i < n_items && ok && rank == 0; i += item_step)
-      for (int kb = 0; kb < kb_n; ++kb, ++g) {
+      for (int kb = 0; kb < kb_n; kb += L::kStep, ++g) {
         const int s = g % L::kStages, buf = g & 1;
         const uint32_t par = (g / L::kStages) & 1, acc_par = ((g >> 1) & 1) ^ 1;
         const bool ready = PAIR ? try_wait_cluster(full(s), par) & try_wait_cluster(acc_empty(buf), acc_par)
@@ -409,11 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         tc_fence_after();
-        const uint32_t a = base + s * L::kStage, b = a + L::kABytes;
-        if (TRANS)
-          mma_block<32 * 128 / 16, PAIR>(tmem + buf * BN, sw128_desc(a), sw128_mn_desc(b, 16384), idesc);
-        else
-          mma_block<2, PAIR>(tmem + buf * BN, sw128_desc(a), sw128_desc(b), idesc);
+#pragma unroll
+        for (int u = 0; u < L::kStep; ++u) {
+          if (kb + u >= kb_n) break;
+          const uint32_t a = base + s * L::kStage + u * L::kBlock, b = a + L::kABytes, d = tmem + (buf * L::kStep + u) * BN;
+          if (TRANS)
+            mma_block<32 * 128 / 16, PAIR>(d, sw128_desc(a), sw128_mn_desc(b, 16384), idesc);
+          else
+            mma_block<2, PAIR>(d, sw128_desc(a), sw128_desc(b), idesc);
+        }
         mma_commit<PAIR>(empty(s));
         mma_commit<PAIR>(acc_full(buf));
       }
@@ -501,21 +514,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           if (kb0 + u < kb_n) {
-            const int buf = g & 1;
-            wait(acc_full(buf), (g >> 1) & 1);
-            tc_fence_after();
-            ++g;
+            const int buf = g & 1, in_step = u % L::kStep;
+            const uint32_t from = taddr + (buf * L::kStep + in_step) * BN;
+            if (in_step == 0) {
+              wait(acc_full(buf), (g >> 1) & 1);
+              tc_fence_after();
+            }
+            const bool last = in_step == L::kStep - 1 || kb0 + u + 1 == kb_n;  // of the step
             float v[2][32];  // the next 32 columns arrive while these are added
-            tmem_ld32(taddr + buf * BN, v[0]);
+            tmem_ld32(from, v[0]);
 #pragma unroll
             for (int c = 0; c < kCols; c += 32) {
               const int x = c / 32 & 1;
               tmem_wait_ld32(v[x]);
               if (c + 32 < kCols) {
-                tmem_ld32(taddr + buf * BN + c + 32, v[x ^ 1]);
-              } else {
+                tmem_ld32(from + c + 32, v[x ^ 1]);
+              } else if (last) {
                 tc_fence_before();
                 arrive_elect<PAIR>(acc_free[buf]);
+                ++g;
               }
 #pragma unroll
               for (int y = 0; y < 32; ++y) acc[c + y] = fmaf(f4[u], v[x][y], acc[c + y]);
@@ -552,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpMma) {
     __syncwarp();
     tc_fence_after();
-    free_tmem<PAIR>(tmem, 2 * BN);
+    free_tmem<PAIR>(tmem, L::kTmemCols);
   }
   if (tid == 0 && *s_abort) set_device_status(p.hdr, MOE_ERR_DEVICE_TIMEOUT);
 }
