@@ -574,10 +574,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && *s_abort) set_device_status(p.hdr, MOE_ERR_DEVICE_TIMEOUT);
 }
 
-// Row tiles at most: every expert that has rows has one that is not full, the others are full ones.
-int64_t most_tiles(const ProductParams& p, int tile) {
+// Items at most: every expert that has rows has a row tile that is not full, the others are full ones.
+int64_t most_items(const ProductParams& p, int tile, int columns) {
   const int hit = p.n_experts < p.rows ? p.n_experts : p.rows;
-  return (p.rows - hit) / tile + hit;
+  return (int64_t)((p.rows - hit) / tile + hit) * ((p.outc + columns - 1) / columns);
+}
+
+// Pairs that run at once: a pair needs two SMs of one group, so that not every SM may find a partner.
+int most_pairs() {
+  static const int n = [] {
+    using L = Layout<256, true>;
+    auto kernel = product_kernel<256, false, true>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::most) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (sm_count() / 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::most;
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = 2;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+  }();
+  return n;
 }
 
 template <int BN, bool TRANS, bool PAIR>
@@ -598,23 +620,8 @@ cudaError_t launch(const ProductParams& p, cudaStream_t s) {
   const cuuint32_t wbox[3] = {128, TRANS ? 128u : (cuuint32_t)L::kBCols, 1};
   if (!encode_tiled(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.wq, wdims, wstr, wbox, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const int64_t items = most_tiles(p, L::kItemM) * ((p.outc + BN - 1) / BN);
-  // As many CTAs as run at once: a pair needs two SMs of one group, so that not every SM may find a partner.
-  static const int at_once = [&] {
-    if (!PAIR) return sm_count();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (sm_count() / 2));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = L::most;
-    cudaLaunchAttribute a;
-    a.id = cudaLaunchAttributeClusterDimension;
-    a.val.clusterDim.x = 2;
-    a.val.clusterDim.y = a.val.clusterDim.z = 1;
-    cfg.attrs = &a;
-    cfg.numAttrs = 1;
-    int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
-  }();
+  const int64_t items = most_items(p, L::kItemM, BN);
+  const int at_once = PAIR ? most_pairs() : sm_count();
   if (at_once < 1) return cudaErrorInvalidConfiguration;
   const int grid = (items < at_once ? (int)items : at_once) * (PAIR ? 2 : 1);
   return launch_pdl(kernel, grid, kThreads, (size_t)(L::fixed + (p.n_experts + 1) * 4), PAIR ? 2 : 1, s, p, maps);
@@ -624,11 +631,25 @@ cudaError_t launch(const ProductParams& p, cudaStream_t s) {
 
 cudaError_t launch_product(const ProductParams& p, cudaStream_t s) {
   if (product_is_small(p)) return launch_product_small(p, s);
-  const bool narrow = most_tiles(p, kTileM) * ((p.outc + 255) / 256) < sm_count();
-  if (narrow) return p.transposed ? launch<128, true, false>(p, s) : launch<128, false, false>(p, s);
-  if (p.rows >= kPairRows * (int64_t)p.n_experts)
-    return p.transposed ? launch<256, true, true>(p, s) : launch<256, false, true>(p, s);
-  return p.transposed ? launch<256, true, false>(p, s) : launch<256, false, false>(p, s);
+  // Which width: a block of 128 inputs takes 0.25 us in an item of 128 columns, 0.46 in one of 256 and 0.44 in a pair's
+  // 256 x 256, times the rounds of items over the SMs; but L2 hands out 21.6 TB/s at most, 32, 48 and 64 KB to an item
+  // and block (0.0015, 0.0022, 0.0030 us), and rows that begin off 128-byte lines take 1.6 times that. Times in 0.1 ns.
+  // (8192 x 8192 x 8192: 483, 432 and 420 us; 3236 rows of 6896 x 4464: 134, 126, 104; 1195 rows of 8 experts of 2640 x
+  // 3264: 24.5, 32.6 and none.) A pair wants rows for both its CTAs: with 128 rows to an expert it loses a fifth, with 512 5%.
+  const int sms = sm_count();
+  const bool off = p.k % 128 || p.a.stride % 128;
+  auto time = [&](int64_t items, int at_once, int block, int l2) {
+    const int64_t a = (items + at_once - 1) / at_once * block, b = items * l2 * (off ? 16 : 10) / 10;
+    return a > b ? a : b;
+  };
+  const int64_t narrow = time(most_items(p, kTileM, 128), sms, 2500, 15);
+  const int64_t wide = time(most_items(p, kTileM, 256), sms, off ? 5600 : 4600, 22);
+  if (p.rows >= kPairRows * (int64_t)p.n_experts && most_pairs() > 0) {
+    const int64_t pair = time(most_items(p, 2 * kTileM, 256), most_pairs(), p.n_experts == 1 ? 4400 : 4700, 30);
+    if (pair <= wide && pair <= narrow) return p.transposed ? launch<256, true, true>(p, s) : launch<256, false, true>(p, s);
+  }
+  if (wide < narrow) return p.transposed ? launch<256, true, false>(p, s) : launch<256, false, false>(p, s);
+  return p.transposed ? launch<128, true, false>(p, s) : launch<128, false, false>(p, s);
 }
 
 }  // namespace moe

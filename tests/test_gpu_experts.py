@@ -496,15 +496,15 @@ def test_product_not_finite(m, ws, counts, transposed):
     assert torch.equal(bad, expect) and torch.equal(got[~bad], want[~bad])
 
 
-@pytest.mark.parametrize("rows", [7, 300])
-def test_product_bad_offsets(m, ws, rows):
+@pytest.mark.parametrize("rows,k", [(7, 256), (300, 256), (300, 2064)])
+def test_product_bad_offsets(m, ws, rows, k):
     """Offsets outside the rows, descending or not reaching them: reported where they are wrong, rows of experts
     whose offsets are right computed, nothing outside written."""
-    n, k = 144, 256
+    n = 144
     a, w, _, _ = make_product(m, 11, [rows, 0, 0, 0], n, k, False)
     one = [m.gemm_e4m3(a, m.E4m3Weights(w.q[e:e + 1], w.scale[e:e + 1]), None, ws) for e in range(4)]
     for offsets, status, right in (([0, 2, 2, rows + 9, rows + 9], 9, [(0, 0, 2)]), ([-5, 3, 4, 4, rows], 9, [(1, 3, 4), (3, 4, rows)]),
-                                   ([0, 4, 2, 5, 6], 9, []), ([2 ** 31 - 1, -2 ** 31, 5, 5, 5], 9, []),
+                                   ([0, 4, 2, 5, 6], 9, []), ([0, rows, 0, rows, 0], 9, []), ([2 ** 31 - 1, -2 ** 31, 5, 5, 5], 9, []),
                                    ([1, 3, 3, 5, 6], 0, [(0, 1, 3), (2, 3, 5), (3, 5, 6)]), ([rows] * 5, 0, [])):
         whole, out = guarded(rows, n, 0x7FC0)
         m.gemm_e4m3(a, w, torch.tensor(offsets, dtype=torch.int32, device="cuda"), ws, out=out)
