@@ -1,8 +1,8 @@
 // Device helpers of the 8-bit expert kernels: bf16 and e4m3 pieces of rows, quantising.
 #pragma once
 
+#include "attn_ptx.cuh"
 #include "experts.h"
-#include "ptx.cuh"
 
 namespace moe {
 
@@ -82,7 +82,7 @@ struct PieceCodes {
 __device__ __forceinline__ PieceCodes quantise_piece(const float (&x)[16]) {
   float a[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) a[i >> 3] = fmaxf(a[i >> 3], fabsf(x[i]));  // NaN is passed over
+  for (int i = 0; i < 16; i += 2) a[i >> 3] = max3(a[i >> 3], fabsf(x[i]), fabsf(x[i + 1]));  // NaN is passed over
   const bool fine = __all_sync(~0u, fmaxf(a[0], a[1]) < INFINITY);
   if (!fine) {  // rare: an infinity does not count either
     a[0] = a[1] = 0.f;
@@ -103,7 +103,8 @@ __device__ __forceinline__ PieceCodes quantise_piece(const float (&x)[16]) {
   float y[16];
   if (fine) {  // no infinities: the product alone (NaN stays NaN)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(x[i], inv[i >> 3]);
+    for (int i = 0; i < 16; i += 2)
+      unpack2(mul2(pack2(x[i], x[i + 1]), pack2(inv[i >> 3], inv[i >> 3])), y[i], y[i + 1]);
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i) y[i] = coded(x[i], inv[i >> 3]);

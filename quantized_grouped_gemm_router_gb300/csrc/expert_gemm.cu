@@ -16,7 +16,6 @@
 // Transposed weights are read as they lie: their tile has its column axis contiguous (the other "major"
 // of the MMA's B operand), so no second copy of the weights is kept.
 #include "expert_device.cuh"
-#include "attn_ptx.cuh"
 
 namespace moe {
 bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, const void* ptr, const cuuint64_t* dims,

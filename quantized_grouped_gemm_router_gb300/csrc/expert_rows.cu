@@ -3,7 +3,6 @@
 // where there are many rows, by launch and one load's latency where there are few.
 //
 // A warp takes pieces of 512 columns, 16 to a lane; a block's largest magnitude takes four shuffles.
-#include "attn_ptx.cuh"
 #include "expert_device.cuh"
 
 namespace moe {
@@ -22,6 +21,12 @@ inline Split split_of(int pieces) {
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// The i-th pair of values of a piece.
+__device__ __forceinline__ uint64_t pair_of(const uint4 (&v)[2], int i) {
+  const uint32_t w = word(v[i >> 2], i & 3);
+  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
 
 // ------------------------------------------------------------------------------------ dispatch
 template <bool E4M3>
@@ -147,10 +152,8 @@ __global__ void __launch_bounds__(512) combine_grad_kernel(const __grid_constant
       float x[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t gw = word(g[i >> 2], i & 3), yw = word(y[i >> 2], i & 3);
-        const uint64_t g2 = pack2(__uint_as_float(gw << 16), __uint_as_float(gw & 0xFFFF0000u));
-        const uint64_t y2 = pack2(__uint_as_float(yw << 16), __uint_as_float(yw & 0xFFFF0000u));
-        dot2[i & 1] = fma2(g2, y2, dot2[i & 1]);
+        const uint64_t g2 = pair_of(g, i);
+        dot2[i & 1] = fma2(g2, pair_of(y, i), dot2[i & 1]);
         unpack2(mul2(g2, w2), x[2 * i], x[2 * i + 1]);
       }
       load_piece(p.ys, now, piece + 1, p.d, y);  // zeros past the end
@@ -174,15 +177,17 @@ __global__ void __launch_bounds__(512) combine_grad_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------------------------ SwiGLU
-// s = 1 / (1 + e^-g): e^-g to a few units of the last place (its argument's rounding: 2^-17 at |g| of 88);
-// below 2^-126 (g < -87.3) s is 0.
-__device__ __forceinline__ float sigmoid(float g) {
-  float e, s;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
-  return s;
+// s = 1 / (1 + e^-g) of two values: e^-g to a few units of the last place (its argument's rounding: 2^-17 at |g| of
+// 88); below 2^-126 (g < -87.3) s is 0.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+  constexpr float c = -1.4426950408889634f;
+  float x, y, r, s;
+  unpack2(mul2(g, pack2(c, c)), x, y);
+  unpack2(add2(pack2(ex2(x), ex2(y)), pack2(1.f, 1.f)), x, y);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(y));
+  return pack2(r, s);
 }
-
 __device__ __forceinline__ int rows_that_count(const SwigluParams& p) {
   if (!p.total) return p.rows;
   const int n = __ldg(p.total);
@@ -231,31 +236,29 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const __grid_constant_
   }
   for (; at.inside(); at = next) {
     next = at.next();
-    float g[16], u[16];
-    piece_to_float(gv, g);
-    piece_to_float(uv, u);
+    uint64_t g[8], u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = pair_of(gv, i), u[i] = pair_of(uv, i);
     if (next.inside()) {
       load_piece(p.gu, next.row, next.piece, p.inter, gv);
       load_piece(up, next.row, next.piece, p.inter, uv);
     }
+    float h[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) g[i] = g[i] * sigmoid(g[i]) * u[i];
-    store_piece<E4M3>(p.out, at.row, at.piece, p.inter, g);
+    for (int i = 0; i < 8; ++i) unpack2(mul2(mul2(g[i], sigmoid2(g[i])), u[i]), h[2 * i], h[2 * i + 1]);
+    store_piece<E4M3>(p.out, at.row, at.piece, p.inter, h);
   }
 }
 
 // dg and du of 16 columns; either may be left out.
 __device__ __forceinline__ void swiglu_grad16(const uint4 (&gv)[2], const uint4 (&uv)[2], const uint4 (&hv)[2],
                                               float (&dg)[16], float (&du)[16]) {
-  float g[16], u[16], h[16];
-  piece_to_float(gv, g);
-  piece_to_float(uv, u);
-  piece_to_float(hv, h);
+  const uint64_t one = pack2(1.f, 1.f), minus = pack2(-1.f, -1.f);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float s = sigmoid(g[i]), hs = h[i] * s;
-    dg[i] = hs * u[i] * fmaf(g[i], 1.f - s, 1.f);
-    du[i] = hs * g[i];
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t g = pair_of(gv, i), s = sigmoid2(g), hs = mul2(pair_of(hv, i), s);
+    unpack2(mul2(mul2(hs, pair_of(uv, i)), fma2(g, fma2(s, minus, one), one)), dg[2 * i], dg[2 * i + 1]);
+    unpack2(mul2(hs, g), du[2 * i], du[2 * i + 1]);
   }
 }
 
