@@ -535,9 +535,9 @@ MOE_API int moe_attn_decode(const moe_kv_cache* cache, moe_heads_view q, const i
  *     are no work.
  *   - int32 and float arrays need 4-byte alignment, rows 16 bytes, `ws` 128. Outputs do not overlap
  *     inputs.
- *   - Ids, offsets and places are device data. A kernel never follows a bad one out of the buffers it
- *     was given: it skips or clamps it and raises MOE_ERR_BAD_INDEX in `ws`; the rows concerned are
- *     undefined.
+ *   - Ids, offsets, places and totals are device data. A kernel never follows a bad one out of the
+ *     buffers it was given: it skips it (each call below says what that leaves) and raises
+ *     MOE_ERR_BAD_INDEX in `ws`. No place is named twice.
  *   - `ws`: moe_expert_workspace_bytes(n_experts) bytes, zero-filled once before the first call; the
  *     rules of moe_workspace_bytes hold. It does not grow with the number of rows. Results do not
  *     vary from run to run.
@@ -573,8 +573,8 @@ MOE_API int moe_sort_tokens(const int32_t* ids, int32_t n, int32_t n_experts, in
 /*
  * Lays token rows out by place: out[inv[t * top_k + j]] = x[t] for every j with a place (inv >= 0).
  * x: bf16, T rows of d; out: bf16 or e4m3, out_rows rows. inv == NULL (top_k 1): row t goes to row t,
- * which is how rows are quantised. Each x row is read, and quantised, once. Its gradient is
- * moe_combine without weights.
+ * which is how rows are quantised. Each x row is read, and quantised, once. A place of out_rows or more
+ * is skipped (MOE_ERR_BAD_INDEX). Its gradient is moe_combine without weights.
  */
 MOE_API int moe_dispatch(const moe_rows* x, const int32_t* inv, int32_t T, int32_t top_k, int32_t d,
                          const moe_rows* out, int32_t out_rows, void* ws, size_t ws_bytes, moe_stream_t stream);
@@ -582,7 +582,8 @@ MOE_API int moe_dispatch(const moe_rows* x, const int32_t* inv, int32_t T, int32
 /*
  * y[t] = add[t] + sum_j w[t * top_k + j] * ys[inv[t * top_k + j]], over the j with a place, in the order of j.
  * ys: bf16, ys_rows rows of d; w: fp32, NULL for ones; add: bf16 or NULL (the shared expert's rows,
- * or the residual); y: bf16, T rows; y may be add itself. A token without places gives add[t], or 0.
+ * or the residual); y: bf16, T rows; y may be add itself. A token without places gives add[t], or 0. A
+ * place of ys_rows or more counts as none (MOE_ERR_BAD_INDEX).
  */
 MOE_API int moe_combine(const moe_rows* ys, int32_t ys_rows, const int32_t* inv, const float* w, int32_t T,
                         int32_t top_k, int32_t d, const moe_rows* add, const moe_rows* y, void* ws, size_t ws_bytes,
@@ -591,7 +592,8 @@ MOE_API int moe_combine(const moe_rows* ys, int32_t ys_rows, const int32_t* inv,
 /*
  * Gradients of moe_combine (that of add is dy): for p = inv[t * top_k + j] with a place,
  * dys[p] = w[t * top_k + j] * dy[t] and dw[t * top_k + j] = dy[t] . ys[p]; dw is 0 without one.
- * dy, ys: bf16; dys: bf16 or e4m3, ys_rows rows; w, dw: fp32 [T, top_k].
+ * dy, ys: bf16; dys: bf16 or e4m3, ys_rows rows; w, dw: fp32 [T, top_k]. A place of ys_rows or more
+ * counts as none (MOE_ERR_BAD_INDEX).
  */
 MOE_API int moe_combine_grad(const moe_rows* dy, const moe_rows* ys, int32_t ys_rows, const int32_t* inv,
                              const float* w, int32_t T, int32_t top_k, int32_t d, const moe_rows* dys, float* dw,
@@ -613,8 +615,8 @@ MOE_API int moe_quant_weights(const uint16_t* w, int32_t n_experts, int32_t n, i
 
 /*
  * Products of e4m3 rows with their experts' matrices. Rows offsets[e] .. offsets[e + 1] - 1 of a
- * belong to expert e (device int32[n_experts + 1], ascending, at most `rows`; NULL: all rows belong to
- * the one expert, n_experts == 1). transposed == 0: out[p] = W[e] a[p] (a: k columns, out: n);
+ * belong to expert e (device int32[n_experts + 1], ascending from 0 or more to at most `rows`; where they
+ * do not, nothing is written (MOE_ERR_BAD_INDEX); NULL: all rows belong to the one expert, n_experts == 1). transposed == 0: out[p] = W[e] a[p] (a: k columns, out: n);
  * transposed != 0: out[p] = W[e]^T a[p] (a: n columns, out: k), the gradient of the former's
  * inputs on the same codes. out: bf16.
  * The codes' products are summed in fp32 within a block of 128; each block's sum is multiplied by its
@@ -625,7 +627,8 @@ MOE_API int moe_gemm_e4m3(const moe_rows* a, int32_t rows, const moe_e4m3_weight
 
 /*
  * h = silu(g) * u for rows gu = g | u of 2 * inter columns (bf16): h of inter columns, bf16 or e4m3.
- * total: device int32, the number of rows that count (offsets + n_experts, say), NULL for all `rows`.
+ * total: device int32, the number of rows that count (offsets + n_experts, say), NULL for all `rows`; one
+ * outside 0 .. rows counts as the nearer end (MOE_ERR_BAD_INDEX).
  */
 MOE_API int moe_swiglu(const moe_rows* gu, int32_t rows, int32_t inter, const int32_t* total, const moe_rows* h,
                        void* ws, size_t ws_bytes, moe_stream_t stream);

@@ -35,15 +35,14 @@ __device__ __forceinline__ Group find_group(const ProductParams& p, int q, bool 
   if (!p.offsets) return {0, q * kRows, min(kRows, p.rows - q * kRows)};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.n_experts + kThreads - 1) / kThreads, e0 = threadIdx.x * per, e1 = min(e0 + per, p.n_experts);
-  auto range = [&](int e, int& lo, int& hi) {
-    const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
-    lo = min(max(a, 0), p.rows);
-    hi = min(max(b, lo), p.rows);
-    if (report && (a != lo || b != hi)) raise_index(p.hdr);
-    return (hi - lo + kRows - 1) / kRows;
-  };
-  int sum = 0, lo, hi;
-  for (int e = e0; e < e1; ++e) sum += range(e, lo, hi);
+  int sum = 0;
+  bool bad = false;
+  for (int e = e0; e < e1; ++e) {
+    const int lo = __ldg(p.offsets + e), hi = __ldg(p.offsets + e + 1);
+    const bool wrong = lo < 0 || hi < lo || hi > p.rows;
+    bad |= wrong;
+    if (!wrong) sum += (hi - lo + kRows - 1) / kRows;
+  }
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -52,13 +51,14 @@ __device__ __forceinline__ Group find_group(const ProductParams& p, int q, bool 
   }
   if (lane == 31) s_sum[warp] = incl;
   if (threadIdx.x == 0) s_group = {0, 0, 0};
-  __syncthreads();
+  bad = __syncthreads_or(bad);  // then there are no groups at all
+  if (report && bad && threadIdx.x == 0) raise_index(p.hdr);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) q -= w < warp ? s_sum[w] : 0;
   q -= incl - sum;
-  if (q >= 0 && q < sum)
+  if (!bad && q >= 0 && q < sum)
     for (int e = e0; e < e1; ++e) {
-      const int n = range(e, lo, hi);
+      const int lo = __ldg(p.offsets + e), hi = __ldg(p.offsets + e + 1), n = (hi - lo + kRows - 1) / kRows;
       if (q >= 0 && q < n) s_group = {e, lo + q * kRows, min(kRows, hi - lo - q * kRows)};
       q -= n;
     }

@@ -498,23 +498,26 @@ def test_product_not_finite(m, ws, counts, transposed):
 
 @pytest.mark.parametrize("rows,k", [(7, 256), (300, 256), (300, 2064)])
 def test_product_bad_offsets(m, ws, rows, k):
-    """Offsets outside the rows, descending or not reaching them: reported where they are wrong, rows of experts
-    whose offsets are right computed, nothing outside written."""
+    """Offsets outside the rows or descending: reported, and nothing written. Offsets that begin late or end early
+    leave the rows around them as they were."""
     n = 144
     a, w, _, _ = make_product(m, 11, [rows, 0, 0, 0], n, k, False)
     one = [m.gemm_e4m3(a, m.E4m3Weights(w.q[e:e + 1], w.scale[e:e + 1]), None, ws) for e in range(4)]
-    for offsets, status, right in (([0, 2, 2, rows + 9, rows + 9], 9, [(0, 0, 2)]), ([-5, 3, 4, 4, rows], 9, [(1, 3, 4), (3, 4, rows)]),
-                                   ([0, 4, 2, 5, 6], 9, []), ([0, rows, 0, rows, 0], 9, []), ([2 ** 31 - 1, -2 ** 31, 5, 5, 5], 9, []),
-                                   ([1, 3, 3, 5, 6], 0, [(0, 1, 3), (2, 3, 5), (3, 5, 6)]), ([rows] * 5, 0, [])):
+    for offsets in ([0, 2, 2, rows + 1, rows + 1], [-5, 3, 4, 4, rows], [0, 4, 2, 5, 6], [0, rows, 0, rows, 0],
+                    [2 ** 31 - 1, -2 ** 31, 5, 5, 5], [-1] * 5, [0, 0, 0, 0, 2 ** 31 - 1]):
         whole, out = guarded(rows, n, 0x7FC0)
         m.gemm_e4m3(a, w, torch.tensor(offsets, dtype=torch.int32, device="cuda"), ws, out=out)
-        assert m.read_device_status(ws) == status, offsets
+        assert m.read_device_status(ws) == 9, offsets
+        assert (whole == 0x7FC0).all()
+    for offsets in ([1, 3, 3, 5, 6], [rows] * 5, [0] * 5, [0, 0, 2, 2, 2], [0, 1, 2, 3, rows]):
+        whole, out = guarded(rows, n, 0x7FC0)
+        m.gemm_e4m3(a, w, torch.tensor(offsets, dtype=torch.int32, device="cuda"), ws, out=out)
+        assert m.read_device_status(ws) == 0, offsets
         assert untouched(whole, rows, n, 0x7FC0)
-        for e, lo, hi in right:
+        for e in range(4):
+            lo, hi = offsets[e:e + 2]
             assert torch.equal(out[lo:hi], one[e][lo:hi]), offsets
-        if status == 0:
-            lo, hi = offsets[0], offsets[-1]
-            assert (out[:lo] == 0x7FC0).all() and (out[hi:] == 0x7FC0).all()
+        assert (out[:offsets[0]] == 0x7FC0).all() and (out[offsets[-1]:] == 0x7FC0).all()
 
 
 @pytest.mark.parametrize("rows", [1, 64])
