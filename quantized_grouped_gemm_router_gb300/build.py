@@ -2,7 +2,8 @@
 
 Each translation unit under csrc/ is compiled in parallel with nvcc, then linked into
 _lib/libmoe_gb300.so with a static CUDA runtime so the library loads on a machine without a
-GPU (the C ABI can then be inspected; compute calls report a CUDA error).
+GPU (the C ABI can then be inspected; compute calls report a CUDA error). The CPython module of the
+8-bit expert calls (csrc/py_experts.c) is built beside it with the host's C compiler.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -18,6 +20,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe_gb300.so")
+MODULE_SOURCE = os.path.join(CSRC, "py_experts.c")
+MODULE_PATH = os.path.join(HERE, "_experts" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -74,7 +78,23 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stderr}")
         os.replace(tmp, LIB_PATH)
+    if force or _stale(MODULE_PATH, [MODULE_SOURCE] + deps):
+        _build_module()
     return LIB_PATH
+
+
+def _build_module() -> None:
+    """The CPython module of the 8-bit expert calls, linked to the library beside it."""
+    cc = shutil.which("cc") or shutil.which("gcc")
+    if not cc:
+        raise RuntimeError("a C compiler is required to build the _experts module")
+    tmp = MODULE_PATH + ".tmp"
+    cmd = [cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", f"-I{sysconfig.get_paths()['include']}", MODULE_SOURCE, "-o", tmp,
+           f"-L{LIB_DIR}", "-lmoe_gb300", "-Wl,-rpath,$ORIGIN/_lib"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"cc failed on {os.path.basename(MODULE_SOURCE)}:\n{res.stderr}")
+    os.replace(tmp, MODULE_PATH)
 
 
 if __name__ == "__main__":

@@ -19,19 +19,44 @@ def m():
     return mod
 
 
+class RowsC(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("p", ctypes.c_void_p), ("stride", ctypes.c_int64), ("scale", ctypes.c_void_p),
+                ("scale_stride", ctypes.c_int64)]
+
+
+class WeightsC(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("n_experts", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("k", ctypes.c_int32)]
+
+
 @pytest.fixture(scope="module")
 def fn(m):
-    from quantized_grouped_gemm_router_gb300 import experts
-    return experts._fn
+    """The C entry points, with their argument types."""
+    i32, vp, rows, weights = ctypes.c_int32, ctypes.c_void_p, ctypes.POINTER(RowsC), ctypes.POINTER(WeightsC)
+    end = [vp, ctypes.c_size_t, vp]  # workspace, its size, stream
+    types = {
+        "moe_sort_tokens": [vp, i32, i32, vp, vp, vp] + end,
+        "moe_dispatch": [rows, vp, i32, i32, i32, rows, i32] + end,
+        "moe_combine": [rows, i32, vp, vp, i32, i32, i32, rows, rows] + end,
+        "moe_combine_grad": [rows, rows, i32, vp, vp, i32, i32, i32, rows, vp] + end,
+        "moe_quant_weights": [vp, i32, i32, i32, vp, vp, vp],
+        "moe_gemm_e4m3": [rows, i32, weights, vp, i32, rows] + end,
+        "moe_swiglu": [rows, i32, i32, vp, rows] + end,
+        "moe_swiglu_grad": [rows, rows, i32, i32, vp, rows] + end,
+    }
+
+    def get(name):
+        f = getattr(m.lib(), name)
+        f.argtypes, f.restype = types[name], ctypes.c_int
+        return f
+    return get
 
 
 def bf16(p=A, stride=64, **kw):
-    from quantized_grouped_gemm_router_gb300.experts import RowsC
     return RowsC(kw.get("format", 0), p, stride, None, 0)
 
 
 def e4m3(p=A, stride=64, scale=A, scale_stride=1):
-    from quantized_grouped_gemm_router_gb300.experts import RowsC
     return RowsC(1, p, stride, scale, scale_stride)
 
 
@@ -133,7 +158,6 @@ def test_weights_refusals(m, fn):
 
 
 def test_product_refusals(m, fn):
-    from quantized_grouped_gemm_router_gb300.experts import WeightsC
     need = m.expert_workspace_bytes(4)
 
     def call(a=e4m3(), rows=9, w=None, offsets=A, transposed=0, out=bf16(), ws=A, size=need, **kw):
@@ -193,73 +217,114 @@ def place(t, dev):
 
 
 def calls(m):
-    """name -> (call, its tensors)"""
+    """(name, call, its tensors). Every workspace is too small, so that the library refuses what reaches it."""
     i16, i32, u8, f32 = torch.int16, torch.int32, torch.uint8, torch.float32
 
     def z(*shape, dtype=i16):
         return torch.zeros(*shape, dtype=dtype)
 
-    ws, inv, w = z(256, dtype=u8), z(3, 2, dtype=i32), z(3, 2, dtype=f32)
+    ws, inv, w = z(16, dtype=u8), z(3, 2, dtype=i32), z(3, 2, dtype=f32)
     rows = lambda n: dict(q=z(n, 32, dtype=u8), s=z(n, 1, dtype=f32))  # noqa: E731
     e = lambda t: m.E4m3Rows(t["q"], t["s"])  # noqa: E731
     wt = dict(wq=z(2, 32, 32, dtype=u8), wsc=z(2, 1, 1, dtype=f32))
-    return {
-        "moe_sort_tokens": (lambda t: m.sort_tokens(t["ids"], 4, t["ws"]), dict(ids=z(3, 2, dtype=i32), ws=ws)),
-        "moe_dispatch": (lambda t: m.dispatch(t["x"], t["inv"], t["ws"], out=t["out"]),
-                         dict(x=z(3, 32), inv=inv, ws=ws, out=z(6, 32))),
-        "moe_dispatch ": (lambda t: m.dispatch(t["x"], t["inv"], t["ws"], out=e(t)),
-                          dict(x=z(3, 32), inv=inv, ws=ws, **rows(6))),
-        "moe_combine": (lambda t: m.combine(t["ys"], t["inv"], t["w"], t["ws"], add=t["add"], y=t["y"]),
-                        dict(ys=z(6, 32), inv=inv, w=w, ws=ws, add=z(3, 32), y=z(3, 32))),
-        "moe_combine_grad": (lambda t: m.combine_grad(t["dy"], t["ys"], t["inv"], t["w"], t["ws"], out=t["out"], dw=t["dw"]),
-                             dict(dy=z(3, 32), ys=z(6, 32), inv=inv, w=w, ws=ws, out=z(6, 32), dw=w.clone())),
-        "moe_gemm_e4m3": (lambda t: m.gemm_e4m3(e(t), m.E4m3Weights(t["wq"], t["wsc"]), t["offsets"], t["ws"], out=t["out"]),
-                          dict(offsets=z(3, dtype=i32), ws=ws, out=z(6, 32), **rows(6), **wt)),
-        "moe_swiglu": (lambda t: m.swiglu(t["gu"], t["ws"], total=t["total"], out=t["out"]),
-                       dict(gu=z(3, 64), ws=ws, total=z(1, dtype=i32), out=z(3, 32))),
-        "moe_swiglu_grad": (lambda t: m.swiglu_grad(t["gu"], t["dh"], t["ws"], total=t["total"], out=t["out"]),
-                            dict(gu=z(3, 64), dh=z(3, 32), ws=ws, total=z(1, dtype=i32), out=z(3, 64))),
-    }
+    return [
+        ("sort", lambda t: m.sort_tokens(t["ids"], 4, t["ws"]), dict(ids=z(3, 2, dtype=i32), ws=ws)),
+        ("dispatch", lambda t: m.dispatch(t["x"], t["inv"], t["ws"], out=t["out"]), dict(x=z(3, 32), inv=inv, ws=ws, out=z(6, 32))),
+        ("dispatch", lambda t: m.dispatch(t["x"], t["inv"], t["ws"], out=e(t)), dict(x=z(3, 32), inv=inv, ws=ws, **rows(6))),
+        ("combine", lambda t: m.combine(t["ys"], t["inv"], t["w"], t["ws"], add=t["add"], y=t["y"]),
+         dict(ys=z(6, 32), inv=inv, w=w, ws=ws, add=z(3, 32), y=z(3, 32))),
+        ("dispatch_grad", lambda t: m.dispatch_grad(t["ys"], t["inv"], t["ws"], add=t["add"], dx=t["y"]),
+         dict(ys=z(6, 32), inv=inv, ws=ws, add=z(3, 32), y=z(3, 32))),
+        ("combine_grad", lambda t: m.combine_grad(t["dy"], t["ys"], t["inv"], t["w"], t["ws"], out=t["out"], dw=t["dw"]),
+         dict(dy=z(3, 32), ys=z(6, 32), inv=inv, w=w, ws=ws, out=z(6, 32), dw=w.clone())),
+        ("gemm", lambda t: m.gemm_e4m3(e(t), m.E4m3Weights(t["wq"], t["wsc"]), t["offsets"], t["ws"], out=t["out"]),
+         dict(offsets=z(3, dtype=i32), ws=ws, out=z(6, 32), **rows(6), **wt)),
+        ("swiglu", lambda t: m.swiglu(t["gu"], t["ws"], total=t["total"], out=t["out"]),
+         dict(gu=z(3, 64), ws=ws, total=z(1, dtype=i32), out=z(3, 32))),
+        ("swiglu_grad", lambda t: m.swiglu_grad(t["gu"], t["dh"], t["ws"], total=t["total"], out=t["out"]),
+         dict(gu=z(3, 64), dh=z(3, 32), ws=ws, total=z(1, dtype=i32), out=z(3, 64))),
+    ]
 
 
-def test_binding_refuses_other_devices(m, monkeypatch):
-    """Every tensor of a call lies on the current device; else nothing reaches the library."""
-    from quantized_grouped_gemm_router_gb300 import experts
-    reached = []
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current, raising=False)
+@pytest.fixture
+def on_device(monkeypatch):
+    """Sets the device that torch says is current."""
+    at = {}
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: at["device"], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
-    monkeypatch.setattr(experts, "_fn", lambda name: lambda *a: reached.append(name) or 0)
-    host = torch.empty
-    monkeypatch.setattr(experts.torch, "empty", lambda *a, device=None, **kw: place(host(*a, **kw), device.place if
-                        isinstance(device, Placed) else current))
-    for name, (call, tensors) in calls(m).items():
+    made, like = torch.empty, torch.empty_like
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: place(made(*a, **kw), at["device"]))
+    monkeypatch.setattr(torch, "empty_like", lambda t: place(like(t.as_subclass(torch.Tensor)), at["device"]))
+
+    def set_device(dev):
+        at["device"] = dev
+    return set_device
+
+
+def reaches(m, call, tensors):
+    """The binding accepts the call: the library refuses its workspace, which is too small or not aligned."""
+    with pytest.raises(m.MoeError) as e:
+        call(tensors)
+    return e.value.code in (3, 4)
+
+
+def test_binding_refuses_other_devices(m, on_device):
+    """Every tensor of a call lies on the current device; else nothing reaches the library."""
+    for name, call, tensors in calls(m):
         for current in (0, 1):
-            call({n: place(t, current) for n, t in tensors.items()})
-            assert reached.pop() == name.strip()
+            on_device(current)
+            assert reaches(m, call, {n: place(t, current) for n, t in tensors.items()}), name
             for odd in tensors:
                 with pytest.raises(ValueError):
                     call({n: place(t, 1 - current if n == odd else current) for n, t in tensors.items()})
-                assert not reached, (name, odd)
+            with pytest.raises(ValueError):
+                call({n: place(t, 1 - current) for n, t in tensors.items()})
 
 
-def test_binding_refuses_wrong_tensors(m, monkeypatch):
+def test_binding_refuses_wrong_tensors(m, on_device):
     """Types, shapes and layouts that the library could not tell."""
-    from quantized_grouped_gemm_router_gb300 import experts
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
-    monkeypatch.setattr(experts, "_fn", lambda name: lambda *a: pytest.fail(f"{name} was reached"))
-    for name, (call, tensors) in calls(m).items():
+    on_device(0)
+    for name, call, tensors in calls(m):
         for n, t in tensors.items():
-            wrong = [t.to(torch.float64)]
-            if t.dim() == 2 and n not in ("x", "gu", "ids") and (name, n) not in (("moe_dispatch", "out"), ("moe_combine", "ys")):
+            wrong = [t.to(torch.float64), "rows", 3]
+            if n not in ("ids", "offsets", "total"):  # these count, whatever their axes
+                wrong += [t[None]]
+            if t.dim() == 2 and n not in ("x", "gu", "ids") and (name, n) not in (("dispatch", "out"), ("combine", "ys"),
+                                                                                  ("dispatch_grad", "ys")):
                 wrong += [torch.zeros(t.shape[0] + 1, t.shape[1], dtype=t.dtype)]
             if t.dim() == 2 and t.shape[1] > 1:
                 wrong += [torch.zeros(t.shape[1], t.shape[0], dtype=t.dtype).t()]
             if n in ("offsets", "total"):
                 wrong += [torch.zeros(t.numel() + 1, dtype=t.dtype)]
             for x in wrong:
+                bad = {k: place(x if k == n else v, 0) if isinstance(x if k == n else v, torch.Tensor) else x
+                       for k, v in tensors.items()}
                 with pytest.raises(ValueError):
-                    call({k: place(x if k == n else v, 0) for k, v in tensors.items()})
+                    call(bad)
+        for n in ("inv", "ws", "ids", "gu", "dh", "dy", "ys", "x"):  # what has no default
+            if n in tensors:
+                if name == "dispatch" and n == "inv":
+                    continue  # no places: a row each
+                with pytest.raises(ValueError):
+                    call({k: None if k == n else place(v, 0) for k, v in tensors.items()})
+
+
+def test_binding_makes_outputs(m, on_device):
+    """Outputs that are not given are made, of the right kind, before the library is called."""
+    on_device(0)
+    p = lambda *shape, dtype=torch.int16: place(torch.zeros(*shape, dtype=dtype), 0)  # noqa: E731
+    ws, inv, w = p(16, dtype=torch.uint8), p(3, 2, dtype=torch.int32), p(3, 2, dtype=torch.float32)
+    for e in (False, True):
+        for call in (lambda: m.dispatch(p(3, 32), inv, ws, e4m3=e), lambda: m.dispatch(p(3, 32), None, ws, e4m3=e),
+                     lambda: m.combine_grad(p(3, 32), p(6, 32), inv, w, ws, e4m3=e), lambda: m.swiglu(p(3, 64), ws, e4m3=e),
+                     lambda: m.swiglu_grad(p(3, 64), p(3, 32), ws, e4m3=e)):
+            assert reaches(m, lambda _: call(), None)
+    assert reaches(m, lambda _: m.combine(p(6, 32), inv, None, ws), None)
+    with pytest.raises(m.MoeError):  # k = 8 is not a multiple of 16
+        m.E4m3Weights.quantise(p(1, 16, 8))
+    for n_experts in (-1, 1 << 31, 1 << 40):
+        with pytest.raises(m.MoeError):
+            m.sort_tokens(inv, n_experts, ws)
 
 
 def test_binding_refuses_host_tensors(m):
@@ -269,6 +334,6 @@ def test_binding_refuses_host_tensors(m):
                  lambda: m.E4m3Rows(torch.zeros(3, 32, dtype=torch.uint8), torch.zeros(3, 1)),
                  lambda: m.E4m3Weights(torch.zeros(1, 32, 32, dtype=torch.uint8), torch.zeros(1, 1, 1)),
                  lambda: m.E4m3Weights.quantise(torch.zeros(1, 32, 32, dtype=torch.int16)),
-                 lambda: m.gemm_e4m3(x, x, None, ws)):
+                 lambda: m.gemm_e4m3(x, x, None, ws), lambda: m.E4m3Rows(x, x), lambda: m.E4m3Weights(None, None)):
         with pytest.raises(ValueError):
             call()
