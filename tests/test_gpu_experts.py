@@ -728,3 +728,33 @@ def test_no_rows(m, ws):
     out = torch.full((5, 32), 0x7FC0, dtype=torch.int16, device="cuda")
     m.gemm_e4m3(m.dispatch(dev(rand(1, 5, 64)), None, ws, e4m3=True), v, offsets, ws, out=out)  # no expert has rows
     assert (out == 0x7FC0).all()
+
+
+# ------------------------------------------------------------------------------------ the widest rows
+@pytest.mark.parametrize("n,k,rows", [(16, 65536, 3), (16, 65536, 40), (65536, 16, 5), (65536, 48, 200), (32, 65520, 129)])
+def test_product_widest(m, ws, n, k, rows):
+    for transposed in (False, True):
+        a, w, offsets, (ref, size) = make_product(m, 1, [rows], n, k, transposed)
+        got = m.gemm_e4m3(a, w, None, ws, transposed=transposed)
+        C.check_product(got, ref, size, C.blocks(n if transposed else k))
+
+
+def test_rows_widest(m, ws):
+    d = 65536
+    x, inv = rand(1, 2, d), torch.tensor([[1, 2], [0, -1]], dtype=torch.int32)
+    rows = m.dispatch(dev(x), inv.cuda(), ws, e4m3=True)
+    q, scale = C.quantise(x.float()[[1, 0, 0]])
+    assert C.same_codes(rows.q[:3], q) and torch.equal(rows.scale[:3].cpu(), scale)
+    ys = rand(2, 4, d)
+    w = torch.tensor([[0.5, 2.0], [1.5, 9.0]])
+    y = m.combine(dev(ys), inv.cuda(), w.cuda(), ws)
+    C.check_combine(y, *C.combine(ys.double(), inv, w.double(), None), 2)
+    dys, dw = m.combine_grad(dev(x), dev(ys), inv.cuda(), w.cuda(), ws)
+    assert torch.equal(dys[:3].cpu(), C.bits(x.float()[[1, 0, 0]] * torch.tensor([[1.5], [0.5], [2.0]])))
+    ref = torch.stack([x[0].double() @ ys[1].double(), x[0].double() @ ys[2].double(), x[1].double() @ ys[0].double()])
+    size = torch.stack([x[0].double().abs() @ ys[1].double().abs(), x[0].double().abs() @ ys[2].double().abs(),
+                        x[1].double().abs() @ ys[0].double().abs()])
+    C.close(dw.reshape(-1)[:3], ref, (d // 512 * 16 + 8) * 2.0 ** -24 * size)
+    gu, dh = rand(3, 2, d, gain=2.0), rand(4, 2, d // 2)
+    C.check_rows(m.swiglu(dev(gu), ws, e4m3=True), *C.swiglu(gu.double()))
+    C.check_rows(m.swiglu_grad(dev(gu), dev(dh), ws, e4m3=True), *C.swiglu_grad(gu.double(), dh.double()))
