@@ -16,12 +16,13 @@
 // Transposed weights are read as they lie: their tile has its column axis contiguous (the other "major"
 // of the MMA's B operand), so no second copy of the weights is kept.
 //
-// What bounds it. Many rows: a block of 256 columns takes 0.45 us where its MMAs take 0.26 (at 1.95 GHz): the
-// scaling is 32768 FMAs a block, 256 cycles of the FMA pipes, behind a barrier, a tensor-memory load and
-// another barrier, with room in tensor memory for two blocks; and shared memory, which carries 96 KB a block
-// (48 in, 48 to the MMAs), 768 cycles. Pairs of CTAs carry 64 KB each, and 8191 x 8192 x 8192 takes 403 us
-// (2730 TFLOP/s; 430 under the power limit) where single CTAs take 447. Few rows to an expert: the weights'
-// bytes; 32768 rows over 256 experts of 1024 x 2048 take 113 us, 5.9 TB/s.
+// What bounds it. Many rows: a pair's block of 256 columns takes 0.45 us where its MMAs take 0.26 by the nominal rate (512
+// cycles). Timestamps: the MMAs of a block follow each other without a gap, but last 950 cycles beside copies and sums and
+// 740 beside the copies alone. Shared memory carries 64 KB a block (32 in, 32 to the MMAs), 512 cycles of it, and 96 KB
+// where CTAs work alone; tensor memory hands 131 KB a block to the sums beside the MMAs' own traffic. The sums
+// themselves are 32768 FMAs, 256 cycles of the FMA pipes. 8191 x 8192 x 8192 takes 403 us (2730 TFLOP/s; 430 under the power
+// limit) in pairs and 447 with single CTAs. Few rows to an expert: the weights' bytes; 32768 rows over 256 experts of
+// 1024 x 2048 take 113 us, 5.9 TB/s.
 // What it took to get there from 809 us: a row's scales read by one warp ahead instead of by all who use them
 // (a line per lane filled L1's tag stage), plain FMAs (pairs cost a move for each register out of tensor memory),
 // loads of scales that no loop waits for, output rows stored 64 bytes at a time, both of the issuing warp's

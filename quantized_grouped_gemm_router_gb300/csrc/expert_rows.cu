@@ -2,7 +2,8 @@
 // gradient, moe_quant_weights. Each reads its rows once and writes its rows once: all are bound by HBM
 // where there are many rows, by launch and one load's latency where there are few.
 //
-// A warp takes pieces of 512 columns, 16 to a lane; a block's largest magnitude takes four shuffles.
+// A warp takes pieces of 512 columns, 16 to a lane; a block's largest magnitude takes four shuffles. Figures below: rows of
+// 2048 columns, 8 assignments to a token, one GB300 (a copy: 6.78 TB/s).
 #include "expert_device.cuh"
 
 namespace moe {
@@ -29,6 +30,7 @@ __device__ __forceinline__ uint64_t pair_of(const uint4 (&v)[2], int i) {
 }
 
 // ------------------------------------------------------------------------------------ dispatch
+// A token's row is read once and written top_k times: 16383 tokens take 53 us in e4m3 (6.3 TB/s), 89 us in bf16 (6.8).
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constant__ DispatchParams p, int warps) {
   pdl_wait();
@@ -64,6 +66,8 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
 }
 
 // ------------------------------------------------------------------------------------ combine
+// The rows of a token, scattered, summed in the order of its list: 4096 tokens take 26.5 us (5.7 TB/s; 28.2 with each token's
+// places loaded only when its turn came).
 constexpr int kCombinePiece = 256;  // 8 columns per lane: one 16-byte load of each row
 constexpr int kTogether = 8;        // rows whose loads are in flight together
 
@@ -117,7 +121,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
   }
 }
 
-// One warp per assignment: dy's row is read by the token's top_k warps out of L1.
+// One warp per assignment: dy's row is read by the token's top_k warps out of L1, and a weight's gradient is one warp's sum.
+// 16383 tokens take 143 us in e4m3 (5.9 TB/s); 171 with one fp32 operation a value and no loads ahead.
 template <bool E4M3>
 __global__ void __launch_bounds__(512) combine_grad_kernel(const __grid_constant__ CombineGradParams p, int tokens) {
   pdl_wait();
@@ -223,6 +228,8 @@ __device__ __forceinline__ moe_rows from_col(moe_rows r, int first) {
   return r;
 }
 
+// 32768 rows of 512 take 16 us in e4m3 (5.3 TB/s, 3 us of them a launch and its tail), 18.3 with a warp to a piece and no loads
+// ahead. More CTAs to an SM cost registers and gain nothing.
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const __grid_constant__ SwigluParams p, int warps) {
   pdl_wait();
@@ -264,7 +271,7 @@ __device__ __forceinline__ void swiglu_grad16(const uint4 (&gv)[2], const uint4 
 
 // WHOLE: inter is a multiple of 128, so that the blocks of dg and of du begin at the same columns and a
 // warp makes both from one reading. Otherwise the blocks of du straddle the two halves: the pieces run
-// over the 2 inter output columns, and what du needs of g and dh is read again (out of L2).
+// over the 2 inter output columns, and what du needs of g and dh is read again (out of L2). 15893 rows of 512: 13.9 us.
 template <bool E4M3, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(const __grid_constant__ SwigluParams p, int warps) {
   pdl_wait();
