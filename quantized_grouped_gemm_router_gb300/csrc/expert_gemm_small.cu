@@ -73,8 +73,8 @@ __device__ __forceinline__ uint4 stream_bytes(const uint8_t* p, bool there) {
   uint4 v = make_uint4(0, 0, 0, 0);
   if (there)
     asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p));
   return v;
 }
 
@@ -99,31 +99,43 @@ __global__ void __launch_bounds__(kThreads, 4) product_small_kernel(const __grid
     const float* as = p.a.scale + (int64_t)(grp.row0 + min(2 * t, grp.rows - 1)) * p.a.scale_stride;
     const int64_t next = 2 * t + 1 < grp.rows ? p.a.scale_stride : 0;
     const int kb0 = (int)((int64_t)slice * p.in_blocks / slices), kb1 = (int)((int64_t)(slice + 1) * p.in_blocks / slices);
-    uint4 x[2][2], y[2];
-    auto load = [&](int kb) {
+    // Two blocks of the inputs, each a set of registers of its own: one is on its way while the other is used. (With copies
+    // out of one set, loads waited for the block before and registers spilled: 8.2 us where this takes 7.2.)
+    struct Block {
+      uint4 w0[2], w8[2], a[2];
+    };
+    auto load = [&](Block& b, int kb) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int i = kb * kScaleBlock + j * 64;
         const bool there = kb < kb1 && i + t * 16 < p.in;  // 16 bytes lie within the row or behind it
-        x[0][j] = stream_bytes(w0 + i, there);
-        x[1][j] = stream_bytes(w8 + i, there);
-        y[j] = load_bytes(a + i, there && has);
+        b.w0[j] = stream_bytes(w0 + i, there);
+        b.w8[j] = stream_bytes(w8 + i, there);
+        b.a[j] = load_bytes(a + i, there && has);
       }
     };
-    load(kb0);
-    for (int kb = kb0; kb < kb1; ++kb) {
+    auto add = [&](const Block& b, int kb) {
       const float fw = __ldg(ws + kb), f0 = __ldg(as + kb) * fw, f1 = __ldg(as + next + kb) * fw;
       float c[4] = {};
-      const uint4 u0 = x[0][0], u8 = x[1][0], v0 = x[0][1], v8 = x[1][1], y0 = y[0], y1 = y[1];
-      load(kb + 1);
-      mma_e4m3(c, u0.x, u8.x, u0.y, u8.y, y0.x, y0.y);
-      mma_e4m3(c, u0.z, u8.z, u0.w, u8.w, y0.z, y0.w);
-      mma_e4m3(c, v0.x, v8.x, v0.y, v8.y, y1.x, y1.y);
-      mma_e4m3(c, v0.z, v8.z, v0.w, v8.w, y1.z, y1.w);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        mma_e4m3(c, b.w0[j].x, b.w8[j].x, b.w0[j].y, b.w8[j].y, b.a[j].x, b.a[j].y);
+        mma_e4m3(c, b.w0[j].z, b.w8[j].z, b.w0[j].w, b.w8[j].w, b.a[j].z, b.a[j].w);
+      }
       acc[0] = fmaf(f0, c[0], acc[0]);
       acc[1] = fmaf(f1, c[1], acc[1]);
       acc[2] = fmaf(f0, c[2], acc[2]);
       acc[3] = fmaf(f1, c[3], acc[3]);
+    };
+    Block even, odd;
+    load(even, kb0);
+#pragma unroll 1
+    for (int kb = kb0; kb < kb1; kb += 2) {
+      load(odd, kb + 1);
+      add(even, kb);
+      if (kb + 1 >= kb1) break;
+      load(even, kb + 2);
+      add(odd, kb + 1);
     }
   }
 #pragma unroll
@@ -145,9 +157,6 @@ __global__ void __launch_bounds__(kThreads, 4) product_small_kernel(const __grid
   }
 }
 
-}  // namespace
-
-namespace {
 struct SmallGrid {
   int slices, groups;
   int64_t columns;  // CTAs side by side
@@ -165,9 +174,10 @@ SmallGrid small_grid(const ProductParams& p) {
 }
 }  // namespace
 
-// Up to 8 rows, while all CTAs are resident at once: 2048 x 2048 takes 3.6 us here and 7.4 in the other kernel, 8192 x
-// 8192 15 and 21, a token's 8 of 256 experts of 1024 x 2048 8.2 and 8.7; but 8 rows over 8 experts of 4096 x 2048, whose
-// 2048 CTAs come in waves of loads and latency, 17.7 and 14.6.
+// Up to 8 rows, while all CTAs are resident at once. Here and in the other kernel, us: 2048 x 2048 3.3 and 6.9, 8192 x 8192
+// 14.4 and 19.1, 1024 x 16384 13.0 and 32.5, a token's 8 of 256 experts of 1024 x 2048 7.2 and 7.7 (of 2048 x 512 5.4 and
+// 5.1, the closest call); but past that number, in waves of loads and latency, 16384 x 1024 6.7 and 5.9, 8 rows over
+// 8 experts of 4096 x 2048 14.9 and 12.3.
 bool product_is_small(const ProductParams& p) {
   if (p.transposed || p.rows > kRows) return false;
   const SmallGrid g = small_grid(p);

@@ -193,6 +193,7 @@ __device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(y));
   return pack2(r, s);
 }
+
 __device__ __forceinline__ int rows_that_count(const SwigluParams& p) {
   if (!p.total) return p.rows;
   const int n = __ldg(p.total);
