@@ -479,9 +479,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             sts32(f + h * 512 + x * 128, a[x].x * w[h].x);
-            sts32(f + 1024 + h * 512 + x * 128, a[x].y * w[h].y);
-            sts32(f + 2048 + h * 512 + x * 128, a[x].z * w[h].z);
-            sts32(f + 3072 + h * 512 + x * 128, a[x].w * w[h].w);
+            sts32(f + 1 * 1024 + h * 512 + x * 128, a[x].y * w[h].y);
+            sts32(f + 2 * 1024 + h * 512 + x * 128, a[x].z * w[h].z);
+            sts32(f + 3 * 1024 + h * 512 + x * 128, a[x].w * w[h].w);
           }
         if (threadIdx.x == kWarpScale0 * 32)
           sts128(base + L::item_off + s * 16, make_uint4(it.row0, it.rows, it.col0, 0));
