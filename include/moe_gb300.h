@@ -616,11 +616,13 @@ MOE_API int moe_quant_weights(const uint16_t* w, int32_t n_experts, int32_t n, i
 /*
  * Products of e4m3 rows with their experts' matrices. Rows offsets[e] .. offsets[e + 1] - 1 of a
  * belong to expert e (device int32[n_experts + 1], ascending from 0 or more to at most `rows`; where they
- * do not, nothing is written (MOE_ERR_BAD_INDEX); NULL: all rows belong to the one expert, n_experts == 1). transposed == 0: out[p] = W[e] a[p] (a: k columns, out: n);
- * transposed != 0: out[p] = W[e]^T a[p] (a: n columns, out: k), the gradient of the former's
- * inputs on the same codes. out: bf16.
- * The codes' products are summed in fp32 within a block of 128; each block's sum is multiplied by its
- * two scales and added in fp32.
+ * do not, nothing is written (MOE_ERR_BAD_INDEX); NULL: all rows belong to the one expert,
+ * n_experts == 1). transposed == 0: out[p] = W[e] a[p] (a: k columns, out: n); transposed != 0:
+ * out[p] = W[e]^T a[p] (a: n columns, out: k), the gradient of the former's inputs on the same
+ * codes. out: bf16.
+ * The codes' products are summed in fp32 within a block of 128; each block's sum is multiplied by the
+ * product of its two scales and added in fp32. That product is formed first, in fp32: it has to stay
+ * below 2^128, and keeps 24 bits from 2^-126 on (blocks whose largest values multiply to 2^-108).
  */
 MOE_API int moe_gemm_e4m3(const moe_rows* a, int32_t rows, const moe_e4m3_weights* w, const int32_t* offsets,
                           int32_t transposed, const moe_rows* out, void* ws, size_t ws_bytes, moe_stream_t stream);
