@@ -8,9 +8,9 @@
 
 #include "../../include/moe_gb300.h"
 
-static PyObject *g_torch, *g_torch_c, *g_tensor, *g_error, *g_rows_class;
+static PyObject *g_torch, *g_torch_c, *g_tensor, *g_error, *g_rows_class, *g_weights_class;
 static PyObject *g_int16, *g_int32, *g_float32, *g_uint8;
-static PyObject *s_dtype, *s_device, *s_get_device, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_empty, *s_described,
+static PyObject *s_dtype, *s_device, *s_get_device, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_empty, *s_q, *s_scale,
     *s_cuda_device, *s_cuda_stream, *g_empty_names;
 
 /* ---------------------------------------------------------------------------------- tensors */
@@ -148,18 +148,103 @@ static int bf16_rows(PyObject* o, const char* name, int64_t rows, int64_t cols, 
   return 0;
 }
 
-/* Copies what describe_rows or describe_weights kept in an object; 0 if it keeps nothing of that size. */
-static int described(PyObject* o, void* to, size_t size) {
-  PyObject* b = PyObject_GetAttr(o, s_described);
-  const int ok = b && PyBytes_Check(b) && (size_t)PyBytes_GET_SIZE(b) == size;
-  if (ok) memcpy(to, PyBytes_AS_STRING(b), size);
-  Py_XDECREF(b);
-  if (!b) PyErr_Clear();
+/* An object that carries two tensors, q and scale. They are read at every call and nothing is kept of them: they may have been
+ * exchanged, moved or copied with the object since the call before. New references; 0 without an exception if the object is
+ * not of the class. */
+static int carried(PyObject* o, PyObject* class, PyObject** q, PyObject** scale) {
+  *q = *scale = NULL;
+  if (PyObject_IsInstance(o, class) == 1 && (*q = PyObject_GetAttr(o, s_q)) && (*scale = PyObject_GetAttr(o, s_scale))) return 1;
+  PyErr_Clear();
+  Py_CLEAR(*q);
+  return 0;
+}
+
+/* The tensors of E4m3Rows; `of`: the object's name and a dot, for messages. */
+static int read_rows(PyObject* q_obj, PyObject* scale_obj, const char* of, rows_t* r) {
+  tensor q, s;
+  if (!read_tensor(q_obj, g_uint8, 1, &q) || q.device < 0 || q.dims != 2 || q.size[0] >= MANY || q.size[1] >= MANY ||
+      (q.stride[1] != 1 && q.size[0] && q.size[1])) {
+    PyErr_Format(PyExc_ValueError, "%sq must be a CUDA tensor of uint8 [rows, columns], the values of a row contiguous", of);
+    return 0;
+  }
+  const int64_t nb = blocks(q.size[1]);
+  if (!read_tensor(scale_obj, g_float32, 1, &s) || s.device != q.device || s.dims != 2 || s.size[0] != q.size[0] || s.size[1] != nb ||
+      (s.stride[1] != 1 && nb > 1 && q.size[0])) {
+    PyErr_Format(PyExc_ValueError,
+                 "%sscale must be a float32 tensor [%lld, %lld] on q's device, the values of a row contiguous", of,
+                 (long long)q.size[0], (long long)nb);
+    return 0;
+  }
+  r->rows = q.size[0];
+  r->cols = q.size[1];
+  r->device = q.device;
+  r->r.format = MOE_ROWS_E4M3;
+  r->r.p = q.data;
+  r->r.stride = q.size[0] > 1 ? q.stride[0] : nb * 128;
+  r->r.scale = s.data;
+  r->r.scale_stride = q.size[0] > 1 ? s.stride[0] : nb;
+  return 1;
+}
+
+typedef struct {
+  moe_e4m3_weights w;
+  int64_t device;
+} weights_t;
+
+/* The same for E4m3Weights. */
+static int read_weights(PyObject* q_obj, PyObject* scale_obj, const char* of, weights_t* w) {
+  tensor q, s;
+  if (!read_tensor(q_obj, g_uint8, 0, &q) || q.device < 0 || q.dims != 3 || q.size[0] >= MANY || q.size[1] >= MANY || q.size[2] >= MANY) {
+    PyErr_Format(PyExc_ValueError, "%sq must be a contiguous CUDA tensor of uint8 [n_experts, n, k]", of);
+    return 0;
+  }
+  if (!read_tensor(scale_obj, g_float32, 0, &s) || s.device != q.device || s.dims != 3 || s.size[0] != q.size[0] ||
+      s.size[1] != blocks(q.size[1]) || s.size[2] != blocks(q.size[2])) {
+    PyErr_Format(PyExc_ValueError, "%sscale must be a contiguous float32 tensor [%lld, %lld, %lld] on q's device", of,
+                 (long long)q.size[0], (long long)blocks(q.size[1]), (long long)blocks(q.size[2]));
+    return 0;
+  }
+  w->w.q = q.data;
+  w->w.scale = s.data;
+  w->w.n_experts = (int32_t)q.size[0];
+  w->w.n = (int32_t)q.size[1];
+  w->w.k = (int32_t)q.size[2];
+  w->device = q.device;
+  return 1;
+}
+
+/* E4m3Rows as they are now, on any device. */
+static int carried_rows(PyObject* o, const char* name, rows_t* r) {
+  PyObject *q, *scale;
+  char of[16];
+  if (!carried(o, g_rows_class, &q, &scale)) {
+    PyErr_Format(PyExc_ValueError, "%s must be E4m3Rows", name);
+    return 0;
+  }
+  PyOS_snprintf(of, sizeof of, "%s.", name);
+  const int ok = read_rows(q, scale, of, r);
+  Py_DECREF(q);
+  Py_DECREF(scale);
   return ok;
 }
 
-static int e4m3_rows(PyObject* o, const char* name, int64_t rows, int64_t cols, int64_t dev, rows_t* r) {
-  if (described(o, r, sizeof *r) && r->device == dev && (rows == ANY || r->rows == rows) && (cols == ANY || r->cols == cols)) return 1;
+static int carried_weights(PyObject* o, const char* name, weights_t* w) {
+  PyObject *q, *scale;
+  char of[16];
+  if (!carried(o, g_weights_class, &q, &scale)) {
+    PyErr_Format(PyExc_ValueError, "%s must be E4m3Weights", name);
+    return 0;
+  }
+  PyOS_snprintf(of, sizeof of, "%s.", name);
+  const int ok = read_weights(q, scale, of, w);
+  Py_DECREF(q);
+  Py_DECREF(scale);
+  return ok;
+}
+
+/* Whether E4m3Rows that were read are of the size, and on the device, that the call takes. */
+static int rows_fit(const rows_t* r, const char* name, int64_t rows, int64_t cols, int64_t dev) {
+  if (r->device == dev && (rows == ANY || r->rows == rows) && (cols == ANY || r->cols == cols)) return 1;
   char a[24], b[24];
   PyErr_Format(PyExc_ValueError, "%s must be E4m3Rows [%s, %s] on the current CUDA device", name,
                size_text(rows, "rows", a, sizeof a), size_text(cols, "columns", b, sizeof b));
@@ -247,8 +332,9 @@ static PyObject* rows_out(PyObject* out, PyObject* e4m3, PyObject* like, int64_t
     out = new_tensor(like, g_int16, 2, made, cols);
   }
   if (!out) return NULL;
-  const int ok = PyObject_TypeCheck(out, (PyTypeObject*)g_tensor) ? bf16_rows(out, "out", rows, cols, dev, r)
-                                                                  : e4m3_rows(out, "out", rows, cols, dev, r);
+  const int ok = PyObject_TypeCheck(out, (PyTypeObject*)g_tensor)
+                     ? bf16_rows(out, "out", rows, cols, dev, r)
+                     : carried_rows(out, "out", r) && rows_fit(r, "out", rows, cols, dev);
   if (ok) return out;
   Py_DECREF(out);
   return NULL;
@@ -279,66 +365,19 @@ static int arity(Py_ssize_t n, Py_ssize_t want, const char* name) {
 }
 
 /* ---------------------------------------------------------------------------------- the calls */
-/* describe_rows(q, scale): what E4m3Rows keeps. */
-static PyObject* describe_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+/* check_rows(q, scale), check_weights(q, scale): whether the classes can carry these tensors. */
+static PyObject* check_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (!arity(n, 2, "describe_rows")) return NULL;
-  tensor q, s;
-  if (!read_tensor(a[0], g_uint8, 1, &q) || q.device < 0 || q.dims != 2 || q.size[0] >= MANY || q.size[1] >= MANY ||
-      (q.stride[1] != 1 && q.size[0] && q.size[1])) {
-    PyErr_SetString(PyExc_ValueError, "q must be a CUDA tensor of uint8 [rows, columns], the values of a row contiguous");
-    return NULL;
-  }
-  const int64_t nb = blocks(q.size[1]);
-  if (!read_tensor(a[1], g_float32, 1, &s) || s.device != q.device || s.dims != 2 || s.size[0] != q.size[0] || s.size[1] != nb ||
-      (s.stride[1] != 1 && nb > 1 && q.size[0])) {
-    PyErr_Format(PyExc_ValueError,
-                 "scale must be a float32 tensor [%lld, %lld] on q's device, the values of a row contiguous",
-                 (long long)q.size[0], (long long)nb);
-    return NULL;
-  }
   rows_t r;
-  memset(&r, 0, sizeof r);
-  r.rows = q.size[0];
-  r.cols = q.size[1];
-  r.device = q.device;
-  r.r.format = MOE_ROWS_E4M3;
-  r.r.p = q.data;
-  r.r.stride = q.size[0] > 1 ? q.stride[0] : nb * 128;
-  r.r.scale = s.data;
-  r.r.scale_stride = q.size[0] > 1 ? s.stride[0] : nb;
-  return PyBytes_FromStringAndSize((const char*)&r, sizeof r);
+  if (!arity(n, 2, "check_rows") || !read_rows(a[0], a[1], "", &r)) return NULL;
+  Py_RETURN_NONE;
 }
 
-typedef struct {
-  moe_e4m3_weights w;
-  int64_t device;
-} weights_t;
-
-/* describe_weights(q, scale): what E4m3Weights keeps. */
-static PyObject* describe_weights(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+static PyObject* check_weights(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (!arity(n, 2, "describe_weights")) return NULL;
-  tensor q, s;
-  if (!read_tensor(a[0], g_uint8, 0, &q) || q.device < 0 || q.dims != 3 || q.size[0] >= MANY || q.size[1] >= MANY || q.size[2] >= MANY) {
-    PyErr_SetString(PyExc_ValueError, "q must be a contiguous CUDA tensor of uint8 [n_experts, n, k]");
-    return NULL;
-  }
-  if (!read_tensor(a[1], g_float32, 0, &s) || s.device != q.device || s.dims != 3 || s.size[0] != q.size[0] ||
-      s.size[1] != blocks(q.size[1]) || s.size[2] != blocks(q.size[2])) {
-    PyErr_Format(PyExc_ValueError, "scale must be a contiguous float32 tensor [%lld, %lld, %lld] on q's device",
-                 (long long)q.size[0], (long long)blocks(q.size[1]), (long long)blocks(q.size[2]));
-    return NULL;
-  }
   weights_t w;
-  memset(&w, 0, sizeof w);
-  w.w.q = q.data;
-  w.w.scale = s.data;
-  w.w.n_experts = (int32_t)q.size[0];
-  w.w.n = (int32_t)q.size[1];
-  w.w.k = (int32_t)q.size[2];
-  w.device = q.device;
-  return PyBytes_FromStringAndSize((const char*)&w, sizeof w);
+  if (!arity(n, 2, "check_weights") || !read_weights(a[0], a[1], "", &w)) return NULL;
+  Py_RETURN_NONE;
 }
 
 /* workspace_bytes(n_experts) */
@@ -460,7 +499,7 @@ static PyObject* combine_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) 
   return result;
 }
 
-/* quant_weights(w, q, scale): int16 [E, n, k] into q and scale of describe_weights' shapes. */
+/* quant_weights(w, q, scale): int16 [E, n, k] into q and scale of E4m3Weights' shapes. */
 static PyObject* quant_weights(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   int64_t dev;
@@ -491,23 +530,20 @@ static PyObject* gemm_e4m3(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   space_t ws;
   if (!arity(n, 6, "gemm_e4m3")) return NULL;
   weights_t w;
-  if (!described(a[0], &x, sizeof x) || !described(a[1], &w, sizeof w)) {
-    PyErr_SetString(PyExc_ValueError, "a must be E4m3Rows and w E4m3Weights");
-    return NULL;
-  }
+  if (!carried_rows(a[0], "a", &x) || !carried_weights(a[1], "w", &w)) return NULL;
   const int transposed = PyObject_IsTrue(a[4]);
   if (transposed < 0 || !current_device(x.device, "a", &dev)) return NULL;
   if (w.device != dev) {
     PyErr_SetString(PyExc_ValueError, "w must be on the current CUDA device");
     return NULL;
   }
-  if (!e4m3_rows(a[0], "a", ANY, transposed ? w.w.n : w.w.k, dev, &x) ||
+  if (!rows_fit(&x, "a", ANY, transposed ? w.w.n : w.w.k, dev) ||
       (a[2] != Py_None && !ints(a[2], "offsets", (int64_t)w.w.n_experts + 1, dev, &offsets)) || !space(a[3], dev, &ws))
     return NULL;
   PyObject* out = a[5];
   const int64_t cols = transposed ? w.w.k : w.w.n;
   if (out == Py_None) {
-    PyObject* q = PyObject_GetAttrString(a[0], "q");
+    PyObject* q = PyObject_GetAttr(a[0], s_q);
     if (!q) return NULL;
     out = new_tensor(q, g_int16, 2, x.rows, cols);
     Py_DECREF(q);
@@ -573,19 +609,21 @@ static PyObject* swiglu_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return NULL;
 }
 
-/* setup(MoeError, E4m3Rows): the package's classes. */
+/* setup(MoeError, E4m3Rows, E4m3Weights): the package's classes. */
 static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (!arity(n, 2, "setup")) return NULL;
+  if (!arity(n, 3, "setup")) return NULL;
   Py_INCREF(a[0]);
   Py_XSETREF(g_error, a[0]);
   Py_INCREF(a[1]);
   Py_XSETREF(g_rows_class, a[1]);
+  Py_INCREF(a[2]);
+  Py_XSETREF(g_weights_class, a[2]);
   Py_RETURN_NONE;
 }
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
-static PyMethodDef methods[] = {FAST(setup), FAST(describe_rows), FAST(describe_weights), {"workspace_bytes", workspace_bytes, METH_O, NULL},
+static PyMethodDef methods[] = {FAST(setup), FAST(check_rows), FAST(check_weights), {"workspace_bytes", workspace_bytes, METH_O, NULL},
                                 FAST(sort_tokens), FAST(dispatch), FAST(combine), FAST(combine_grad), FAST(quant_weights),
                                 FAST(gemm_e4m3), FAST(swiglu), FAST(swiglu_grad), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_experts", NULL, -1, methods, NULL, NULL, NULL, NULL};
@@ -610,7 +648,8 @@ PyMODINIT_FUNC PyInit__experts(void) {
                      {&s_data_ptr, "data_ptr"},
                      {&s_is_contiguous, "is_contiguous"},
                      {&s_empty, "empty"},
-                     {&s_described, "_described"},
+                     {&s_q, "q"},
+                     {&s_scale, "scale"},
                      {&s_cuda_device, "_cuda_getDevice"},
                      {&s_cuda_stream, "_cuda_getCurrentRawStream"}};
   for (size_t i = 0; i < sizeof names / sizeof *names; ++i)

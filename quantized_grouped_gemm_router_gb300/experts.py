@@ -26,7 +26,7 @@ class _Unloaded:
         global _native
         lib()  # says what to do where nothing is built
         _native = importlib.import_module("._experts", __package__)
-        _native.setup(MoeError, E4m3Rows)
+        _native.setup(MoeError, E4m3Rows, E4m3Weights)
         return getattr(_native, name)
 
 
@@ -51,11 +51,18 @@ def _blocks(n: int) -> int:
 
 class E4m3Rows:
     """Rows in 8 bits over the caller's tensors: codes q uint8 [rows, columns], scale float32
-    [rows, ceil(columns / 128)]; a code c of column j stands for scale[row, j // 128] * c."""
+    [rows, ceil(columns / 128)]; a code c of column j stands for scale[row, j // 128] * c.
+
+    Every call reads the two tensors, and checks them, as they are then: others may be put in their place, and a copy
+    of the object (copy.deepcopy, pickle) has tensors of its own."""
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor):
-        self._described = _native.describe_rows(q, scale)
-        self.q, self.scale, self.shape = q, scale, q.shape
+        _native.check_rows(q, scale)
+        self.q, self.scale = q, scale
+
+    @property
+    def shape(self) -> torch.Size:
+        return self.q.shape
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda"):
@@ -70,11 +77,15 @@ class E4m3Rows:
 
 class E4m3Weights:
     """Expert matrices in 8 bits over the caller's tensors, contiguous: codes q uint8
-    [n_experts, n, k], scale float32 [n_experts, ceil(n / 128), ceil(k / 128)]."""
+    [n_experts, n, k], scale float32 [n_experts, ceil(n / 128), ceil(k / 128)]. Read at every call, as E4m3Rows."""
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor):
-        self._described = _native.describe_weights(q, scale)
-        self.q, self.scale, self.shape = q, scale, q.shape
+        _native.check_weights(q, scale)
+        self.q, self.scale = q, scale
+
+    @property
+    def shape(self) -> torch.Size:
+        return self.q.shape
 
     @classmethod
     def quantise(cls, w: torch.Tensor) -> "E4m3Weights":
