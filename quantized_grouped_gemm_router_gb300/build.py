@@ -3,7 +3,8 @@
 Each translation unit under csrc/ is compiled in parallel with nvcc, then linked into
 _lib/libmoe_gb300.so with a static CUDA runtime so the library loads on a machine without a
 GPU (the C ABI can then be inspected; compute calls report a CUDA error). The CPython module of the
-8-bit expert calls (csrc/py_experts.c) is built beside it with the host's C compiler.
+8-bit expert calls (csrc/py_experts.c) is built beside it with the host's C compiler; where that or Python's
+headers are missing it is left out, with a warning, and those calls raise ImportError.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -85,11 +87,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
 
 def _build_module() -> None:
     """The CPython module of the 8-bit expert calls, linked to the library beside it."""
-    cc = shutil.which("cc") or shutil.which("gcc")
-    if not cc:
-        raise RuntimeError("a C compiler is required to build the _experts module")
+    cc, headers = shutil.which("cc") or shutil.which("gcc"), sysconfig.get_paths()["include"]
+    if not cc or not os.path.exists(os.path.join(headers, "Python.h")):
+        if os.path.exists(MODULE_PATH):
+            os.remove(MODULE_PATH)  # it belongs to an earlier library
+        warnings.warn(f"built without the 8-bit expert calls: they need a C compiler and {os.path.join(headers, 'Python.h')}")
+        return
     tmp = MODULE_PATH + ".tmp"
-    cmd = [cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", f"-I{sysconfig.get_paths()['include']}", MODULE_SOURCE, "-o", tmp,
+    cmd = [cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", f"-I{headers}", MODULE_SOURCE, "-o", tmp,
            f"-L{LIB_DIR}", "-lmoe_gb300", "-Wl,-rpath,$ORIGIN/_lib"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

@@ -25,7 +25,11 @@ class _Unloaded:
     def __getattr__(self, name):
         global _native
         lib()  # says what to do where nothing is built
-        _native = importlib.import_module("._experts", __package__)
+        try:
+            module = importlib.import_module("._experts", __package__)
+        except ModuleNotFoundError as e:
+            raise ImportError("the 8-bit expert calls are not built: build() needs a C compiler and Python's headers for them") from e
+        _native = module
         _native.setup(MoeError, E4m3Rows, E4m3Weights)
         return getattr(_native, name)
 
