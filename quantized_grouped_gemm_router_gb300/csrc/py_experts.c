@@ -322,9 +322,11 @@ static PyObject* new_tensor(PyObject* like, PyObject* dtype, int dims, int64_t a
 
 /* The output rows, a new reference: those given, or `rows` new ones of the kind asked for. */
 static PyObject* rows_out(PyObject* out, PyObject* e4m3, PyObject* like, int64_t rows, int64_t made, int64_t cols, int64_t dev, rows_t* r) {
+  const int as_codes = out == Py_None ? PyObject_IsTrue(e4m3) : 0;
+  if (as_codes < 0) return NULL;
   if (out != Py_None) {
     Py_INCREF(out);
-  } else if (PyObject_IsTrue(e4m3) == 1) {
+  } else if (as_codes) {
     PyObject* device = PyObject_GetAttr(like, s_device);
     out = device ? PyObject_CallMethod(g_rows_class, "empty", "LLO", (long long)made, (long long)cols, device) : NULL;
     Py_XDECREF(device);

@@ -238,3 +238,21 @@ def test_unfit_tensors_are_refused(m, stand_in):
         m.gemm_e4m3(r, weights(m), off, ws)
     with pytest.raises(ValueError):
         m.gemm_e4m3(rows(m), w, off, ws)
+
+
+class Undecided:
+    """Neither true nor false, as an array of several values is."""
+
+    def __bool__(self):
+        raise ValueError("truth value of several values")
+
+
+def test_an_undecided_format(m, stand_in):
+    """What cannot say whether it is true is an error, not `False`."""
+    ws = z(16, dtype=torch.uint8)
+    inv, w = z(6, 1, dtype=torch.int32), z(6, 1, dtype=torch.float32)
+    for call in (lambda e: m.dispatch(z(6, 32), None, ws, e4m3=e), lambda e: m.swiglu(z(6, 64), ws, e4m3=e),
+                 lambda e: m.swiglu_grad(z(6, 64), z(6, 32), ws, e4m3=e), lambda e: m.combine_grad(z(6, 32), z(6, 32), inv, w, ws, e4m3=e)):
+        with pytest.raises(ValueError, match="truth value"):
+            call(Undecided())
+        call(True), call(False)
