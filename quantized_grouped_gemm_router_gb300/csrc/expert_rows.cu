@@ -182,8 +182,7 @@ __global__ void __launch_bounds__(512) combine_grad_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------------------------ SwiGLU
-// s = 1 / (1 + e^-g) of two values: e^-g to a few units of the last place (its argument's rounding: 2^-17 at |g| of
-// 88); below 2^-126 (g < -87.3) s is 0.
+// s = 1 / (1 + e^-g) of two values from -32 on: e^-g to a few units of the last place (its argument's rounding: |g| 2^-24).
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
   constexpr float c = -1.4426950408889634f;
   float x, y, r, s;
@@ -192,6 +191,26 @@ __device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(y));
   return pack2(r, s);
+}
+
+// Below -32, where s is less than 2^-46, its products are made in 64 bits: from -87 on s is no normal fp32 number, while a
+// large u or dh may bring the result back into range (bf16 reaches from 2^-133 to 2^128). There s is e^g to 2^-46, taken
+// as the fourth power of 2^(g log2(e) / 4), which is normal down to g = -349; below, no result is. Such values are rare: a
+// piece is looked over once, and one that has any takes the longer way (a value at a time: 80 registers in the gradient,
+// where calls in any order take 125).
+constexpr float kFar = -32.f;
+constexpr uint32_t kFarBits = 0xC200;  // in bf16; greater as an unsigned number are the values below (and NaN with a sign)
+__device__ __forceinline__ bool any_far(const uint4 (&g)[2]) {
+  uint32_t m = __vmaxu2(word(g[0], 0), word(g[1], 0));
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = __vmaxu2(m, __vmaxu2(word(g[0], i), word(g[1], i)));
+  return m >> 16 > kFarBits || (m & 0xFFFFu) > kFarBits;
+}
+__device__ __forceinline__ double far_sigmoid(float g) {
+  float x;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(g * (1.4426950408889634f / 4)));  // volatile: one after the other
+  const double r = x, r2 = r * r;
+  return r2 * r2;
 }
 
 __device__ __forceinline__ int rows_that_count(const SwigluParams& p) {
@@ -247,18 +266,33 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const __grid_constant_
     uint64_t g[8], u[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = pair_of(gv, i), u[i] = pair_of(uv, i);
+    const bool far = any_far(gv);
     if (next.inside()) {
       load_piece(p.gu, next.row, next.piece, p.inter, gv);
       load_piece(up, next.row, next.piece, p.inter, uv);
     }
     float h[16];
+    if (!far) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) unpack2(mul2(mul2(g[i], sigmoid2(g[i])), u[i]), h[2 * i], h[2 * i + 1]);
+      for (int i = 0; i < 8; ++i) unpack2(mul2(mul2(g[i], sigmoid2(g[i])), u[i]), h[2 * i], h[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x[2], y[2];
+        unpack2(mul2(mul2(g[i], sigmoid2(g[i])), u[i]), h[2 * i], h[2 * i + 1]);
+        unpack2(g[i], x[0], x[1]);
+        unpack2(u[i], y[0], y[1]);
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+          if (x[v] < kFar) h[2 * i + v] = (float)(far_sigmoid(x[v]) * x[v] * y[v]);
+      }
+    }
     store_piece<E4M3>(p.out, at.row, at.piece, p.inter, h);
   }
 }
 
 // dg and du of 16 columns; either may be left out.
+template <bool FAR>
 __device__ __forceinline__ void swiglu_grad16(const uint4 (&gv)[2], const uint4 (&uv)[2], const uint4 (&hv)[2],
                                               float (&dg)[16], float (&du)[16]) {
   const uint64_t one = pack2(1.f, 1.f), minus = pack2(-1.f, -1.f);
@@ -267,6 +301,19 @@ __device__ __forceinline__ void swiglu_grad16(const uint4 (&gv)[2], const uint4 
     const uint64_t g = pair_of(gv, i), s = sigmoid2(g), hs = mul2(pair_of(hv, i), s);
     unpack2(mul2(mul2(hs, pair_of(uv, i)), fma2(g, fma2(s, minus, one), one)), dg[2 * i], dg[2 * i + 1]);
     unpack2(mul2(hs, g), du[2 * i], du[2 * i + 1]);
+    if (FAR) {
+      float x[2], u[2], h[2];
+      unpack2(g, x[0], x[1]);
+      unpack2(pair_of(uv, i), u[0], u[1]);
+      unpack2(pair_of(hv, i), h[0], h[1]);
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+        if (x[v] < kFar) {
+          const double s = far_sigmoid(x[v]) * h[v];
+          dg[2 * i + v] = (float)(s * u[v] * (1.0 + x[v]));
+          du[2 * i + v] = (float)(s * x[v]);
+        }
+    }
   }
 }
 
@@ -305,7 +352,10 @@ __global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(const __grid_cons
   for (; at.inside(); at = next) {
     next = at.next();
     float dg[16], du[16];
-    swiglu_grad16(gv, uv, hv, dg, du);
+    if (any_far(gv))
+      swiglu_grad16<true>(gv, uv, hv, dg, du);
+    else
+      swiglu_grad16<false>(gv, uv, hv, dg, du);
     if (next.inside()) load(next);
     if (WHOLE) {
       store_piece<E4M3>(p.out, at.row, at.piece, p.inter, dg);

@@ -1,0 +1,72 @@
+"""The 8-bit expert calls on a GB300 where their arguments are unusual: gates far below zero."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import expert_check as C  # noqa: E402
+from tests.test_gpu_experts import dev, m, ws  # noqa: E402, F401
+
+pytestmark = pytest.mark.gpu
+
+
+def far_values():
+    """g from -30 down to where no result is left, u and dh over bf16's range; only results below 2^126."""
+    g, u, h = [], [], []
+    for x in (-30.0, -32.0, -32.25, -46.0, -64.0, -87.0, -87.5, -88.0, -88.5, -89.0, -96.0, -104.0, -120.0, -150.0, -174.0, -175.0, -200.0,
+              -250.0, -300.0, -348.0, -350.0, -1000.0, -2.0 ** 127):
+        for y in (1.0, -3.0, 2.0 ** -60, 2.0 ** 40, 1.5 * 2.0 ** 100, -1.75 * 2.0 ** 126):
+            for z in (1.0, -2.0 ** -30, 2.0 ** 60, 1.25 * 2.0 ** 120):
+                g.append(x), u.append(y), h.append(z)
+    return (torch.tensor(v, dtype=torch.float64) for v in (g, u, h))
+
+
+def as_rows(x, cols):
+    """Values as bf16 rows of `cols`, the last row filled up with -40."""
+    assert torch.equal(x.to(torch.bfloat16).double(), x)
+    n = (len(x) + cols - 1) // cols * cols
+    return torch.cat([x, torch.full((n - len(x),), -40.0, dtype=torch.float64)]).view(-1, cols)
+
+
+@pytest.mark.parametrize("inter", [48, 128, 528])
+def test_swiglu_far_below(m, ws, inter):  # noqa: F811
+    """Where s = 1 / (1 + e^-g) is no normal fp32 number, a large u or dh brings its products back into range. The bounds
+    are those of expert_check without its allowance of 2^-126 in s: fp32 results below 2^-126 are off by 2^-150, and the
+    rest by (|g| + 8) 2^-23 of themselves (1 + g (1 - s) is 1 + g there to 2^-46, exact in 64 bits)."""
+    g, u, h = far_values()
+    s = torch.sigmoid(g)
+    for name, ref in (("h", g * s * u), ("du", h * g * s), ("dg", h * u * s * (1 + g * torch.sigmoid(-g)))):
+        keep = ref.abs() < 2.0 ** 126
+        if name == "dg":  # both halves of the gradient
+            keep &= (h * g * s).abs() < 2.0 ** 126
+        G, U, H = (as_rows(v[keep], inter) for v in (g, u, h))
+        S = torch.sigmoid(G)
+        e = (G.abs() + 8) * 2.0 ** -23
+        gu = torch.cat([G, U], 1).to(torch.bfloat16)
+        if name == "h":
+            ref = G * S * U
+            got = m.swiglu(dev(gu), ws)
+            err = ref.abs() * e + 2.0 ** -149
+        else:
+            dg, du = H * U * S * (1 + G * torch.sigmoid(-G)), H * G * S
+            if name == "du":  # dg may be out of range: its u is left out
+                gu[:, inter:] = 0
+                dg = torch.zeros_like(dg)
+            ref = torch.cat([dg, du], 1)
+            got = m.swiglu_grad(dev(gu), dev(H.to(torch.bfloat16)), ws)
+            err = ref.abs() * torch.cat([e, e], 1) + 2.0 ** -149
+        C.check_rows(got, ref, err, name)
+        assert (ref.abs() > 2.0 ** -100).any() and (ref[ref.abs() < 2.0 ** -100].abs() > 2.0 ** -126).any()
+
+
+def test_swiglu_far_below_in_8_bits(m, ws):  # noqa: F811
+    g = torch.tensor([-88.0, -90.0, -100.0, -120.0]).double().repeat(2, 64)
+    u = torch.full_like(g, 2.0 ** 100)
+    u[1] = -1.5 * 2.0 ** 120
+    h = torch.full_like(g, 2.0 ** 20)
+    s = torch.sigmoid(g)
+    e = (g.abs() + 8) * 2.0 ** -23
+    gu = torch.cat([g, u], 1).to(torch.bfloat16)
+    ref = g * s * u
+    C.check_rows(m.swiglu(dev(gu), ws, e4m3=True), ref, ref.abs() * e)
+    ref = torch.cat([h * u * s * (1 + g * torch.sigmoid(-g)), h * g * s], 1)
+    C.check_rows(m.swiglu_grad(dev(gu), dev(h.to(torch.bfloat16)), ws, e4m3=True), ref, ref.abs() * torch.cat([e, e], 1) + 2.0 ** -149)
