@@ -1,10 +1,12 @@
-"""The 8-bit expert calls on a GB300 where their arguments are unusual: gates far below zero."""
+"""The 8-bit expert calls on a GB300 where their arguments are unusual: gates far below zero, copied handles."""
+import copy
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from tests import expert_check as C  # noqa: E402
-from tests.test_gpu_experts import dev, m, ws  # noqa: E402, F401
+from tests.test_gpu_experts import dev, make_product, m, rand, ws  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +72,20 @@ def test_swiglu_far_below_in_8_bits(m, ws):  # noqa: F811
     C.check_rows(m.swiglu(dev(gu), ws, e4m3=True), ref, ref.abs() * e)
     ref = torch.cat([h * u * s * (1 + g * torch.sigmoid(-g)), h * g * s], 1)
     C.check_rows(m.swiglu_grad(dev(gu), dev(h.to(torch.bfloat16)), ws, e4m3=True), ref, ref.abs() * torch.cat([e, e], 1) + 2.0 ** -149)
+
+
+def test_copied_handles(m, ws):  # noqa: F811
+    """A copy computes with its own memory: the original may change, and go."""
+    a, w, offsets, _ = make_product(m, 5, [40, 0, 91], 272, 400, False)
+    want = m.gemm_e4m3(a, w, offsets, ws)
+    a2, w2 = copy.deepcopy(a), copy.deepcopy(w)
+    for x in (a.q, w.q):
+        x.fill_(0x7F)
+    assert torch.equal(m.gemm_e4m3(a2, w2, offsets, ws), want)
+    assert not torch.equal(m.gemm_e4m3(a, w, offsets, ws), want)
+    out, x = copy.deepcopy(a2), dev(rand(1, 131, 400))
+    m.dispatch(x, None, ws, out=out)
+    assert torch.equal(m.gemm_e4m3(a2, w2, offsets, ws), want)  # what was written to a copy of it
+    a.q, a.scale, w.q.data, w.scale.data = a2.q, a2.scale, w2.q, w2.scale
+    del a2, w2
+    assert torch.equal(m.gemm_e4m3(a, w, offsets, ws), want)
