@@ -627,6 +627,15 @@ MOE_API int moe_quant_weights(const uint16_t* w, int32_t n_experts, int32_t n, i
 MOE_API int moe_gemm_e4m3(const moe_rows* a, int32_t rows, const moe_e4m3_weights* w, const int32_t* offsets,
                           int32_t transposed, const moe_rows* out, void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* Which form of the kernel moe_gemm_e4m3 takes for these sizes on a device of `sms` SMs that runs `pairs` pairs of CTAs at
+ * once (the offsets do not matter; `stride` is that of a), so that a test can tell what it covers. -1: unsupported. */
+#define MOE_PRODUCT_FEW_ROWS 0 /* up to 8 rows: weights straight into registers */
+#define MOE_PRODUCT_128 1      /* 128 rows x 128 columns to a CTA */
+#define MOE_PRODUCT_256 2      /* 128 rows x 256 columns */
+#define MOE_PRODUCT_PAIRS 3    /* 256 rows x 256 columns to a pair of CTAs */
+MOE_API int32_t moe_gemm_e4m3_form(int32_t rows, int32_t n_experts, int32_t n, int32_t k, int32_t transposed, int64_t stride,
+                                   int32_t sms, int32_t pairs);
+
 /*
  * h = silu(g) * u for rows gu = g | u of 2 * inter columns (bf16): h of inter columns, bf16 or e4m3.
  * total: device int32, the number of rows that count (offsets + n_experts, say), NULL for all `rows`; one

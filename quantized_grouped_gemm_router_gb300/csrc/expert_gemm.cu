@@ -640,14 +640,13 @@ cudaError_t launch(const ProductParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_product(const ProductParams& p, cudaStream_t s) {
-  if (product_is_small(p)) return launch_product_small(p, s);
+int product_form(const ProductParams& p, int sms, int pairs) {
+  if (product_is_small(p, sms)) return MOE_PRODUCT_FEW_ROWS;
   // Which width: a block of 128 inputs takes 0.25 us in an item of 128 columns, 0.46 in one of 256 and 0.44 in a pair's
   // 256 x 256, times the rounds of items over the SMs; but L2 hands out 21.6 TB/s at most, 32, 48 and 64 KB to an item
   // and block (0.0015, 0.0022, 0.0030 us), and rows that begin off 128-byte lines take 1.6 times that. Times in 0.1 ns.
   // (8192 x 8192 x 8192: 483, 432 and 420 us; 3236 rows of 6896 x 4464: 134, 126, 104; 1195 rows of 8 experts of 2640 x
   // 3264: 24.5, 32.6 and none.) A pair wants rows for both its CTAs: with 128 rows to an expert it loses a fifth, with 512 5%.
-  const int sms = sm_count();
   const bool off = p.k % 128 || p.a.stride % 128;
   auto time = [&](int64_t items, int at_once, int block, int l2) {
     const int64_t a = (items + at_once - 1) / at_once * block, b = items * l2 * (off ? 16 : 10) / 10;
@@ -655,12 +654,21 @@ cudaError_t launch_product(const ProductParams& p, cudaStream_t s) {
   };
   const int64_t narrow = time(most_items(p, kTileM, 128), sms, 2500, 15);
   const int64_t wide = time(most_items(p, kTileM, 256), sms, off ? 5600 : 4600, 22);
-  if (p.rows >= kPairRows * (int64_t)p.n_experts && most_pairs() > 0) {
-    const int64_t pair = time(most_items(p, 2 * kTileM, 256), most_pairs(), p.n_experts == 1 ? 4400 : 4700, 30);
-    if (pair <= wide && pair <= narrow) return p.transposed ? launch<256, true, true>(p, s) : launch<256, false, true>(p, s);
+  if (p.rows >= kPairRows * (int64_t)p.n_experts && pairs > 0) {
+    const int64_t pair = time(most_items(p, 2 * kTileM, 256), pairs, p.n_experts == 1 ? 4400 : 4700, 30);
+    if (pair <= wide && pair <= narrow) return MOE_PRODUCT_PAIRS;
   }
-  if (wide < narrow) return p.transposed ? launch<256, true, false>(p, s) : launch<256, false, false>(p, s);
-  return p.transposed ? launch<128, true, false>(p, s) : launch<128, false, false>(p, s);
+  return wide < narrow ? MOE_PRODUCT_256 : MOE_PRODUCT_128;
+}
+
+cudaError_t launch_product(const ProductParams& p, cudaStream_t s) {
+  const int pairs = p.rows >= kPairRows * (int64_t)p.n_experts ? most_pairs() : 0;  // else never asked for
+  switch (product_form(p, sm_count(), pairs)) {
+    case MOE_PRODUCT_FEW_ROWS: return launch_product_small(p, s);
+    case MOE_PRODUCT_PAIRS: return p.transposed ? launch<256, true, true>(p, s) : launch<256, false, true>(p, s);
+    case MOE_PRODUCT_256: return p.transposed ? launch<256, true, false>(p, s) : launch<256, false, false>(p, s);
+    default: return p.transposed ? launch<128, true, false>(p, s) : launch<128, false, false>(p, s);
+  }
 }
 
 }  // namespace moe

@@ -178,10 +178,10 @@ SmallGrid small_grid(const ProductParams& p) {
 // 14.4 and 19.1, 1024 x 16384 13.0 and 32.5, a token's 8 of 256 experts of 1024 x 2048 7.2 and 7.7 (of 2048 x 512 5.4 and
 // 5.1, the closest call); but past that number, in waves of loads and latency, 16384 x 1024 6.7 and 5.9, 8 rows over
 // 8 experts of 4096 x 2048 14.9 and 12.3.
-bool product_is_small(const ProductParams& p) {
+bool product_is_small(const ProductParams& p, int sms) {
   if (p.transposed || p.rows > kRows) return false;
   const SmallGrid g = small_grid(p);
-  return g.columns * g.groups <= 4 * (int64_t)sm_count();
+  return g.columns * g.groups <= 4 * (int64_t)sms;
 }
 
 cudaError_t launch_product_small(const ProductParams& p, cudaStream_t s) {

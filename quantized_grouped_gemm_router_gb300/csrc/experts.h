@@ -90,7 +90,8 @@ cudaError_t launch_combine_grad(const CombineGradParams& p, cudaStream_t s);
 cudaError_t launch_swiglu(SwigluParams p, bool grad, cudaStream_t s);
 cudaError_t launch_quant_weights(const QuantWeightsParams& p, int n_experts, cudaStream_t s);
 cudaError_t launch_product(const ProductParams& p, cudaStream_t s);
-bool product_is_small(const ProductParams& p);  // the kernel for few rows takes the call
+int product_form(const ProductParams& p, int sms, int pairs);  // MOE_PRODUCT_*
+bool product_is_small(const ProductParams& p, int sms);  // the kernel for few rows takes the call
 cudaError_t launch_product_small(const ProductParams& p, cudaStream_t s);
 
 int sm_count();  // of the device that was current at the first call

@@ -202,6 +202,24 @@ int moe_gemm_e4m3(const moe_rows* a, int32_t rows, const moe_e4m3_weights* w, co
   return status_of(launch_product(p, stream));
 }
 
+int32_t moe_gemm_e4m3_form(int32_t rows, int32_t n_experts, int32_t n, int32_t k, int32_t transposed, int64_t stride, int32_t sms,
+                           int32_t pairs) {
+  if (rows < 1 || rows >= kExpMaxRows || !experts_ok(n_experts) || !cols_ok(n) || !cols_ok(k) || stride < 1 || sms < 1 || pairs < 0)
+    return -1;
+  ProductParams p = {};
+  p.a.stride = stride;
+  p.rows = rows;
+  p.n_experts = n_experts;
+  p.n = n;
+  p.k = k;
+  p.transposed = transposed != 0;
+  p.in = p.transposed ? n : k;
+  p.outc = p.transposed ? k : n;
+  p.in_blocks = (p.in + kScaleBlock - 1) / kScaleBlock;
+  p.out_blocks = (p.outc + kScaleBlock - 1) / kScaleBlock;
+  return product_form(p, sms, pairs);
+}
+
 static int swiglu_call(const moe_rows* gu, const moe_rows* dh, int32_t rows, int32_t inter, const int32_t* total,
                        const moe_rows* out, void* ws, size_t ws_bytes, moe_stream_t stream, bool grad) {
   int st = check_counts(rows);

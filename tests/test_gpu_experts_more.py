@@ -1,12 +1,15 @@
-"""The 8-bit expert calls on a GB300 where their arguments are unusual: gates far below zero, copied handles."""
+"""The 8-bit expert calls on a GB300 where their arguments are unusual: gates far below zero, copied handles, each form of the product's
+kernel."""
 import copy
+import ctypes
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from tests import expert_check as C  # noqa: E402
-from tests.test_gpu_experts import dev, make_product, m, rand, ws  # noqa: E402, F401
+from tests.product_forms import FORM_CASES  # noqa: E402
+from tests.test_gpu_experts import dev, guarded, make_product, m, rand, untouched, ws  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +92,24 @@ def test_copied_handles(m, ws):  # noqa: F811
     a.q, a.scale, w.q.data, w.scale.data = a2.q, a2.scale, w2.q, w2.scale
     del a2, w2
     assert torch.equal(m.gemm_e4m3(a, w, offsets, ws), want)
+
+
+@pytest.mark.parametrize("form,counts,out,cols,pad,transposed", FORM_CASES)
+def test_product_forms(m, ws, form, counts, out, cols, pad, transposed):  # noqa: F811
+    """Each form of the kernel, on rows on and off 128-byte lines (on a GPU of other SMs the sizes may take other forms)."""
+    n, k = (cols, out) if transposed else (out, cols)
+    a, w, offsets, (ref, size) = make_product(m, out + cols, counts, n, k, transposed)
+    rows = sum(counts)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    if sms == 152:
+        got = m.lib().moe_gemm_e4m3_form(rows, len(counts), n, k, int(transposed), ctypes.c_int64(cols + pad), sms, sms // 2)
+        assert got == form
+    if pad:
+        wide = torch.full((rows, cols + pad), 0x7F, dtype=torch.uint8, device="cuda")
+        wide[:, :cols] = a.q
+        a = m.E4m3Rows(wide[:, :cols], a.scale)
+    whole, got = guarded(rows, out, 0x7FC0)
+    for _ in range(2):
+        m.gemm_e4m3(a, w, offsets, ws, transposed=transposed, out=got)
+    C.check_product(got, ref, size, C.blocks(cols))
+    assert untouched(whole, rows, out, 0x7FC0)
