@@ -1,5 +1,5 @@
 """The 8-bit expert calls on a GB300 where their arguments are unusual: gates far below zero, copied handles, each form of the product's
-kernel."""
+kernel, weights of more than 2^31 codes."""
 import copy
 import ctypes
 
@@ -113,3 +113,21 @@ def test_product_forms(m, ws, form, counts, out, cols, pad, transposed):  # noqa
         m.gemm_e4m3(a, w, offsets, ws, transposed=transposed, out=got)
     C.check_product(got, ref, size, C.blocks(cols))
     assert untouched(whole, rows, out, 0x7FC0)
+
+
+def test_more_weights_than_31_bits(m, ws):  # noqa: F811
+    """The last of 33 experts of 8192 x 8192 lies behind 2^31 codes (and 2^32 bytes of bf16): the same bits as alone."""
+    E, n = 33, 8192
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w16 = torch.zeros(E, n, n, dtype=torch.int16, device="cuda")
+    w16[-1] = (torch.randn(n, n, generator=g, device="cuda") / 90).to(torch.bfloat16).view(torch.int16)
+    w = m.E4m3Weights.quantise(w16)
+    one = m.E4m3Weights.quantise(w16[-1:])
+    assert w.q.numel() > 2 ** 31 and torch.equal(w.q[-1:], one.q) and torch.equal(w.scale[-1:], one.scale) and one.q.any()
+    assert not w.q[:-1].any()
+    for rows in (1, 300):
+        a = m.dispatch(torch.randn(rows, n, generator=g, device="cuda").to(torch.bfloat16).view(torch.int16), None, ws, e4m3=True)
+        offsets = torch.tensor([0] * E + [rows], dtype=torch.int32, device="cuda")
+        for transposed in (False, True):
+            want = m.gemm_e4m3(a, one, None, ws, transposed=transposed)
+            assert torch.equal(m.gemm_e4m3(a, w, offsets, ws, transposed=transposed), want) and want.any()
