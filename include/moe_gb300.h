@@ -530,9 +530,9 @@ MOE_API int moe_attn_decode(const moe_kv_cache* cache, moe_heads_view q, const i
  *   - Sums are fp32. Outputs are rounded once, to bf16 or, from the fp32 values, to e4m3.
  *   - Rows that no assignment names, and rows from offsets[n_experts] (or `total`) on, are left as
  *     they were.
- *   - Supported: 1 <= n_experts <= 1024, 1 <= top_k <= 16, columns (d, n, k, inter) multiples of 16,
- *     16 to 65536; fewer than 2^26 rows, tokens and assignments (MOE_ERR_UNSUPPORTED_SHAPE). No rows
- *     are no work.
+ *   - Supported: 1 <= n_experts <= 1024, 1 <= top_k <= 16, columns multiples of 16: d, n and k from 16
+ *     to 65536, inter, of which a row of gate and up has two, to 32768; fewer than 2^26 rows, tokens and
+ *     assignments (MOE_ERR_UNSUPPORTED_SHAPE). No rows are no work.
  *   - int32 and float arrays need 4-byte alignment, rows 16 bytes, `ws` 128. Outputs do not overlap
  *     inputs.
  *   - Ids, offsets, places and totals are device data. A kernel never follows a bad one out of the
@@ -637,7 +637,8 @@ MOE_API int32_t moe_gemm_e4m3_form(int32_t rows, int32_t n_experts, int32_t n, i
                                    int32_t sms, int32_t pairs);
 
 /*
- * h = silu(g) * u for rows gu = g | u of 2 * inter columns (bf16): h of inter columns, bf16 or e4m3.
+ * h = silu(g) * u for rows gu = g | u of 2 * inter columns (bf16, inter up to 32768): h of inter columns,
+ * bf16 or e4m3.
  * total: device int32, the number of rows that count (offsets + n_experts, say), NULL for all `rows`; one
  * outside 0 .. rows counts as the nearer end (MOE_ERR_BAD_INDEX).
  */

@@ -4,7 +4,8 @@
 // out[p, c] = sum_b s_a[p, b] s_w[e, c / 128, b] (sum of the 128 code products of block b). The tensor cores
 // sum a block's codes into a fresh accumulator in tensor memory; 8 warps then read it, multiply by the two
 // scales (one factor per row and warp: a row's scale times the block's) and add to fp32 sums in registers,
-// while the next block goes into another accumulator. So scales of any fp32 value cost no accuracy.
+// while the next block goes into another accumulator. The factor is formed first, in fp32: it has to stay below 2^128 and
+// keeps 24 bits from 2^-126 on.
 //
 // A CTA makes 128 rows of one expert x BN columns, rows as the MMA's M: a thread owns a row, so that its
 // factor is one register. Persistent CTAs, one per SM, walk the items (expert, row tile, column tile):
@@ -20,9 +21,10 @@
 // cycles). Timestamps: the MMAs of a block follow each other without a gap, but last 950 cycles beside copies and sums and
 // 740 beside the copies alone. Shared memory carries 64 KB a block (32 in, 32 to the MMAs), 512 cycles of it, and 96 KB
 // where CTAs work alone; tensor memory hands 131 KB a block to the sums beside the MMAs' own traffic. The sums
-// themselves are 32768 FMAs, 256 cycles of the FMA pipes. 8191 x 8192 x 8192 takes 403 us (2730 TFLOP/s; 430 under the power
-// limit) in pairs and 447 with single CTAs. Few rows to an expert: the weights' bytes; 32768 rows over 256 experts of
-// 1024 x 2048 take 113 us, 5.9 TB/s.
+// themselves are 32768 FMAs, 256 cycles of the FMA pipes. 8191 x 8192 x 8192 takes 394 us in pairs where calls are spaced out
+// (2790 TFLOP/s) and, under the power limit, 414 to 440 back to back (2660 to 2500); single CTAs take 447. Few rows
+// to an expert: the weights' bytes; 32768 rows over 256 experts of 1024 x 2048 take 114 us, 5.9 TB/s. (The single CTAs'
+// kernel of 256 columns, which does that, spills 20 bytes a thread; the others spill nothing.)
 // What it took to get there from 809 us: a row's scales read by one warp ahead instead of by all who use them
 // (a line per lane filled L1's tag stage), plain FMAs (pairs cost a move for each register out of tensor memory),
 // loads of scales that no loop waits for, output rows stored 64 bytes at a time, both of the issuing warp's

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
 }
 
 // ------------------------------------------------------------------------------------ combine
-// The rows of a token, scattered, summed in the order of its list: 4096 tokens take 26.5 us (5.7 TB/s; 28.2 with each token's
+// The rows of a token, scattered, summed in the order of its list: 4096 tokens take 25.6 us (5.9 TB/s; 28.2 with each token's
 // places loaded only when its turn came).
 constexpr int kCombinePiece = 256;  // 8 columns per lane: one 16-byte load of each row
 constexpr int kTogether = 8;        // rows whose loads are in flight together
@@ -248,7 +248,7 @@ __device__ __forceinline__ moe_rows from_col(moe_rows r, int first) {
   return r;
 }
 
-// 32768 rows of 512 take 16 us in e4m3 (5.3 TB/s, 3 us of them a launch and its tail), 18.3 with a warp to a piece and no loads
+// 32768 rows of 512 take 15 us in e4m3 (5.6 TB/s, 2 us of them a launch and its tail), 18.3 with a warp to a piece and no loads
 // ahead. More CTAs to an SM cost registers and gain nothing.
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const __grid_constant__ SwigluParams p, int warps) {
@@ -319,7 +319,7 @@ __device__ __forceinline__ void swiglu_grad16(const uint4 (&gv)[2], const uint4 
 
 // WHOLE: inter is a multiple of 128, so that the blocks of dg and of du begin at the same columns and a
 // warp makes both from one reading. Otherwise the blocks of du straddle the two halves: the pieces run
-// over the 2 inter output columns, and what du needs of g and dh is read again (out of L2). 15893 rows of 512: 13.9 us.
+// over the 2 inter output columns, and what du needs of g and dh is read again (out of L2). 15893 rows of 512: 13.1 us.
 template <bool E4M3, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(const __grid_constant__ SwigluParams p, int warps) {
   pdl_wait();

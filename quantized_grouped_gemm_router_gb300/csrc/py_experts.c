@@ -1,7 +1,8 @@
 /* CPython side of the 8-bit expert calls: checks the tensors of a call, makes the outputs that are not given, and calls
  * the library. In C because a call on a few rows is bound by its host time: the same checks in Python with ctypes took
- * 8.6 us for moe_combine, here 4.1. Tensors are read through their Python attributes, so that nothing here depends on
- * torch's own headers or version. */
+ * 8.6 us for moe_combine, here 4.1. Tensors are read through their Python attributes, so that torch's own headers are not
+ * needed. Two names are private to torch: _C._cuda_getDevice and _C._cuda_getCurrentRawStream, which give the current
+ * device and its stream without making objects. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
